@@ -6,12 +6,15 @@ Usage: ``python -m gemv_tq2_g128_amd.build`` or ``build()`` from Python.
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(os.path.dirname(PKG_DIR), "include")
 LIB_NAME = "libtq2.so"
-SOURCES = ["tq2_api.hip", "tq2_reformat.hip", "tq2_gemv.hip", "tq2_gemm.hip"]
+SOURCES = ["tq2_api.hip", "tq2_reformat.hip", "tq2_gemv.hip", "tq2_gemm.hip", "tq2_q4.hip",
+           "tq2_layer_api.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
@@ -44,11 +47,8 @@ def build(verbose: bool = False) -> str:
     return _compile(SOURCES, LIB_NAME, verbose)
 
 
-def _compile(sources, lib_name, verbose):
-    out = os.path.join(PKG_DIR, lib_name)
-    tmp = out + ".tmp%d" % os.getpid()
-    cmd = [hipcc_path(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC,
-           *[os.path.join(CSRC, s) for s in sources], "-o", tmp]
+def _run(cmd, verbose):
+    """Run one hipcc command; its output, or RuntimeError."""
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
@@ -56,11 +56,28 @@ def _compile(sources, lib_name, verbose):
     noise = "is not a recognized feature for this target"
     msg = "\n".join(l for l in res.stdout.splitlines() if noise not in l)
     if res.returncode != 0:
-        if os.path.exists(tmp):
-            os.remove(tmp)
         raise RuntimeError("hipcc failed (%d):\n%s" % (res.returncode, msg))
     if verbose and msg.strip():
         print(msg)
+
+
+def _compile(sources, lib_name, verbose):
+    """One object per source, in parallel, then the link."""
+    out = os.path.join(PKG_DIR, lib_name)
+    tmp = out + ".tmp%d" % os.getpid()
+    flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory(prefix="tq2_build_") as work:
+        objs = [os.path.join(work, s + ".o") for s in sources]
+        cmds = [[hipcc_path(), *flags, "-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, s),
+                 "-o", o] for s, o in zip(sources, objs)]
+        with ThreadPoolExecutor(max_workers=min(len(cmds), 8)) as pool:
+            list(pool.map(lambda c: _run(c, verbose), cmds))
+        try:
+            _run([hipcc_path(), *HIPCC_FLAGS, *objs, "-o", tmp], verbose)
+        except RuntimeError:
+            if os.path.exists(tmp):
+                os.remove(tmp)
+            raise
     os.replace(tmp, out)
     return out
 

@@ -5,16 +5,18 @@
 // including k % 128 != 0 and size mismatches, is returned to the caller and
 // nothing panics.  Unlike the pages there is no CPU fallback behind it.
 #include <atomic>
-#include <cstring>
 
 #include "../../include/tq2.h"
+#include "tq2_host.h"
 #include "tq2_internal.h"
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-// 0 = unknown, 1 = gfx950, 2 = other architecture.
-std::atomic<int> g_device_kind[kMaxDevices];
+using tq2::aligned;
+using tq2::check_device;
+using tq2::kMaxDevices;
+using tq2::launch_status;
+using tq2::overlaps;
 
 // Device memory of tq2_gemm_noalloc: one fixed array per GPU, held from the
 // library's load until the process ends, so that call allocates nothing.
@@ -34,29 +36,6 @@ void* device_scratch(int dev) {
   return p;
 }
 
-int check_device() {
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return TQ2_ERR_DEVICE;
-  if (dev < kMaxDevices) {
-    const int kind = g_device_kind[dev].load(std::memory_order_relaxed);
-    if (kind == 1) return TQ2_OK;
-    if (kind == 2) return TQ2_ERR_DEVICE;
-  }
-  hipDeviceProp_t prop;
-  if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return TQ2_ERR_DEVICE;
-  const bool ok = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-  if (dev < kMaxDevices) g_device_kind[dev].store(ok ? 1 : 2, std::memory_order_relaxed);
-  return ok ? TQ2_OK : TQ2_ERR_DEVICE;
-}
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  if (!a || !b || na == 0 || nb == 0) return false;
-  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-  return pa < pb + nb && pb < pa + na;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 constexpr int64_t kMaxDim = int64_t(1) << 30;   // keeps every 32-bit index in range
 
 // Shape check shared by every entry point; m may be 0 (no-op) where allowed.
@@ -66,8 +45,6 @@ int check_shape(int64_t m, int64_t n, int64_t k) {
   if (m > kMaxDim || n > kMaxDim || k > kMaxDim) return TQ2_ERR_INVALID;
   return TQ2_OK;
 }
-
-int launch_status(hipError_t e) { return e == hipSuccess ? TQ2_OK : TQ2_ERR_LAUNCH; }
 
 // Host-side checks common to the matmul entry points once the shape is valid
 // and non-empty: pointers, alignment and aliasing.
