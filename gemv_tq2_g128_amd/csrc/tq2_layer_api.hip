@@ -1,9 +1,13 @@
-// C ABI of the operators around the matmuls (tq2_q4.h): argument checks, device
-// check, launch.  Same error policy as tq2_api.hip: every failure is a status.
+// C ABI of the operators around the matmuls (tq2_q4.h, tq2_attn.h): argument
+// checks, device check, launch.  Same error policy as tq2_api.hip: every failure is a status.
+#include "../../include/tq2_attn.h"
 #include "../../include/tq2_q4.h"
+#include "tq2_attn_internal.h"
 #include "tq2_host.h"
 #include "tq2_internal.h"
 #include "tq2_q4_internal.h"
+
+#include <utility>
 
 namespace {
 
@@ -13,6 +17,98 @@ using tq2::launch_status;
 using tq2::overlaps;
 
 constexpr int64_t kMaxDim = int64_t(1) << 30;
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+
+int type_bytes(int64_t t) { return t == TQ2_TYPE_F32 ? 4 : (t == TQ2_TYPE_E4M3 ? 1 : 2); }
+
+bool size_ok(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
+
+// Whether the strides keep rows 16-byte aligned; *bad is set if one is out of range.
+bool strides_ok(int64_t bytes, int64_t s0, int64_t s1, int64_t s2, bool* bad) {
+  for (int64_t s : {s0, s1, s2})
+    if (!size_ok(s, 0, kMaxStride)) *bad = true;
+  return !((s0 * bytes) & 15) && !((s1 * bytes) & 15) && !((s2 * bytes) & 15);
+}
+
+// Bytes from the first to the last element of a strided [n0, n1, n2, dim] array.
+size_t extent(int64_t bytes, int64_t dim, int64_t n0, int64_t s0, int64_t n1, int64_t s1,
+              int64_t n2 = 1, int64_t s2 = 0) {
+  typedef unsigned __int128 wide;
+  const wide most = wide(1) << 62;               // past any array, and no overflow when added to an address
+  const wide all = (wide(n0 - 1) * s0 + wide(n1 - 1) * s1 + wide(n2 - 1) * s2 + dim) * bytes;
+  return size_t(all < most ? all : most);
+}
+
+// Sizes and types of the cache; nothing is dereferenced.
+int check_cache_sizes(const tq2_paged_cache& c) {
+  if (!size_ok(c.batch, 0, TQ2_ATTN_MAX_BATCH) || !size_ok(c.tokens, 0, kMaxDim) ||
+      !size_ok(c.pages, 0, kMaxDim) || !size_ok(c.table_cols, 0, kMaxDim) ||
+      !size_ok(c.table_stride, 0, kMaxDim) || !size_ok(c.kv_heads, 1, TQ2_ATTN_MAX_HEADS) ||
+      !size_ok(c.q_heads, 1, TQ2_ATTN_MAX_HEADS))
+    return TQ2_ERR_INVALID;
+  if (c.head_dim != 64 && c.head_dim != 96 && c.head_dim != 128 && c.head_dim != 192 &&
+      c.head_dim != 256)
+    return TQ2_ERR_INVALID;
+  const bool wide = (c.act_type == TQ2_TYPE_F32 && c.cache_type == TQ2_TYPE_F16) ||
+                    (c.act_type == TQ2_TYPE_F16 && c.cache_type == TQ2_TYPE_F16) ||
+                    (c.act_type == TQ2_TYPE_BF16 && c.cache_type == TQ2_TYPE_BF16);
+  const bool narrow = c.cache_type == TQ2_TYPE_E4M3 && size_ok(c.act_type, TQ2_TYPE_F32, TQ2_TYPE_BF16);
+  if (!wide && !narrow) return TQ2_ERR_INVALID;
+  if (!c.cu_q && c.tokens != c.batch) return TQ2_ERR_INVALID;
+  if (!size_ok(c.page, 16, int64_t(1) << 20) || (c.page & (c.page - 1))) return TQ2_ERR_SHAPE;
+  if (c.q_heads % c.kv_heads) return TQ2_ERR_SHAPE;
+  return TQ2_OK;
+}
+
+// Pointers and strides of the cache.
+int check_cache_arrays(const tq2_paged_cache& c) {
+  if (!c.table || !c.kv_len || (c.pages > 0 && (!c.k || !c.v))) return TQ2_ERR_INVALID;
+  const bool narrow = c.cache_type == TQ2_TYPE_E4M3;
+  if (narrow != (c.k_scale != nullptr) || narrow != (c.v_scale != nullptr)) return TQ2_ERR_INVALID;
+  const int64_t cb = type_bytes(c.cache_type);
+  bool bad = false;
+  const bool even = strides_ok(cb, c.k_page_stride, c.k_head_stride, c.k_token_stride, &bad) &
+                    strides_ok(cb, c.v_page_stride, c.v_head_stride, c.v_token_stride, &bad);
+  if (bad) return TQ2_ERR_INVALID;
+  if (!even || !aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.table, 4) ||
+      !aligned(c.kv_len, 4) || !aligned(c.cu_q, 4) || !aligned(c.k_scale, 4) || !aligned(c.v_scale, 4))
+    return TQ2_ERR_ALIGN;
+  if (c.k && c.k == c.v) return TQ2_ERR_ALIAS;
+  return TQ2_OK;
+}
+
+size_t k_extent(const tq2_paged_cache& c) {
+  return c.pages == 0 ? 0 : extent(type_bytes(c.cache_type), c.head_dim, c.pages, c.k_page_stride, c.kv_heads,
+                                   c.k_head_stride, c.page, c.k_token_stride);
+}
+
+size_t v_extent(const tq2_paged_cache& c) {
+  return c.pages == 0 ? 0 : extent(type_bytes(c.cache_type), c.head_dim, c.pages, c.v_page_stride, c.kv_heads,
+                                   c.v_head_stride, c.page, c.v_token_stride);
+}
+
+tq2::Pages pages_of(const tq2_paged_cache& c) {
+  tq2::Pages p;
+  p.table = c.table;
+  p.kv_len = c.kv_len;
+  p.cu_q = c.cu_q;
+  p.batch = int32_t(c.batch);
+  p.tokens = int32_t(c.tokens);
+  p.pages = int32_t(c.pages);
+  p.cols = int32_t(c.table_cols);
+  p.page_shift = __builtin_ctzll(uint64_t(c.page));
+  p.kv_heads = int32_t(c.kv_heads);
+  p.q_heads = int32_t(c.q_heads);
+  p.head_dim = int32_t(c.head_dim);
+  p.table_stride = c.table_stride;
+  p.k_page = c.k_page_stride;
+  p.k_head = c.k_head_stride;
+  p.k_token = c.k_token_stride;
+  p.v_page = c.v_page_stride;
+  p.v_head = c.v_head_stride;
+  p.v_token = c.v_token_stride;
+  return p;
+}
 
 }  // namespace
 
@@ -40,6 +136,84 @@ int tq2_q4_gemv(const void* codes, const void* scales, const float* x, const flo
   const tq2::Q4Args a = {static_cast<const uint8_t*>(codes), static_cast<const uint16_t*>(scales),
                          x, residual, out, m, n, k};
   return launch_status(tq2::launch_q4_gemv(a, group, static_cast<hipStream_t>(stream)));
+}
+
+int tq2_kv_append(const tq2_kv_append_args* args, void* stream) {
+  if (!args) return TQ2_ERR_INVALID;
+  const tq2_kv_append_args& a = *args;
+  const tq2_paged_cache& c = a.cache;
+  int st = check_cache_sizes(c);
+  if (st != TQ2_OK) return st;
+  if (!size_ok(a.rot, 0, c.head_dim) || !size_ok(a.axes, 1, 3)) return TQ2_ERR_INVALID;
+  if (a.rot % 8) return TQ2_ERR_SHAPE;
+  if (a.axes > 1 && !a.positions) return TQ2_ERR_INVALID;
+  int64_t sum = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (!size_ok(a.section[i], 0, i < a.axes ? a.rot / 2 : 0)) return TQ2_ERR_INVALID;
+    sum += a.section[i];
+  }
+  if (sum != a.rot / 2) return TQ2_ERR_INVALID;
+  if (!(a.eps >= 0.0)) return TQ2_ERR_INVALID;
+  if (c.tokens == 0) return TQ2_OK;
+  st = check_cache_arrays(c);
+  if (st != TQ2_OK) return st;
+  if (!a.k || !a.v || (a.q != nullptr) != (a.q_out != nullptr) || (a.rot > 0 && !a.freqs))
+    return TQ2_ERR_INVALID;
+  const int64_t ab = type_bytes(c.act_type), d = c.head_dim;
+  bool bad = false;
+  const bool even = strides_ok(ab, a.k_token_stride, a.k_head_stride, 0, &bad) &
+                    strides_ok(ab, a.v_token_stride, a.v_head_stride, 0, &bad) &
+                    (!a.q || (strides_ok(ab, a.q_token_stride, a.q_head_stride, 0, &bad) &
+                              strides_ok(ab, a.q_out_token_stride, a.q_out_head_stride, 0, &bad)));
+  if (bad) return TQ2_ERR_INVALID;
+  if (!even || !aligned(a.q, 16) || !aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.q_out, 16) ||
+      !aligned(a.q_norm, 16) || !aligned(a.k_norm, 16) || !aligned(a.freqs, 8) || !aligned(a.positions, 4))
+    return TQ2_ERR_ALIGN;
+  const size_t kb = extent(ab, d, c.tokens, a.k_token_stride, c.kv_heads, a.k_head_stride);
+  const size_t vb = extent(ab, d, c.tokens, a.v_token_stride, c.kv_heads, a.v_head_stride);
+  const size_t qb = a.q ? extent(ab, d, c.tokens, a.q_token_stride, c.q_heads, a.q_head_stride) : 0;
+  const size_t ob = a.q ? extent(ab, d, c.tokens, a.q_out_token_stride, c.q_heads, a.q_out_head_stride) : 0;
+  for (const auto& cache : {std::make_pair(c.k, k_extent(c)), std::make_pair(c.v, v_extent(c))})
+    if (overlaps(cache.first, cache.second, a.q, qb) || overlaps(cache.first, cache.second, a.k, kb) ||
+        overlaps(cache.first, cache.second, a.v, vb) || overlaps(cache.first, cache.second, a.q_out, ob))
+      return TQ2_ERR_ALIAS;
+  // In place, q_out's extent is q's own, which k and v may share as columns of one array.
+  const bool in_place = a.q_out == a.q && a.q_out_token_stride == a.q_token_stride &&
+                        a.q_out_head_stride == a.q_head_stride;
+  if (a.q && !in_place &&
+      (overlaps(a.q_out, ob, a.q, qb) || overlaps(a.q_out, ob, a.k, kb) || overlaps(a.q_out, ob, a.v, vb)))
+    return TQ2_ERR_ALIAS;
+  st = check_device();
+  if (st != TQ2_OK) return st;
+  tq2::AppendArgs g;
+  g.pages = pages_of(c);
+  g.q = a.q;
+  g.k = a.k;
+  g.v = a.v;
+  g.q_out = a.q_out;
+  g.k_cache = c.k;
+  g.v_cache = c.v;
+  g.q_token = a.q_token_stride;
+  g.q_head = a.q_head_stride;
+  g.k_token = a.k_token_stride;
+  g.k_head = a.k_head_stride;
+  g.v_token = a.v_token_stride;
+  g.v_head = a.v_head_stride;
+  g.o_token = a.q_out_token_stride;
+  g.o_head = a.q_out_head_stride;
+  g.freqs = a.freqs;
+  g.positions = a.positions;
+  g.q_norm = a.q_norm;
+  g.k_norm = a.k_norm;
+  g.k_scale = c.k_scale;
+  g.v_scale = c.v_scale;
+  g.eps = float(a.eps);
+  g.half = int32_t(a.rot / 2);
+  g.cut[0] = int32_t(a.section[0]);
+  g.cut[1] = int32_t(a.section[0] + a.section[1]);
+  g.interleaved = a.interleaved != 0;
+  return launch_status(
+      tq2::launch_kv_append(g, int(c.act_type), int(c.cache_type), static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
