@@ -17,21 +17,35 @@ import torch
 
 from .tq2 import _check, _launch, lib
 
-EXPORTED_SYMBOLS = ("tq2_kv_append",)
+EXPORTED_SYMBOLS = ("tq2_kv_append", "tq2_paged_attention", "tq2_paged_attention_workspace_bytes")
 HEAD_DIMS = (64, 96, 128, 192, 256)
 
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3}
-# tq2_paged_cache and tq2_kv_append_args: every field is 8 bytes wide.
+# tq2_paged_cache and what follows it in the two argument structs: every field is 8 bytes wide.
 _CACHE = struct.Struct("=7Q17q")
 _APPEND = struct.Struct("=4Q8q2Q6q2Qd")
+_ATTENTION = struct.Struct("=2Q7qdQq")
 
 lib.tq2_kv_append.argtypes = [ctypes.c_char_p, ctypes.c_void_p]
 lib.tq2_kv_append.restype = ctypes.c_int
+lib.tq2_paged_attention.argtypes = [ctypes.c_char_p, ctypes.c_void_p]
+lib.tq2_paged_attention.restype = ctypes.c_int
+lib.tq2_paged_attention_workspace_bytes.argtypes = [ctypes.c_char_p]
+lib.tq2_paged_attention_workspace_bytes.restype = ctypes.c_size_t
 
 
 def kv_append_ptr(args: bytes, stream: int = 0) -> int:
     """args: the bytes of a tq2_kv_append_args."""
     return lib.tq2_kv_append(args, stream or None)
+
+
+def paged_attention_ptr(args: bytes, stream: int = 0) -> int:
+    """args: the bytes of a tq2_paged_attention_args."""
+    return lib.tq2_paged_attention(args, stream or None)
+
+
+def paged_attention_workspace_bytes_ptr(args: bytes) -> int:
+    return lib.tq2_paged_attention_workspace_bytes(args)
 
 
 def _on(dev: int, t, what: str):
@@ -143,3 +157,38 @@ def kv_append(k, v, k_cache, v_cache, kv_len, table, q=None, q_out=None, cu_q=No
         _plain(dev, q_norm, torch.float32, dim, "q_norm"), _plain(dev, k_norm, torch.float32, dim, "k_norm"), eps)
     _check(_launch(k.device, kv_append_ptr, args), "kv_append")
     return q_out
+
+
+def paged_attention(q, k_cache, v_cache, kv_len, table, cu_q=None, max_q=None, max_kv=None, window=0, scale=None,
+                    k_scale=None, v_scale=None, out=None):
+    """softmax(scale * q K^T) V of q [tokens, q_heads, head_dim] over the cache, each token seeing its sequence up to
+    itself (the last ``window`` tokens of that, if given); rows that see nothing give zeros.
+
+    ``max_q`` and ``max_kv``, the most new tokens and the most tokens of a sequence, shape the launch (by default all
+    of q and all that the table holds); larger ones are still done.  ``scale`` is 1 / sqrt(head_dim) by default.
+    ``out`` may be q itself."""
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, q_heads, head_dim]")
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("q must be a device tensor")
+    tokens, q_heads, dim = q.shape
+    act = q.dtype
+    if k_cache.dim() == 4 and k_cache.shape[3] != dim:
+        raise ValueError("q must be [tokens, q_heads, %d] for this cache" % k_cache.shape[3])
+    if out is None:
+        out = torch.empty(q.shape, dtype=act, device=q.device)
+    q_st, o_st = _rows(dev, q, act, q.shape, "q"), _rows(dev, out, act, q.shape, "out")
+    cache = _cache(dev, act, tokens, q_heads, k_cache, v_cache, kv_len, table, cu_q, k_scale, v_scale)
+    if max_q is None:
+        max_q = 1 if cu_q is None else tokens
+    if max_kv is None:
+        max_kv = min(table.shape[1] * k_cache.shape[2], 2 ** 31 - 1)
+    if scale is None:
+        scale = dim ** -0.5
+    sizes = (q.data_ptr(), out.data_ptr(), *q_st, *o_st, max_q, max_kv, window, scale)
+    need = paged_attention_workspace_bytes_ptr(cache + _ATTENTION.pack(*sizes, 0, 0))
+    workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    args = cache + _ATTENTION.pack(*sizes, workspace.data_ptr() if need else 0, need)
+    _check(_launch(q.device, paged_attention_ptr, args), "paged_attention")
+    return out

@@ -1,0 +1,721 @@
+// Attention of new tokens over a paged cache, streaming form.
+//     o = sum_j p_j v_j / sum_j p_j,   p_j = 2^(c q.k_j - m),   c = scale log2 e
+// with the running maximum m of a row: one pass over the keys, f32 sums.
+//
+// Bound.  A decode step reads every visible key and value once and does a
+// few operations with each: HBM.  So keys and values go straight from memory
+// to the operand registers of the matrix cores, with no LDS in between and no
+// barrier in the loop; each wave walks over its own tiles of 32 keys with its
+// own m, sum and output, and the waves of a block meet once at the end.
+//
+// Matrix form (v_mfma_f32_16x16x32, 16 rows: the new tokens times the query
+// heads that share a key head).
+//   S^T = K Q^T: a lane reads 16 bytes of one key, and holds four keys' scores
+//     of one row for each 16 keys.
+//   O^T = V^T P^T: the eight probabilities of a lane (two tiles of 16 keys) are
+//     its operand words as they are, with the keys of a matrix step in the order
+//     4 g + j, 16 + 4 g + j of lane group g.  For V^T a lane reads the same 8
+//     components of those eight keys (rows of 256 bytes by 16 lanes), and byte
+//     permutes turn its 8 x 8 block: word i of the eight keys is the operand of
+//     matrix step i, whose row c is component 8 c + i.
+// Softmax statistics are per lane (a row) and its 16-lane group's keys; the
+// maximum is joined across the four groups each tile, the sum once at the end.
+//
+// 32-bit q is split into two binary16 parts under a power of two per row, and
+// so are the probabilities (scaled by 2^14): two matrix steps each.  16-bit q enters
+// as it is.  e4m3 codes become binary16 (keys: q's type) exactly.
+//
+// Masks.  A 16-key run lies in one page; its buffer resource ends at the last
+// key that counts, so that everything past it (or in a page that is not there)
+// loads as zero.  Tiles that every row sees whole skip the comparisons.  Where
+// rows differ in what they see, a value that is not finite is kept from rows
+// that do not see it (zero times infinity would reach them).
+#include "tq2_attn_internal.h"
+#include "tq2_device.h"
+#include "tq2_types.h"
+
+namespace tq2 {
+namespace {
+
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr float kNone = -__builtin_inff();
+
+__device__ __forceinline__ f32x4_t mfma(F16, u32x4_t a, u32x4_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a),
+                                                __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4_t mfma(BF16, u32x4_t a, u32x4_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                 __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t pack2(F16, float a, float b) {
+  typedef _Float16 v2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, v2{_Float16(a), _Float16(b)});
+}
+__device__ __forceinline__ uint32_t pack2(BF16, float a, float b) {
+  typedef __bf16 v2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, v2{__bf16(a), __bf16(b)});
+}
+// What rounding a and b to the type leaves, in the type.
+__device__ __forceinline__ uint32_t pack2_rest(F16, float a, float b) {
+  return pack2(F16(), a - float(_Float16(a)), b - float(_Float16(b)));
+}
+__device__ __forceinline__ uint32_t pack2_rest(BF16, float a, float b) {
+  return pack2(BF16(), a - float(__bf16(a)), b - float(__bf16(b)));
+}
+
+// Two e4m3 codes (half `hi` of the word) as two 16-bit values, exactly.
+template <bool hi>
+__device__ __forceinline__ uint32_t widen2(F16, uint32_t w) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, hi));
+}
+template <bool hi>
+__device__ __forceinline__ uint32_t widen2(BF16, uint32_t w) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, hi));
+}
+
+__device__ __forceinline__ float word(uint32_t w) { return __builtin_bit_cast(float, w); }
+__device__ __forceinline__ uint32_t word(float v) { return __builtin_bit_cast(uint32_t, v); }
+
+// v of the lane's place in the lower and upper half of the wave, and in the
+// even and odd 16-lane groups.  (A bit cast takes no vector element itself: the
+// compiler would read element 0.)
+__device__ __forceinline__ float2 halves32(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(word(v), word(v), false, false);
+  const uint32_t x = a[0], y = a[1];
+  return float2{word(x), word(y)};
+}
+__device__ __forceinline__ float2 halves16(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(word(v), word(v), false, false);
+  const uint32_t x = a[0], y = a[1];
+  return float2{word(x), word(y)};
+}
+
+// Maximum and sum over the lanes 16, 32 and 48 on (a row's four lane groups).
+__device__ __forceinline__ float over_groups_max(float v) {
+  float2 a = halves32(v);
+  a = halves16(fmaxf(a.x, a.y));
+  return fmaxf(a.x, a.y);
+}
+__device__ __forceinline__ float over_groups_sum(float v) {
+  float2 a = halves32(v);
+  a = halves16(a.x + a.y);
+  return a.x + a.y;
+}
+
+__device__ __forceinline__ float row16_top(float v) {
+  v = fmaxf(v, dpp_move<0xB1, 0xF>(v));
+  v = fmaxf(v, dpp_move<0x4E, 0xF>(v));
+  v = fmaxf(v, dpp_move<0x141, 0xF>(v));
+  return fmaxf(v, dpp_move<0x140, 0xF>(v));
+}
+
+// Types of the two products.
+template <class Act, class Cache>
+struct Kinds {
+  typedef F16 QK;
+  typedef F16 PV;
+};
+template <class Cache>
+struct Kinds<BF16, Cache> {
+  typedef BF16 QK;
+  typedef F16 PV;
+};
+template <>
+struct Kinds<BF16, BF16> {
+  typedef BF16 QK;
+  typedef BF16 PV;
+};
+
+// Components per lane of the value chunks that make up a head: 128, 64 or 32 wide.
+template <int D>
+struct Chunks {
+  static constexpr int count = D == 96 || D == 192 || D == 256 ? 2 : 1;
+  __host__ __device__ static constexpr int per_lane(int c) {
+    return D == 64 ? 4 : D == 96 ? (c == 0 ? 4 : 2) : D == 192 ? (c == 0 ? 8 : 4) : 8;
+  }
+  __host__ __device__ static constexpr int start(int c) { return c == 0 ? 0 : (D == 96 ? 64 : 128); }
+  __host__ __device__ static constexpr int tile(int c) { return c == 0 ? 0 : per_lane(0); }
+};
+
+// First component of the 8 that lane group g feeds to step t of S^T = K Q^T.
+template <class Cache, int D>
+__device__ __forceinline__ constexpr int key_dim(int t, int g) {
+  if (__is_same(Cache, E4M3) && t < 2 * (D / 64)) return (t >> 1) * 64 + g * 16 + (t & 1) * 8;
+  return t * 32 + g * 8;
+}
+
+// A buffer resource that the compiler keeps in scalar registers.
+__device__ __forceinline__ rsrc_t uniform_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t at = reinterpret_cast<uint64_t>(base);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(at)), hi = __builtin_amdgcn_readfirstlane(uint32_t(at >> 32));
+  return make_rsrc(reinterpret_cast<const void*>(uint64_t(hi) << 32 | lo), __builtin_amdgcn_readfirstlane(bytes));
+}
+
+// A 16-key run: where its keys and values start, and how many count.
+struct Run {
+  rsrc_t k, v;
+  int count;
+};
+
+// Waves per SIMD that the register budget aims at.
+template <int D, int MT>
+constexpr int kMinWaves = D * MT <= 128 ? 2 : 1;
+
+template <class Act, class Cache, int D, int MT, int W>
+__global__ __launch_bounds__(64 * W, (kMinWaves<D, MT>)) void stream_kernel(AttnArgs a) {
+  typedef typename Kinds<Act, Cache>::QK QK;
+  typedef typename Kinds<Act, Cache>::PV PV;
+  typedef typename Act::elem act_t;
+  typedef typename Cache::elem cache_t;
+  constexpr bool kSplitQ = __is_same(Act, F32);
+  // Probabilities in two parts: where 16 bits of them would show in the output.
+  constexpr bool kSplitP = __is_same(Act, F32);
+  constexpr float kLift = __is_same(PV, F16) ? 14.f : 0.f;      // log2: keeps small probabilities normal
+  constexpr int kSize = int(sizeof(cache_t));
+  constexpr int kSteps = D / 32;
+  constexpr int kTiles = D / 16;
+  constexpr int kRegs = MT * kTiles * 4;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  u32x4_t* qf = reinterpret_cast<u32x4_t*>(smem);                // [part][MT][step][64]
+  float* join = reinterpret_cast<float*>(smem);                  // after the loop
+  __shared__ float back[MT * 16];                                // power of two of each row of q
+
+  const Pages& p = a.pages;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, g4 = lane >> 4;
+  const int group = p.q_heads / p.kv_heads;
+  const int head = blockIdx.y % p.kv_heads;
+  const int split = blockIdx.x;
+  const int b = blockIdx.z;
+  const Seq s = sequence(p, b);
+  const int64_t rows = int64_t(s.q_len) * group;
+  const Parts parts = parts_of(s, a.window, a.splits, a.split_keys);
+  if (split >= parts.count) return;
+
+  for (int64_t row0 = int64_t(blockIdx.y / p.kv_heads) * (MT * 16); row0 < rows;
+       row0 += int64_t(gridDim.y / p.kv_heads) * (MT * 16)) {
+    // Keys of this part that any of the rows sees.
+    const int last = int((row0 + MT * 16 < rows ? row0 + MT * 16 : rows) - 1 - row0);
+    const int place_lo = s.first + int(row0 / group), place_hi = s.first + int((row0 + last) / group);
+    const int start = parts.base + split * parts.per;
+    const int part_end = s.keys - start < parts.per ? s.keys : start + parts.per;
+    const int hi = place_hi + 1 < part_end ? place_hi + 1 : part_end;
+    int lo = start;
+    if (a.window) {
+      const int64_t edge = int64_t(place_lo) - a.window + 1;
+      if (edge > lo) lo = edge < part_end ? int(edge) & ~31 : part_end;
+    }
+
+    // q into LDS in operand order, 16 lanes for each row.
+    __syncthreads();
+    for (int r = wave * 4 + g4; r < MT * 16; r += W * 4) {
+      const int64_t row = row0 + r;
+      const bool live = row < rows;
+      const act_t* src = static_cast<const act_t*>(a.q) +
+                         (live ? (s.q0 + row / group) * a.q_token + (head * group + row % group) * a.q_head : 0);
+      constexpr int kUnits = (D / 8 + 15) / 16;
+      f32x4_t x[kUnits][2];
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int u = r16 + 16 * i;
+        x[i][0] = x[i][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        if (live && u < D / 8) {
+          x[i][0] = load4(Act(), src + u * 8);
+          x[i][1] = load4(Act(), src + u * 8 + 4);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(x[i][0][j]), fabsf(x[i][1][j])));
+      }
+      int up = 0;
+      if constexpr (kSplitQ) {
+        // 2^13 <= |q| 2^up < 2^14: high parts normal, low parts down to 2^-39 of the largest.
+        top = row16_top(top);
+        const int e = int((__builtin_bit_cast(uint32_t, top) >> 23) & 255) - 127;
+        up = top > 0.f ? min(13 - e, 126) : 0;
+      }
+      if (r16 == 0) back[r] = __builtin_ldexpf(1.f, -up);
+      const float lift = __builtin_ldexpf(1.f, up);
+      const int mt = r >> 4, rr = r & 15;
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int u = r16 + 16 * i;
+        if (u >= D / 8) continue;
+        const bool pairs = __is_same(Cache, E4M3) && u < 8 * (D / 64);
+        const int t = pairs ? 2 * (u / 8) + (u & 1) : u / 4;
+        const int g = pairs ? (u % 8) / 2 : u % 4;
+        const f32x4_t y = x[i][0] * lift, z = x[i][1] * lift;
+        qf[(mt * kSteps + t) * 64 + g * 16 + rr] =
+            u32x4_t{pack2(QK(), y[0], y[1]), pack2(QK(), y[2], y[3]), pack2(QK(), z[0], z[1]), pack2(QK(), z[2], z[3])};
+        if constexpr (kSplitQ)
+          qf[((MT + mt) * kSteps + t) * 64 + g * 16 + rr] =
+              u32x4_t{pack2_rest(QK(), y[0], y[1]), pack2_rest(QK(), y[2], y[3]),
+                      pack2_rest(QK(), z[0], z[1]), pack2_rest(QK(), z[2], z[3])};
+      }
+    }
+    __syncthreads();
+
+    float scale[MT], m[MT], sum[MT];
+    int place[MT];
+    f32x4_t o[MT][kTiles];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int64_t row = row0 + mt * 16 + r16;
+      place[mt] = row < rows ? s.first + int(row / group) : -1;
+      scale[mt] = a.scale * back[mt * 16 + r16];
+      if constexpr (kSize == 1) scale[mt] *= a.k_scale[head];
+      m[mt] = kNone;
+      sum[mt] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) o[mt][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+
+    const int all = hi > lo ? (hi - lo + 31) >> 5 : 0;           // tiles of 32 keys
+    const int mine = wave < all ? (all - wave + W - 1) / W : 0;
+    const cache_t* kbase = static_cast<const cache_t*>(a.k_cache) + head * p.k_head;
+    const cache_t* vbase = static_cast<const cache_t*>(a.v_cache) + head * p.v_head;
+    const uint32_t ktok = uint32_t(p.k_token) * kSize, vtok = uint32_t(p.v_token) * kSize;
+    int ids = -1;                                                // page of run `lane` of the next 64
+
+    auto runs = [&](int j, Run (&run)[2]) {
+      const int key0 = lo + (j * W + wave) * 32;
+      if ((j & 31) == 0) {
+        const int64_t key = lo + (int64_t(j + (lane >> 1)) * W + wave) * 32 + (lane & 1) * 16;
+        ids = key < hi ? page_of(p, b, int(key)) : -1;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int id = __builtin_amdgcn_readlane(ids, (j & 31) * 2 + h);
+        const int key = key0 + h * 16;
+        const int count = id < 0 ? 0 : (hi - key < 16 ? hi - key : 16);
+        const int in = key & ((1 << p.page_shift) - 1);
+        const int64_t page = id < 0 ? 0 : id;
+        run[h].count = count;
+        run[h].k = uniform_rsrc(kbase + page * p.k_page + in * p.k_token, count ? (count - 1) * ktok + D * kSize : 0);
+        run[h].v = uniform_rsrc(vbase + page * p.v_page + in * p.v_token, count ? (count - 1) * vtok + D * kSize : 0);
+      }
+    };
+    u32x4_t kf[2][kSteps];                                       // operand words of two 16-key runs
+    auto load_k = [&](const Run (&run)[2]) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t row = r16 * ktok;
+        if constexpr (kSize == 2) {
+#pragma unroll
+          for (int t = 0; t < kSteps; ++t)
+            kf[h][t] = __builtin_amdgcn_raw_buffer_load_b128(run[h].k, row + t * 64 + g4 * 16, 0, kStreamOnce);
+        } else {
+          // Raw codes; two steps' worth in the first one's words.
+#pragma unroll
+          for (int t = 0; t + 1 < kSteps; t += 2)
+            kf[h][t] = __builtin_amdgcn_raw_buffer_load_b128(run[h].k, row + t * 32 + g4 * 16, 0, kStreamOnce);
+          if constexpr (kSteps & 1) {
+            const u32x2_t w = __builtin_amdgcn_raw_buffer_load_b64(run[h].k, row + (D - 32) + g4 * 8, 0, kStreamOnce);
+            kf[h][kSteps - 1] = u32x4_t{w[0], w[1], 0, 0};
+          }
+        }
+      }
+    };
+    auto key_words = [&](int h, int t) -> u32x4_t {
+      if constexpr (kSize == 2) return kf[h][t];
+      const u32x4_t w = kf[h][t & ~1];
+      const uint32_t x = (t & 1) ? w[2] : w[0], y = (t & 1) ? w[3] : w[1];
+      return u32x4_t{widen2<false>(QK(), x), widen2<true>(QK(), x), widen2<false>(QK(), y), widen2<true>(QK(), y)};
+    };
+    // Eight keys' words of each value chunk: per_lane components of a key.
+    u32x4_t vf[Chunks<D>::count][8];
+    auto load_v = [&](const Run (&run)[2]) {
+#pragma unroll
+      for (int c = 0; c < Chunks<D>::count; ++c) {
+        constexpr int kMost = 8;
+        const int n = Chunks<D>::per_lane(c);
+#pragma unroll
+        for (int j = 0; j < kMost; ++j) {
+          const rsrc_t r = run[j >> 2].v;
+          const uint32_t off = (g4 * 4 + (j & 3)) * vtok + (Chunks<D>::start(c) + r16 * n) * kSize;
+          const int bytes = n * kSize;
+          if (bytes == 16) {
+            vf[c][j] = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kStreamOnce);
+          } else if (bytes == 8) {
+            const u32x2_t w = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, kStreamOnce);
+            vf[c][j] = u32x4_t{w[0], w[1], 0, 0};
+          } else if (bytes == 4) {
+            vf[c][j] = u32x4_t{__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, kStreamOnce), 0, 0, 0};
+          } else {
+            vf[c][j] = u32x4_t{__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, kStreamOnce), 0, 0, 0};
+          }
+        }
+      }
+    };
+    // Word e of key j of chunk c as two 16-bit values.
+    auto value_word = [&](int c, int j, int e) -> uint32_t {
+      if constexpr (kSize == 2) return vf[c][j][e];
+      const uint32_t w = vf[c][j][e >> 1];
+      return (e & 1) ? widen2<true>(PV(), w) : widen2<false>(PV(), w);
+    };
+
+    auto sees = [&](int at, int key) {
+      return key <= at && (a.window == 0 || int64_t(key) > int64_t(at) - a.window);
+    };
+    auto is_clean = [&](int key0, const Run (&run)[2]) {         // every row sees every key
+      return run[0].count == 16 && run[1].count == 16 && key0 + 31 <= place_lo &&
+             (a.window == 0 || int64_t(key0) > int64_t(place_hi) - a.window);
+    };
+    // Zeros for the values that are not finite; whether the wave has any.
+    auto tame_values = [&]() {
+      uint32_t any = 0;
+#pragma unroll
+      for (int c = 0; c < Chunks<D>::count; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int e = 0; e < (Chunks<D>::per_lane(c) * kSize + 3) / 4; ++e) {
+            constexpr uint32_t top = kSize == 1 ? 0x7Fu : (__is_same(Cache, F16) ? 0x7C00u : 0x7F80u);
+            constexpr uint32_t whole = kSize == 1 ? 0xFFu : 0xFFFFu;
+#pragma unroll
+            for (int bit = 0; bit < 32; bit += 8 * kSize)
+              if ((vf[c][k][e] >> bit & top) == top) {
+                any = 1;
+                vf[c][k][e] &= ~(whole << bit);
+              }
+          }
+      return __ballot(any != 0) != 0;
+    };
+    // What tame_values left out, added where a row sees it.
+    auto add_wild = [&](int key0, const Run& run) {
+#pragma unroll 1
+      for (int k = 0; k < run.count; ++k)
+#pragma unroll
+        for (int c = 0; c < Chunks<D>::count; ++c)
+#pragma unroll
+          for (int i = 0; i < Chunks<D>::per_lane(c); ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int comp = Chunks<D>::start(c) + (4 * g4 + r) * Chunks<D>::per_lane(c) + i;
+              const uint32_t off = uint32_t(k) * vtok + comp * kSize;
+              float x;
+              asm volatile("" ::: "memory");                     // one load at a time: registers are short
+              if constexpr (kSize == 1) {
+                x = __builtin_amdgcn_cvt_f32_fp8(__builtin_amdgcn_raw_buffer_load_b8(run.v, off, 0, 0), 0);
+              } else {
+                const uint16_t w = __builtin_amdgcn_raw_buffer_load_b16(run.v, off, 0, 0);
+                x = float(__builtin_bit_cast(cache_t, w));
+              }
+              if (fabsf(x) < __builtin_inff()) continue;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+                if (sees(place[mt], key0 + k)) o[mt][Chunks<D>::tile(c) + i][r] += x;
+            }
+    };
+
+    Run run[2], next[2];
+    if (mine > 0) {
+      runs(0, run);
+      load_k(run);
+      load_v(run);
+    }
+    bool wild = false;
+    for (int j = 0; j < mine; ++j) {
+      const int key0 = lo + (j * W + wave) * 32;
+      f32x4_t sc[MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) sc[mt][0] = sc[mt][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int t = 0; t < kSteps; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const u32x4_t k = key_words(h, t);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            sc[mt][h] = mfma(QK(), k, qf[(mt * kSteps + t) * 64 + lane], sc[mt][h]);
+            if constexpr (kSplitQ)
+              sc[mt][h] = mfma(QK(), k, qf[((MT + mt) * kSteps + t) * 64 + lane], sc[mt][h]);
+          }
+        }
+      const bool more = j + 1 < mine;
+      if (more) {
+        runs(j + 1, next);
+        load_k(next);
+      }
+      const bool clean = is_clean(key0, run);
+      u32x4_t pf[MT], pl[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = sc[mt][i >> 2][i & 3] * scale[mt];
+        if (!clean) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int in = g4 * 4 + (i & 3);
+            if (in >= run[i >> 2].count || !sees(place[mt], key0 + (i >> 2) * 16 + in)) x[i] = kNone;
+          }
+        }
+        float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+        top = fmaxf(m[mt], over_groups_max(top));
+        const float base = top == kNone ? 0.f : top;             // no key yet: every p is 2^-inf
+        const float shrink = __builtin_amdgcn_exp2f(m[mt] - base);
+        m[mt] = top;
+        float total = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] = __builtin_amdgcn_exp2f(x[i] - base + kLift);
+          total += x[i];
+        }
+        sum[mt] = sum[mt] * shrink + total;
+        pf[mt] = u32x4_t{pack2(PV(), x[0], x[1]), pack2(PV(), x[2], x[3]), pack2(PV(), x[4], x[5]), pack2(PV(), x[6], x[7])};
+        if constexpr (kSplitP)
+          pl[mt] = u32x4_t{pack2_rest(PV(), x[0], x[1]), pack2_rest(PV(), x[2], x[3]),
+                           pack2_rest(PV(), x[4], x[5]), pack2_rest(PV(), x[6], x[7])};
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) o[mt][i] = o[mt][i] * shrink;
+      }
+      // Values that are not finite must not meet the zeros of rows that do not see them.
+      if (!clean) wild |= tame_values();
+#pragma unroll
+      for (int c = 0; c < Chunks<D>::count; ++c)
+#pragma unroll
+        for (int e = 0; e < Chunks<D>::per_lane(c) / 2; ++e) {
+          uint32_t w[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) w[k] = value_word(c, k, e);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t pick = half ? 0x07060302u : 0x05040100u;
+            u32x4_t v;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = __builtin_amdgcn_perm(w[2 * k + 1], w[2 * k], pick);
+            const int tile = Chunks<D>::tile(c) + 2 * e + half;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              o[mt][tile] = mfma(PV(), v, pf[mt], o[mt][tile]);
+              if constexpr (kSplitP) o[mt][tile] = mfma(PV(), v, pl[mt], o[mt][tile]);
+            }
+          }
+        }
+      if (more) {
+        load_v(next);
+        run[0] = next[0];
+        run[1] = next[1];
+      }
+    }
+
+    // Rare: once more over the tiles whose rows differ in what they see.
+    if (wild) {
+      for (int j = 0; j < mine; ++j) {
+        runs(j, run);
+        const int key0 = lo + (j * W + wave) * 32;
+        if (is_clean(key0, run)) continue;
+        add_wild(key0, run[0]);
+        add_wild(key0 + 16, run[1]);
+      }
+    }
+
+    // Join the waves: the upper half leaves its state, the lower half takes it in.
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) sum[mt] = over_groups_sum(sum[mt]);
+#pragma unroll
+    for (int live = W / 2; live > 0; live >>= 1) {
+      __syncthreads();                                           // q and the last states are done with
+      if (wave >= live && wave < 2 * live) {
+        float* to = join + size_t(wave - live) * (kRegs + 2 * MT) * 64 + lane;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) to[((mt * kTiles + i) * 4 + r) * 64] = o[mt][i][r];
+          to[(kRegs + 2 * mt) * 64] = m[mt];
+          to[(kRegs + 2 * mt + 1) * 64] = sum[mt];
+        }
+      }
+      __syncthreads();
+      if (wave < live) {
+        const float* from = join + size_t(wave) * (kRegs + 2 * MT) * 64 + lane;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const float m2 = from[(kRegs + 2 * mt) * 64], s2 = from[(kRegs + 2 * mt + 1) * 64];
+          const float top = fmaxf(m[mt], m2), base = top == kNone ? 0.f : top;
+          const float f1 = __builtin_amdgcn_exp2f(m[mt] - base), f2 = __builtin_amdgcn_exp2f(m2 - base);
+          m[mt] = top;
+          sum[mt] = sum[mt] * f1 + s2 * f2;
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              o[mt][i][r] = o[mt][i][r] * f1 + from[((mt * kTiles + i) * 4 + r) * 64] * f2;
+        }
+      }
+    }
+    if (wave != 0) continue;
+    // Lane (r16, g4) holds row r16 and, of chunk c, components start + (4 g4 + r) n + 0 .. n - 1.
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int64_t row = row0 + mt * 16 + r16;
+      if (row >= rows) continue;
+      const int64_t token = s.q0 + row / group;
+      const int qh = head * group + int(row % group);
+      const float vs = kSize == 1 ? a.v_scale[head] : 1.f;
+      const float f = a.splits > 1 ? 1.f : (sum[mt] > 0.f || sum[mt] != sum[mt] ? vs / sum[mt] : 0.f);
+      float* part = a.part + ((token * p.q_heads + qh) * a.splits + split) * (D + 4);
+      act_t* dst = static_cast<act_t*>(a.out) + token * a.o_token + qh * a.o_head;
+#pragma unroll
+      for (int c = 0; c < Chunks<D>::count; ++c) {
+        const int n = Chunks<D>::per_lane(c);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int at = Chunks<D>::start(c) + (4 * g4 + r) * n;
+          if (n >= 4) {
+#pragma unroll
+            for (int i = 0; i < n; i += 4) {
+              const int t0 = Chunks<D>::tile(c) + i;
+              const f32x4_t y = f32x4_t{o[mt][t0][r], o[mt][t0 + 1][r], o[mt][t0 + 2][r], o[mt][t0 + 3][r]} * f;
+              if (a.splits > 1) store4(F32(), part + 4 + at + i, y);
+              else store4(Act(), dst + at + i, y);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+              const float y = o[mt][Chunks<D>::tile(c) + i][r] * f;
+              if (a.splits > 1) part[4 + at + i] = y;
+              else dst[at + i] = act_t(y);
+            }
+          }
+        }
+      }
+      if (a.splits > 1 && g4 == 0) {
+        part[0] = m[mt];
+        part[1] = sum[mt];
+      }
+    }
+  }
+}
+
+// Join the parts of a row: one wave for each new token and head.
+template <class Act, int D>
+__global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
+  const Pages& p = a.pages;
+  const int lane = threadIdx.x & 63;
+  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (row >= int64_t(p.tokens) * p.q_heads) return;
+  const int token = int(row / p.q_heads), qh = int(row % p.q_heads);
+  const int b = owner(p, token);
+  if (b >= p.batch) return;
+  const Seq s = sequence(p, b);
+  if (token < s.q0 || token >= s.q0 + s.q_len) return;
+  const int parts = parts_of(s, a.window, a.splits, a.split_keys).count;
+  const float* part = a.part + row * a.splits * (D + 4);
+  float m = kNone;
+  for (int i = lane; i < parts; i += 64) m = fmaxf(m, part[size_t(i) * (D + 4)]);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  const float base = m == kNone ? 0.f : m;
+  constexpr int kPer = (D + 63) / 64;
+  float sum = 0.f, o[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) o[i] = 0.f;
+  for (int i = 0; i < parts; ++i) {
+    const float* at = part + size_t(i) * (D + 4);
+    const float f = __builtin_amdgcn_exp2f(at[0] - base);
+    // A part in which this row sees no key has nothing to add, whatever it holds.
+    if (at[0] == kNone) continue;
+    sum += at[1] * f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (lane + 64 * j < D) o[j] += at[4 + lane + 64 * j] * f;
+  }
+  const float vs = a.v_scale ? a.v_scale[qh / (p.q_heads / p.kv_heads)] : 1.f;
+  const float f = sum > 0.f || sum != sum ? vs / sum : 0.f;
+  typedef typename Act::elem act_t;
+  act_t* dst = static_cast<act_t*>(a.out) + token * a.o_token + qh * a.o_head;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (lane + 64 * j < D) dst[lane + 64 * j] = act_t(o[j] * f);
+}
+
+constexpr int kWaves = 4;
+
+template <class Act, class Cache, int D, int MT>
+hipError_t launch_stream(const AttnArgs& a, const AttnPlan& plan, hipStream_t stream) {
+  constexpr size_t q_bytes = size_t(__is_same(Act, F32) ? 2 : 1) * MT * (D / 32) * 1024;
+  constexpr size_t join_bytes = size_t(kWaves / 2) * (MT * (D / 16) * 4 + 2 * MT) * 256;
+  constexpr size_t lds = q_bytes > join_bytes ? q_bytes : join_bytes;
+  auto fn = stream_kernel<Act, Cache, D, MT, kWaves>;
+  if (lds > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(fn, dim3(plan.splits, plan.steps * a.pages.kv_heads, a.pages.batch), dim3(64 * kWaves), lds,
+                     stream, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || plan.splits == 1) return e;
+  const int64_t rows = int64_t(a.pages.tokens) * a.pages.q_heads;
+  hipLaunchKernelGGL((join_kernel<Act, D>), dim3(uint32_t((rows + 3) / 4)), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <class Act, class Cache, int D>
+hipError_t launch_rows(const AttnArgs& a, const AttnPlan& plan, hipStream_t stream) {
+  if constexpr (D <= 128) {
+    if (plan.row_tiles == 2) return launch_stream<Act, Cache, D, 2>(a, plan, stream);
+  }
+  return launch_stream<Act, Cache, D, 1>(a, plan, stream);
+}
+
+template <class Act, class Cache>
+hipError_t launch_dim(const AttnArgs& a, const AttnPlan& plan, hipStream_t stream) {
+  switch (a.pages.head_dim) {
+    case 64: return launch_rows<Act, Cache, 64>(a, plan, stream);
+    case 96: return launch_rows<Act, Cache, 96>(a, plan, stream);
+    case 128: return launch_rows<Act, Cache, 128>(a, plan, stream);
+    case 192: return launch_rows<Act, Cache, 192>(a, plan, stream);
+    default: return launch_rows<Act, Cache, 256>(a, plan, stream);
+  }
+}
+
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+AttnPlan plan_attention(const tq2_paged_attention_args& a) {
+  const tq2_paged_cache& c = a.cache;
+  AttnPlan plan;
+  const int64_t max_q = a.max_q < 1 ? 1 : (a.max_q < c.tokens ? a.max_q : c.tokens);
+  const int64_t rows = max_q * (c.q_heads / c.kv_heads);
+  // Two row tiles share the loads of keys and values; wider heads' outputs leave no registers for a second.
+  plan.row_tiles = rows <= 16 || c.head_dim > 128 ? 1 : 2;
+  const int64_t steps = up(rows, plan.row_tiles * 16);
+  const int64_t room = 65535 / c.kv_heads;                       // of the grid's second axis
+  plan.steps = int32_t(steps < room ? steps : room);
+  // Parts: enough blocks for every CU several times over, but at least 128
+  // keys each, a tile for every wave.
+  const int64_t span = a.window ? a.window + max_q + 31 : a.max_kv;   // that a sequence's rows see
+  const int64_t keys = span < a.max_kv ? span : a.max_kv;
+  const int64_t blocks = c.batch * c.kv_heads * plan.steps;
+  int64_t per = up(up(keys * blocks, 4096), 128) * 128;
+  if (per < 128) per = 128;
+  int64_t splits = keys < 1 ? 1 : up(keys, per);
+  if (splits > 512) splits = 512;
+  plan.splits = int32_t(splits);
+  plan.split_keys = int32_t(per);
+  plan.workspace = splits == 1 ? 0 : size_t(c.tokens) * size_t(c.q_heads) * size_t(splits) * size_t(c.head_dim + 4) * 4;
+  return plan;
+}
+
+hipError_t launch_paged_attention(const AttnArgs& a, const AttnPlan& plan, int act, int cache,
+                                  hipStream_t stream) {
+  const bool narrow = cache == TQ2_TYPE_E4M3;
+  if (act == TQ2_TYPE_F32)
+    return narrow ? launch_dim<F32, E4M3>(a, plan, stream) : launch_dim<F32, F16>(a, plan, stream);
+  if (act == TQ2_TYPE_F16)
+    return narrow ? launch_dim<F16, E4M3>(a, plan, stream) : launch_dim<F16, F16>(a, plan, stream);
+  return narrow ? launch_dim<BF16, E4M3>(a, plan, stream) : launch_dim<BF16, BF16>(a, plan, stream);
+}
+
+}  // namespace tq2

@@ -32,4 +32,32 @@ struct AppendArgs {
 // Arguments are already validated: tokens >= 1.
 hipError_t launch_kv_append(const AppendArgs& a, int act, int cache, hipStream_t stream);
 
+struct AttnArgs {
+  Pages pages;
+  const void* q;
+  void* out;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  int64_t q_token, q_head, o_token, o_head;
+  float* part;                           // partial outputs, nullptr if splits == 1
+  float scale;                           // of the scores, times log2 e
+  int32_t window;                        // 0: none
+  int32_t splits;                        // parts of a sequence's keys
+  int32_t split_keys;                    // least keys of a part, a multiple of 32
+};
+
+// How a call is laid out; from sizes alone.
+struct AttnPlan {
+  int32_t row_tiles;                     // 16-row tiles of a step (rows: new tokens times heads of a key head)
+  int32_t steps;                         // steps of max_q new tokens
+  int32_t splits, split_keys;
+  size_t workspace;                      // bytes
+};
+AttnPlan plan_attention(const tq2_paged_attention_args& a);
+// Arguments are already validated: tokens >= 1.
+hipError_t launch_paged_attention(const AttnArgs& a, const AttnPlan& plan, int act, int cache,
+                                  hipStream_t stream);
+
 }  // namespace tq2

@@ -63,17 +63,6 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// Number of sequences that end at or before row t: the one that owns it.
-__device__ __forceinline__ int owner(const Pages& p, int t) {
-  if (!p.cu_q) return t;
-  int n = 0;
-  for (int lo = 0; lo < p.batch; lo += 64) {
-    const int b = lo + int(threadIdx.x & 63);
-    n += __popcll(__ballot(b < p.batch && p.cu_q[b + 1] <= t));
-  }
-  return n;
-}
-
 // T tokens of a block; blockIdx.y shares a token's heads out.
 template <class Act, class Cache, int G, int T>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a) {

@@ -110,6 +110,16 @@ tq2::Pages pages_of(const tq2_paged_cache& c) {
   return p;
 }
 
+// Sizes of an attention call; nothing is dereferenced.
+int check_attention_sizes(const tq2_paged_attention_args& a) {
+  const int st = check_cache_sizes(a.cache);
+  if (st != TQ2_OK) return st;
+  if (!size_ok(a.max_q, 0, kMaxDim) || !size_ok(a.max_kv, 0, (int64_t(1) << 31) - 1) ||
+      !size_ok(a.window, 0, (int64_t(1) << 31) - 1))
+    return TQ2_ERR_INVALID;
+  return TQ2_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -214,6 +224,66 @@ int tq2_kv_append(const tq2_kv_append_args* args, void* stream) {
   g.interleaved = a.interleaved != 0;
   return launch_status(
       tq2::launch_kv_append(g, int(c.act_type), int(c.cache_type), static_cast<hipStream_t>(stream)));
+}
+
+size_t tq2_paged_attention_workspace_bytes(const tq2_paged_attention_args* args) {
+  if (!args || check_attention_sizes(*args) != TQ2_OK || args->cache.tokens == 0) return 0;
+  return tq2::plan_attention(*args).workspace;
+}
+
+int tq2_paged_attention(const tq2_paged_attention_args* args, void* stream) {
+  if (!args) return TQ2_ERR_INVALID;
+  const tq2_paged_attention_args& a = *args;
+  const tq2_paged_cache& c = a.cache;
+  int st = check_attention_sizes(a);
+  if (st != TQ2_OK) return st;
+  if (!(a.scale > 0.0) || !(a.scale <= 3e38)) return TQ2_ERR_INVALID;
+  if (c.tokens == 0) return TQ2_OK;
+  st = check_cache_arrays(c);
+  if (st != TQ2_OK) return st;
+  if (!a.q || !a.out) return TQ2_ERR_INVALID;
+  const int64_t ab = type_bytes(c.act_type), cb = type_bytes(c.cache_type), d = c.head_dim;
+  bool bad = false;
+  const bool even = strides_ok(ab, a.q_token_stride, a.q_head_stride, 0, &bad) &
+                    strides_ok(ab, a.out_token_stride, a.out_head_stride, 0, &bad);
+  // A buffer resource spans 16 tokens of a page.
+  const int64_t most = (int64_t(1) << 31) - 4096;
+  if (bad || c.k_token_stride * cb * 16 > most || c.v_token_stride * cb * 16 > most) return TQ2_ERR_INVALID;
+  const tq2::AttnPlan plan = tq2::plan_attention(a);
+  if (a.workspace_bytes < 0 || (plan.workspace > 0 && (!a.workspace || size_t(a.workspace_bytes) < plan.workspace)))
+    return TQ2_ERR_INVALID;
+  if (!even || !aligned(a.q, 16) || !aligned(a.out, 16) || !aligned(a.workspace, 16)) return TQ2_ERR_ALIGN;
+  const size_t qb = extent(ab, d, c.tokens, a.q_token_stride, c.q_heads, a.q_head_stride);
+  const size_t ob = extent(ab, d, c.tokens, a.out_token_stride, c.q_heads, a.out_head_stride);
+  const bool in_place = a.out == a.q && a.out_token_stride == a.q_token_stride && a.out_head_stride == a.q_head_stride;
+  if (!in_place && overlaps(a.out, ob, a.q, qb)) return TQ2_ERR_ALIAS;
+  for (const auto& cache : {std::make_pair(c.k, k_extent(c)), std::make_pair(c.v, v_extent(c))})
+    if (overlaps(cache.first, cache.second, a.out, ob) ||
+        overlaps(cache.first, cache.second, a.workspace, plan.workspace))
+      return TQ2_ERR_ALIAS;
+  if (overlaps(a.workspace, plan.workspace, a.out, ob) || overlaps(a.workspace, plan.workspace, a.q, qb))
+    return TQ2_ERR_ALIAS;
+  st = check_device();
+  if (st != TQ2_OK) return st;
+  tq2::AttnArgs g;
+  g.pages = pages_of(c);
+  g.q = a.q;
+  g.out = a.out;
+  g.k_cache = c.k;
+  g.v_cache = c.v;
+  g.k_scale = c.k_scale;
+  g.v_scale = c.v_scale;
+  g.q_token = a.q_token_stride;
+  g.q_head = a.q_head_stride;
+  g.o_token = a.out_token_stride;
+  g.o_head = a.out_head_stride;
+  g.part = plan.splits > 1 ? static_cast<float*>(a.workspace) : nullptr;
+  g.scale = float(a.scale * 1.4426950408889634);                 // scores as exponents of two
+  g.window = int32_t(a.window);
+  g.splits = plan.splits;
+  g.split_keys = plan.split_keys;
+  return launch_status(tq2::launch_paged_attention(g, plan, int(c.act_type), int(c.cache_type),
+                                                   static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

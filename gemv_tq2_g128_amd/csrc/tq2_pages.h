@@ -12,6 +12,9 @@
 
 namespace tq2 {
 
+// Places past this are never reached; sums of a place and a tile stay in 32 bits.
+constexpr int64_t kMaxKeys = 0x7FFF0000;
+
 // The cache as kernels see it.
 struct Pages {
   const int32_t* table;
@@ -48,7 +51,8 @@ TQ2_HD Seq sequence(const Pages& p, int32_t b) {
   s.q0 = lo;
   s.q_len = hi - lo;
   s.first = int32_t(int64_t(len) - (int64_t(end) - lo));
-  const int64_t room = int64_t(p.cols) << p.page_shift;
+  int64_t room = int64_t(p.cols) << p.page_shift;
+  if (room > kMaxKeys) room = kMaxKeys;
   s.keys = len < 0 ? 0 : (len > room ? int32_t(room) : len);
   return s;
 }
@@ -61,5 +65,39 @@ TQ2_HD int32_t page_of(const Pages& p, int32_t b, int32_t n) {
   const int32_t id = p.table[int64_t(b) * p.table_stride + col];
   return id >= 0 && id < p.pages ? id : -1;
 }
+
+// The parts that a sequence's keys are cut into for attention: part i covers
+// base + i * per and on, for i < count.  At most `splits` parts of a multiple of
+// 32 keys, at least `split_keys`; keys that no row sees through the window
+// are left out in front.
+struct Parts {
+  int32_t base, per, count;
+};
+
+TQ2_HD Parts parts_of(const Seq& s, int32_t window, int32_t splits, int32_t split_keys) {
+  Parts r;
+  const int64_t edge = window ? int64_t(s.first) - window + 1 : 0;
+  r.base = edge <= 0 ? 0 : int32_t(edge < s.keys ? edge : s.keys) & ~31;
+  const int32_t keys = s.keys - r.base;
+  const int64_t even = (int64_t(keys) + splits - 1) / splits;
+  const int64_t up = (even + 31) & ~int64_t(31);
+  r.per = up > split_keys ? int32_t(up) : split_keys;
+  r.count = keys > 0 ? int32_t((int64_t(keys) + r.per - 1) / r.per) : 1;
+  return r;
+}
+
+#ifdef __HIP__
+// Number of sequences that end at or before row t: the one that owns it.  For a
+// whole wave.
+__device__ __forceinline__ int owner(const Pages& p, int t) {
+  if (!p.cu_q) return t;
+  int n = 0;
+  for (int lo = 0; lo < p.batch; lo += 64) {
+    const int b = lo + int(threadIdx.x & 63);
+    n += __popcll(__ballot(b < p.batch && p.cu_q[b + 1] <= t));
+  }
+  return n;
+}
+#endif
 
 }  // namespace tq2

@@ -103,6 +103,42 @@ typedef struct tq2_kv_append_args {
  * operand), DEVICE, LAUNCH. */
 int tq2_kv_append(const tq2_kv_append_args* args, void* stream);
 
+typedef struct tq2_paged_attention_args {
+  tq2_paged_cache cache;
+  const void* q;             /* [tokens, q_heads, head_dim] */
+  void* out;                 /* the same shape; may be q itself (same strides) */
+  int64_t q_token_stride, q_head_stride;
+  int64_t out_token_stride, out_head_stride;
+  int64_t max_q;             /* most new tokens of a sequence, most tokens of one: the launch is */
+  int64_t max_kv;            /* shaped for them; larger ones in cu_q and kv_len are still done */
+  int64_t window;            /* a token sees itself and window - 1 before it; 0: all before it */
+  double scale;              /* of the scores, usually 1 / sqrt(head_dim) */
+  void* workspace;           /* NULL if none is needed */
+  int64_t workspace_bytes;
+} tq2_paged_attention_args;
+
+/* Bytes of workspace that tq2_paged_attention needs for these sizes, types,
+ * max_q, max_kv and window (no pointer but whether cu_q is NULL is looked at),
+ * or 0; also 0 for sizes that it refuses.  Pure host function. */
+size_t tq2_paged_attention_workspace_bytes(const tq2_paged_attention_args* args);
+
+/* out = softmax(scale * q K^T + mask) V for each new token over the tokens of
+ * its sequence up to itself, query head h reading key head
+ * h / (q_heads / kv_heads).  Rows that see no token give zeros.
+ * Keys and values of places that a row does not see do not reach it, whatever
+ * they hold.
+ * Accuracy: f32 activations as two binary16 parts, products and sums f32,
+ * about 1e-6 of sum_j p_j |v_j|; 16-bit activations enter the products as they
+ * are and the probabilities are rounded to the cache's type (binary16 for
+ * e4m3), half a step each.
+ * Activations, caches and workspace: 16-byte aligned, strides multiples of 16
+ * bytes; 16 tokens of a page lie within 2^31 bytes.  The workspace's content
+ * needs no preparation and means nothing afterwards.
+ * tokens == 0 is a no-op.  Errors: INVALID (null pointer, size out of range, a
+ * workspace that is too small, types or head_dim not listed), SHAPE, ALIGN,
+ * ALIAS (out overlaps a cache, the workspace or a part of q), DEVICE, LAUNCH. */
+int tq2_paged_attention(const tq2_paged_attention_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -41,6 +41,15 @@ def append(**over):
     return attn.kv_append_ptr(attn._CACHE.pack(*(c[n] for n in CACHE)) + attn._APPEND.pack(*a.values()))
 
 
+def attention(entry=attn.paged_attention_ptr, **over):
+    c = cache_fields(**over)
+    a = dict(q=A + 4 * G, out=A + 7 * G, q_ts=512, q_hs=128, o_ts=512, o_hs=128, max_q=1, max_kv=64, window=0,
+             scale=0.1, workspace=0, workspace_bytes=0)
+    assert set(over) <= set(c) | set(a)
+    a.update({n: x for n, x in over.items() if n in a})
+    return entry(attn._CACHE.pack(*(c[n] for n in CACHE)) + attn._ATTENTION.pack(*a.values()))
+
+
 def test_header_and_binding_agree():
     with open(os.path.join(ROOT, "include", "tq2_attn.h")) as f:
         text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
@@ -109,6 +118,64 @@ def test_append_without_tokens_is_a_no_op():
     assert append(tokens=0, batch=0, page=24) == tq2.TQ2_ERR_SHAPE
 
 
+E8 = dict(cache_type=E4M3, k_scale=A + 9 * G, v_scale=A + 10 * G)
+
+
+def test_valid_attention_reaches_the_device_check():
+    if torch.cuda.device_count() > 0:
+        pytest.skip("a GPU is visible; this check is for GPU-less hosts")
+    need = attention(attn.paged_attention_workspace_bytes_ptr, max_kv=5000)
+    assert need > 0
+    for over in (dict(), dict(act_type=BF16, cache_type=BF16), dict(act_type=F16, cache_type=F16), E8,
+                 dict(out=A + 4 * G), dict(cu_q=A + 12 * G, tokens=100, max_q=90), dict(window=17), dict(max_q=0),
+                 dict(max_kv=0), dict(pages=0, k=0, v=0),
+                 dict(max_kv=5000, workspace=A + 13 * G, workspace_bytes=need)):
+        assert attention(**over) == tq2.TQ2_ERR_DEVICE, over
+
+
+@pytest.mark.parametrize("over", [
+    dict(k=0), dict(v=0), dict(table=0), dict(kv_len=0), dict(q=0), dict(out=0), dict(batch=-1), dict(tokens=4),
+    dict(tokens=-1), dict(kv_heads=0), dict(q_heads=0), dict(head_dim=80), dict(act_type=BF16), dict(cache_type=E4M3),
+    dict(k_scale=A + 9 * G, v_scale=A + 10 * G), dict(q_ts=-512), dict(o_hs=1 << 41), dict(max_q=-1), dict(max_kv=-1),
+    dict(max_kv=1 << 31), dict(window=-1), dict(window=1 << 31), dict(scale=0.0), dict(scale=-1.0),
+    dict(scale=float("nan")), dict(scale=float("inf")), dict(workspace_bytes=-1), dict(max_kv=5000),
+    dict(max_kv=5000, workspace=A + 13 * G, workspace_bytes=4096), dict(k_token_stride=1 << 27),
+    dict(v_token_stride=1 << 27)])
+def test_attention_invalid(over):
+    assert attention(**over) == tq2.TQ2_ERR_INVALID
+
+
+@pytest.mark.parametrize("over", [dict(page=0), dict(page=8), dict(page=48), dict(kv_heads=3)])
+def test_attention_shape(over):
+    assert attention(**over) == tq2.TQ2_ERR_SHAPE
+
+
+@pytest.mark.parametrize("over", [dict(k=A + 8), dict(q=A + 4 * G + 8), dict(out=A + 7 * G + 4), dict(q_ts=514),
+                                  dict(o_hs=130), dict(v_page_stride=4100), dict(workspace=A + 13 * G + 8)])
+def test_attention_alignment(over):
+    assert attention(**over) == tq2.TQ2_ERR_ALIGN
+
+
+@pytest.mark.parametrize("over", [
+    dict(v=A), dict(out=A + 4 * G + 16), dict(out=A + 4 * G, o_ts=1024), dict(out=A + 4096), dict(out=A + G),
+    dict(max_kv=5000, workspace=A + 4 * G, workspace_bytes=1 << 30),
+    dict(max_kv=5000, workspace=A + 7 * G, workspace_bytes=1 << 30),
+    dict(max_kv=5000, workspace=A, workspace_bytes=1 << 30)])
+def test_attention_aliasing(over):
+    assert attention(**over) == tq2.TQ2_ERR_ALIAS
+
+
+def test_attention_workspace():
+    def need(**over):
+        return attention(attn.paged_attention_workspace_bytes_ptr, **over)
+
+    assert need(max_kv=0) == need(max_kv=1) == 0
+    assert need(head_dim=80, max_kv=5000) == need(page=7, max_kv=5000) == need(tokens=0, batch=0, max_kv=5000) == 0
+    assert 0 < need(max_kv=100000, window=500) < need(max_kv=100000)
+    assert attention(tokens=0, batch=0, k=0, q=0, out=0, table=0) == tq2.TQ2_OK
+    assert attention(tokens=0, batch=0, page=24) == tq2.TQ2_ERR_SHAPE
+
+
 def test_front_end_checks():
     k = torch.zeros(2, 2, 64)
     cache = torch.zeros(4, 2, 16, 64, dtype=torch.float16)
@@ -117,6 +184,10 @@ def test_front_end_checks():
         attn.kv_append(k, k, cache, cache, lens, table)
     with pytest.raises(ValueError, match="kv_heads, head_dim"):
         attn.kv_append(k[0], k[0], cache, cache, lens, table)
+    with pytest.raises(ValueError, match="device tensor"):
+        attn.paged_attention(k, cache, cache, lens, table)
+    with pytest.raises(ValueError, match="q_heads, head_dim"):
+        attn.paged_attention(k[0], cache, cache, lens, table)
 
 
 HARNESS = r"""
@@ -127,6 +198,10 @@ extern "C" int64_t place_offset(const int32_t* table, const int32_t* kv_len, con
   p.table = table; p.kv_len = kv_len; p.cu_q = cu_q; p.batch = batch; p.tokens = tokens; p.pages = pages;
   p.cols = cols; p.page_shift = shift; p.table_stride = table_stride;
   return tq2::page_of(p, b, n);
+}
+extern "C" void parts(int32_t first, int32_t keys, int32_t window, int32_t splits, int32_t split_keys, int32_t* out) {
+  const tq2::Parts r = tq2::parts_of(tq2::Seq{0, 1, first, keys}, window, splits, split_keys);
+  out[0] = r.base; out[1] = r.per; out[2] = r.count;
 }
 extern "C" void seq(const int32_t* kv_len, const int32_t* cu_q, int batch, int tokens, int cols, int shift, int b,
                     int32_t* out) {
@@ -161,6 +236,24 @@ def test_page_lookups_stay_inside(pages_lib):
     assert [look(0, n) for n in (0, 15, 16, 31, 32, 48, 63)] == [3, 3, -1, -1, -1, 9, 9]
     assert [look(1, n) for n in (0, 16, 32, 63)] == [-1, 0, -1, 5]
     assert [look(0, n) for n in (-1, -2 ** 31, 64, 2 ** 31 - 1)] == [-1] * 4
+
+
+def test_parts_cover_the_keys(pages_lib):
+    """The parts of a sequence's keys: in order, no more than asked for, and every key a row can see is in one."""
+    rng = random.Random(2)
+    edge = [0, 1, 31, 32, 33, 100, 4096, 131071, 2 ** 31 - 1]
+    for _ in range(4000):
+        keys = rng.choice(edge) if rng.random() < 0.5 else rng.randrange(0, 1 << rng.randrange(1, 31))
+        keys = min(keys, 0x7FFF0000)
+        first = keys - rng.choice([0, 1, 5, 200, keys, keys + 7])
+        window = rng.choice([0, 0, 1, 40, 1024, 2 ** 31 - 1])
+        splits, split_keys = rng.choice([1, 2, 7, 512]), rng.choice([128, 1024])
+        out = (ctypes.c_int32 * 3)()
+        pages_lib.parts(first, keys, window, splits, split_keys, out)
+        base, per, count = out
+        assert base % 32 == 0 and per % 32 == 0 and per >= split_keys and 1 <= count <= splits
+        assert 0 <= base <= keys and base + count * per >= keys and (count == 1 or base + (count - 1) * per < keys)
+        assert base <= max(0, first - window + 1 if window else 0)
 
 
 def test_sequences_are_cut_to_the_arrays(pages_lib):
