@@ -30,70 +30,10 @@
 // loads as zero.  Tiles that every row sees whole skip the comparisons.  Where
 // rows differ in what they see, a value that is not finite is kept from rows
 // that do not see it (zero times infinity would reach them).
-#include "tq2_attn_internal.h"
-#include "tq2_device.h"
-#include "tq2_types.h"
+#include "tq2_attn_device.h"
 
 namespace tq2 {
 namespace {
-
-typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-
-constexpr float kNone = -__builtin_inff();
-
-__device__ __forceinline__ f32x4_t mfma(F16, u32x4_t a, u32x4_t b, f32x4_t c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a),
-                                                __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x4_t mfma(BF16, u32x4_t a, u32x4_t b, f32x4_t c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
-                                                 __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
-}
-
-__device__ __forceinline__ uint32_t pack2(F16, float a, float b) {
-  typedef _Float16 v2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, v2{_Float16(a), _Float16(b)});
-}
-__device__ __forceinline__ uint32_t pack2(BF16, float a, float b) {
-  typedef __bf16 v2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, v2{__bf16(a), __bf16(b)});
-}
-// What rounding a and b to the type leaves, in the type.
-__device__ __forceinline__ uint32_t pack2_rest(F16, float a, float b) {
-  return pack2(F16(), a - float(_Float16(a)), b - float(_Float16(b)));
-}
-__device__ __forceinline__ uint32_t pack2_rest(BF16, float a, float b) {
-  return pack2(BF16(), a - float(__bf16(a)), b - float(__bf16(b)));
-}
-
-// Two e4m3 codes (half `hi` of the word) as two 16-bit values, exactly.
-template <bool hi>
-__device__ __forceinline__ uint32_t widen2(F16, uint32_t w) {
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, hi));
-}
-template <bool hi>
-__device__ __forceinline__ uint32_t widen2(BF16, uint32_t w) {
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, hi));
-}
-
-__device__ __forceinline__ float word(uint32_t w) { return __builtin_bit_cast(float, w); }
-__device__ __forceinline__ uint32_t word(float v) { return __builtin_bit_cast(uint32_t, v); }
-
-// v of the lane's place in the lower and upper half of the wave, and in the
-// even and odd 16-lane groups.  (A bit cast takes no vector element itself: the
-// compiler would read element 0.)
-__device__ __forceinline__ float2 halves32(float v) {
-  auto a = __builtin_amdgcn_permlane32_swap(word(v), word(v), false, false);
-  const uint32_t x = a[0], y = a[1];
-  return float2{word(x), word(y)};
-}
-__device__ __forceinline__ float2 halves16(float v) {
-  auto a = __builtin_amdgcn_permlane16_swap(word(v), word(v), false, false);
-  const uint32_t x = a[0], y = a[1];
-  return float2{word(x), word(y)};
-}
 
 // Maximum and sum over the lanes 16, 32 and 48 on (a row's four lane groups).
 __device__ __forceinline__ float over_groups_max(float v) {
@@ -114,23 +54,6 @@ __device__ __forceinline__ float row16_top(float v) {
   return fmaxf(v, dpp_move<0x140, 0xF>(v));
 }
 
-// Types of the two products.
-template <class Act, class Cache>
-struct Kinds {
-  typedef F16 QK;
-  typedef F16 PV;
-};
-template <class Cache>
-struct Kinds<BF16, Cache> {
-  typedef BF16 QK;
-  typedef F16 PV;
-};
-template <>
-struct Kinds<BF16, BF16> {
-  typedef BF16 QK;
-  typedef BF16 PV;
-};
-
 // Components per lane of the value chunks that make up a head: 128, 64 or 32 wide.
 template <int D>
 struct Chunks {
@@ -141,20 +64,6 @@ struct Chunks {
   __host__ __device__ static constexpr int start(int c) { return c == 0 ? 0 : (D == 96 ? 64 : 128); }
   __host__ __device__ static constexpr int tile(int c) { return c == 0 ? 0 : per_lane(0); }
 };
-
-// First component of the 8 that lane group g feeds to step t of S^T = K Q^T.
-template <class Cache, int D>
-__device__ __forceinline__ constexpr int key_dim(int t, int g) {
-  if (__is_same(Cache, E4M3) && t < 2 * (D / 64)) return (t >> 1) * 64 + g * 16 + (t & 1) * 8;
-  return t * 32 + g * 8;
-}
-
-// A buffer resource that the compiler keeps in scalar registers.
-__device__ __forceinline__ rsrc_t uniform_rsrc(const void* base, uint32_t bytes) {
-  const uint64_t at = reinterpret_cast<uint64_t>(base);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(at)), hi = __builtin_amdgcn_readfirstlane(uint32_t(at >> 32));
-  return make_rsrc(reinterpret_cast<const void*>(uint64_t(hi) << 32 | lo), __builtin_amdgcn_readfirstlane(bytes));
-}
 
 // A 16-key run: where its keys and values start, and how many count.
 struct Run {
@@ -653,10 +562,6 @@ hipError_t launch_stream(const AttnArgs& a, const AttnPlan& plan, hipStream_t st
   }
   hipLaunchKernelGGL(fn, dim3(plan.splits, plan.steps * a.pages.kv_heads, a.pages.batch), dim3(64 * kWaves), lds,
                      stream, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || plan.splits == 1) return e;
-  const int64_t rows = int64_t(a.pages.tokens) * a.pages.q_heads;
-  hipLaunchKernelGGL((join_kernel<Act, D>), dim3(uint32_t((rows + 3) / 4)), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -679,6 +584,28 @@ hipError_t launch_dim(const AttnArgs& a, const AttnPlan& plan, hipStream_t strea
   }
 }
 
+hipError_t launch_streaming(const AttnArgs& a, const AttnPlan& plan, int act, int cache, hipStream_t stream) {
+  const bool narrow = cache == TQ2_TYPE_E4M3;
+  if (act == TQ2_TYPE_F32)
+    return narrow ? launch_dim<F32, E4M3>(a, plan, stream) : launch_dim<F32, F16>(a, plan, stream);
+  if (act == TQ2_TYPE_F16)
+    return narrow ? launch_dim<F16, E4M3>(a, plan, stream) : launch_dim<F16, F16>(a, plan, stream);
+  return narrow ? launch_dim<BF16, E4M3>(a, plan, stream) : launch_dim<BF16, BF16>(a, plan, stream);
+}
+
+template <class Act>
+hipError_t launch_join(const AttnArgs& a, hipStream_t stream) {
+  const dim3 grid(uint32_t((int64_t(a.pages.tokens) * a.pages.q_heads + 3) / 4));
+  switch (a.pages.head_dim) {
+    case 64: hipLaunchKernelGGL((join_kernel<Act, 64>), grid, dim3(256), 0, stream, a); break;
+    case 96: hipLaunchKernelGGL((join_kernel<Act, 96>), grid, dim3(256), 0, stream, a); break;
+    case 128: hipLaunchKernelGGL((join_kernel<Act, 128>), grid, dim3(256), 0, stream, a); break;
+    case 192: hipLaunchKernelGGL((join_kernel<Act, 192>), grid, dim3(256), 0, stream, a); break;
+    default: hipLaunchKernelGGL((join_kernel<Act, 256>), grid, dim3(256), 0, stream, a); break;
+  }
+  return hipGetLastError();
+}
+
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
@@ -688,34 +615,45 @@ AttnPlan plan_attention(const tq2_paged_attention_args& a) {
   AttnPlan plan;
   const int64_t max_q = a.max_q < 1 ? 1 : (a.max_q < c.tokens ? a.max_q : c.tokens);
   const int64_t rows = max_q * (c.q_heads / c.kv_heads);
+  plan.tiled = rows > 32;
   // Two row tiles share the loads of keys and values; wider heads' outputs leave no registers for a second.
   plan.row_tiles = rows <= 16 || c.head_dim > 128 ? 1 : 2;
-  const int64_t steps = up(rows, plan.row_tiles * 16);
-  const int64_t room = 65535 / c.kv_heads;                       // of the grid's second axis
+  const int64_t steps = up(rows, plan.tiled ? kTileRows : plan.row_tiles * 16);
+  const int64_t room = (plan.tiled ? int64_t(1) << 20 : 65535) / c.kv_heads;  // of the grid
   plan.steps = int32_t(steps < room ? steps : room);
-  // Parts: enough blocks for every CU several times over, but at least 128
-  // keys each, a tile for every wave.
   const int64_t span = a.window ? a.window + max_q + 31 : a.max_kv;   // that a sequence's rows see
   const int64_t keys = span < a.max_kv ? span : a.max_kv;
   const int64_t blocks = c.batch * c.kv_heads * plan.steps;
-  int64_t per = up(up(keys * blocks, 4096), 128) * 128;
-  if (per < 128) per = 128;
-  int64_t splits = keys < 1 ? 1 : up(keys, per);
+  int64_t per, splits;
+  if (plan.tiled) {
+    // Two blocks for each CU, of at least 512 keys.
+    splits = up(512, blocks);
+    per = up(up(keys, splits), 128) * 128;
+    if (per < 512) per = 512;
+  } else {
+    // Enough blocks for every CU several times over, but at least 128 keys each,
+    // a tile for every wave.
+    per = up(up(keys * blocks, 4096), 128) * 128;
+    if (per < 128) per = 128;
+  }
+  splits = keys < 1 ? 1 : up(keys, per);
   if (splits > 512) splits = 512;
   plan.splits = int32_t(splits);
   plan.split_keys = int32_t(per);
+  const int64_t most = (int64_t(1) << 31) - 1;                   // blocks of the tiled form
+  while (plan.tiled && plan.steps > 1 && c.batch * c.kv_heads * plan.steps * splits > most) plan.steps /= 2;
   plan.workspace = splits == 1 ? 0 : size_t(c.tokens) * size_t(c.q_heads) * size_t(splits) * size_t(c.head_dim + 4) * 4;
   return plan;
 }
 
 hipError_t launch_paged_attention(const AttnArgs& a, const AttnPlan& plan, int act, int cache,
                                   hipStream_t stream) {
-  const bool narrow = cache == TQ2_TYPE_E4M3;
-  if (act == TQ2_TYPE_F32)
-    return narrow ? launch_dim<F32, E4M3>(a, plan, stream) : launch_dim<F32, F16>(a, plan, stream);
-  if (act == TQ2_TYPE_F16)
-    return narrow ? launch_dim<F16, E4M3>(a, plan, stream) : launch_dim<F16, F16>(a, plan, stream);
-  return narrow ? launch_dim<BF16, E4M3>(a, plan, stream) : launch_dim<BF16, BF16>(a, plan, stream);
+  const hipError_t e = plan.tiled ? launch_attention_tiles(a, plan, act, cache, stream)
+                                  : launch_streaming(a, plan, act, cache, stream);
+  if (e != hipSuccess || plan.splits == 1) return e;
+  if (act == TQ2_TYPE_F32) return launch_join<F32>(a, stream);
+  if (act == TQ2_TYPE_F16) return launch_join<F16>(a, stream);
+  return launch_join<BF16>(a, stream);
 }
 
 }  // namespace tq2

@@ -106,6 +106,16 @@ def test_chunks(attn, act, cache, dim):
     check(attn, c, "%s %s %d" % (act, cache, dim))
 
 
+@pytest.mark.parametrize("act,cache", PAIRS)
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_prompts(attn, act, cache, dim):
+    """Several blocks of rows, several parts of the keys, tiles of keys that end early and pages longer than a run."""
+    c = make(dim + 1, act, cache, q_len=(513, 0, 1, 65, 300), kv_len=(1213, 20, 700, 65, 333), dim=dim, heads=(3, 1),
+             page=32)
+    check(attn, c, "%s %s %d" % (act, cache, dim))
+    check(attn, c, "window %s %s %d" % (act, cache, dim), window=130)
+
+
 @pytest.mark.parametrize("heads", [(1, 1), (16, 16), (32, 2), (24, 4), (40, 8), (5, 1)])
 @pytest.mark.parametrize("q_len", [1, 3, 70])
 def test_head_counts(attn, heads, q_len):
