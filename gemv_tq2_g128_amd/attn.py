@@ -15,7 +15,7 @@ import struct
 
 import torch
 
-from .tq2 import _check, _launch, lib
+from .tq2 import _check, _launch_on, lib
 
 EXPORTED_SYMBOLS = ("tq2_kv_append", "tq2_paged_attention", "tq2_paged_attention_workspace_bytes")
 HEAD_DIMS = (64, 96, 128, 192, 256)
@@ -155,7 +155,7 @@ def kv_append(k, v, k_cache, v_cache, kv_len, table, q=None, q_out=None, cu_q=No
         _plain(dev, freqs, torch.float64, half, "freqs"),
         _plain(dev, positions, torch.int32, axes * tokens, "positions"), 2 * half, axes, *cuts, int(interleaved),
         _plain(dev, q_norm, torch.float32, dim, "q_norm"), _plain(dev, k_norm, torch.float32, dim, "k_norm"), eps)
-    _check(_launch(k.device, kv_append_ptr, args), "kv_append")
+    _check(_launch_on(dev, kv_append_ptr, args), "kv_append")
     return q_out
 
 
@@ -190,5 +190,5 @@ def paged_attention(q, k_cache, v_cache, kv_len, table, cu_q=None, max_q=None, m
     need = paged_attention_workspace_bytes_ptr(cache + _ATTENTION.pack(*sizes, 0, 0))
     workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
     args = cache + _ATTENTION.pack(*sizes, workspace.data_ptr() if need else 0, need)
-    _check(_launch(q.device, paged_attention_ptr, args), "paged_attention")
+    _check(_launch_on(dev, paged_attention_ptr, args), "paged_attention")
     return out

@@ -75,44 +75,52 @@ struct Run {
 template <int D, int MT>
 constexpr int kMinWaves = D * MT <= 128 ? 2 : 1;
 
+// LDS of a block: q in operand order during the loop, then every wave's output,
+// maximum and sum of each row (rows are four floats apart, so that 16 rows' words lie
+// in 16 bank groups).
+template <class Act, int D, int MT, int W>
+struct StreamLds {
+  static constexpr size_t q = size_t(__is_same(Act, F32) ? 2 : 1) * MT * (D / 32) * 1024;
+  static constexpr int row = D + 4;
+  static constexpr size_t states = size_t(W) * MT * 16 * row * 4;
+  static constexpr size_t bytes = q > states ? q : states;
+};
+
 template <class Act, class Cache, int D, int MT, int W>
 __global__ __launch_bounds__(64 * W, (kMinWaves<D, MT>)) void stream_kernel(AttnArgs a) {
   typedef typename Kinds<Act, Cache>::QK QK;
   typedef typename Kinds<Act, Cache>::PV PV;
   typedef typename Act::elem act_t;
   typedef typename Cache::elem cache_t;
-  constexpr bool kSplitQ = __is_same(Act, F32);
-  // Probabilities in two parts: where 16 bits of them would show in the output.
-  constexpr bool kSplitP = __is_same(Act, F32);
-  constexpr float kLift = __is_same(PV, F16) ? 14.f : 0.f;      // log2: keeps small probabilities normal
+  constexpr bool kSplit = __is_same(Act, F32);                   // q and probabilities in two parts
+  constexpr float kLift = __is_same(PV, F16) ? 14.f : 0.f;       // log2: keeps small probabilities normal
   constexpr int kSize = int(sizeof(cache_t));
   constexpr int kSteps = D / 32;
   constexpr int kTiles = D / 16;
-  constexpr int kRegs = MT * kTiles * 4;
+  constexpr int kState = StreamLds<Act, D, MT, W>::row;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   u32x4_t* qf = reinterpret_cast<u32x4_t*>(smem);                // [part][MT][step][64]
-  float* join = reinterpret_cast<float*>(smem);                  // after the loop
+  float* states = reinterpret_cast<float*>(smem);                // [wave][row]: output; maximum, sum
   __shared__ float back[MT * 16];                                // power of two of each row of q
 
   const Pages& p = a.pages;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
-  const int group = p.q_heads / p.kv_heads;
+  const uint32_t group = a.group;
   const int head = blockIdx.y % p.kv_heads;
   const int split = blockIdx.x;
   const int b = blockIdx.z;
   const Seq s = sequence(p, b);
-  const int64_t rows = int64_t(s.q_len) * group;
+  const uint32_t rows = uint32_t(s.q_len) * group;               // below 2^31
   const Parts parts = parts_of(s, a.window, a.splits, a.split_keys);
   if (split >= parts.count) return;
+  const int start = parts.base + split * parts.per;
+  const int part_end = s.keys - start < parts.per ? s.keys : start + parts.per;
 
-  for (int64_t row0 = int64_t(blockIdx.y / p.kv_heads) * (MT * 16); row0 < rows;
-       row0 += int64_t(gridDim.y / p.kv_heads) * (MT * 16)) {
+  for (uint32_t row0 = blockIdx.y / p.kv_heads * (MT * 16); row0 < rows; row0 += gridDim.y / p.kv_heads * (MT * 16)) {
     // Keys of this part that any of the rows sees.
-    const int last = int((row0 + MT * 16 < rows ? row0 + MT * 16 : rows) - 1 - row0);
-    const int place_lo = s.first + int(row0 / group), place_hi = s.first + int((row0 + last) / group);
-    const int start = parts.base + split * parts.per;
-    const int part_end = s.keys - start < parts.per ? s.keys : start + parts.per;
+    const uint32_t live_rows = rows - row0 < MT * 16 ? rows - row0 : MT * 16;
+    const int place_lo = s.first + int(row0 / group), place_hi = s.first + int((row0 + live_rows - 1) / group);
     const int hi = place_hi + 1 < part_end ? place_hi + 1 : part_end;
     int lo = start;
     if (a.window) {
@@ -120,70 +128,35 @@ __global__ __launch_bounds__(64 * W, (kMinWaves<D, MT>)) void stream_kernel(Attn
       if (edge > lo) lo = edge < part_end ? int(edge) & ~31 : part_end;
     }
 
-    // q into LDS in operand order, 16 lanes for each row.
-    __syncthreads();
-    for (int r = wave * 4 + g4; r < MT * 16; r += W * 4) {
-      const int64_t row = row0 + r;
-      const bool live = row < rows;
+    // q: 16 lanes for each row, 8 components each.
+    constexpr int kUnits = (D / 8 + 15) / 16, kPasses = (MT * 4 + W - 1) / W;
+    f32x4_t qx[kPasses][kUnits][2];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const uint32_t r = (i * W + wave) * 4 + g4;
+      const bool live = r < live_rows;
+      const uint32_t row = row0 + r, token = row / group;
       const act_t* src = static_cast<const act_t*>(a.q) +
-                         (live ? (s.q0 + row / group) * a.q_token + (head * group + row % group) * a.q_head : 0);
-      constexpr int kUnits = (D / 8 + 15) / 16;
-      f32x4_t x[kUnits][2];
-      float top = 0.f;
+                         (live ? int64_t(s.q0 + token) * a.q_token + (head * group + row - token * group) * a.q_head : 0);
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int u = r16 + 16 * i;
-        x[i][0] = x[i][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < kUnits; ++j) {
+        const int u = r16 + 16 * j;
+        qx[i][j][0] = qx[i][j][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         if (live && u < D / 8) {
-          x[i][0] = load4(Act(), src + u * 8);
-          x[i][1] = load4(Act(), src + u * 8 + 4);
+          qx[i][j][0] = load4(Act(), src + u * 8);
+          qx[i][j][1] = load4(Act(), src + u * 8 + 4);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(x[i][0][j]), fabsf(x[i][1][j])));
-      }
-      int up = 0;
-      if constexpr (kSplitQ) {
-        // 2^13 <= |q| 2^up < 2^14: high parts normal, low parts down to 2^-39 of the largest.
-        top = row16_top(top);
-        const int e = int((__builtin_bit_cast(uint32_t, top) >> 23) & 255) - 127;
-        up = top > 0.f ? min(13 - e, 126) : 0;
-      }
-      if (r16 == 0) back[r] = __builtin_ldexpf(1.f, -up);
-      const float lift = __builtin_ldexpf(1.f, up);
-      const int mt = r >> 4, rr = r & 15;
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int u = r16 + 16 * i;
-        if (u >= D / 8) continue;
-        const bool pairs = __is_same(Cache, E4M3) && u < 8 * (D / 64);
-        const int t = pairs ? 2 * (u / 8) + (u & 1) : u / 4;
-        const int g = pairs ? (u % 8) / 2 : u % 4;
-        const f32x4_t y = x[i][0] * lift, z = x[i][1] * lift;
-        qf[(mt * kSteps + t) * 64 + g * 16 + rr] =
-            u32x4_t{pack2(QK(), y[0], y[1]), pack2(QK(), y[2], y[3]), pack2(QK(), z[0], z[1]), pack2(QK(), z[2], z[3])};
-        if constexpr (kSplitQ)
-          qf[((MT + mt) * kSteps + t) * 64 + g * 16 + rr] =
-              u32x4_t{pack2_rest(QK(), y[0], y[1]), pack2_rest(QK(), y[2], y[3]),
-                      pack2_rest(QK(), z[0], z[1]), pack2_rest(QK(), z[2], z[3])};
       }
     }
-    __syncthreads();
 
     float scale[MT], m[MT], sum[MT];
-    int place[MT];
     f32x4_t o[MT][kTiles];
+    int place[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const int64_t row = row0 + mt * 16 + r16;
+      const uint32_t row = row0 + mt * 16 + r16;
       place[mt] = row < rows ? s.first + int(row / group) : -1;
-      scale[mt] = a.scale * back[mt * 16 + r16];
-      if constexpr (kSize == 1) scale[mt] *= a.k_scale[head];
-      m[mt] = kNone;
-      sum[mt] = 0.f;
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i) o[mt][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
-
     const int all = hi > lo ? (hi - lo + 31) >> 5 : 0;           // tiles of 32 keys
     const int mine = wave < all ? (all - wave + W - 1) / W : 0;
     const cache_t* kbase = static_cast<const cache_t*>(a.k_cache) + head * p.k_head;
@@ -275,7 +248,11 @@ __global__ __launch_bounds__(64 * W, (kMinWaves<D, MT>)) void stream_kernel(Attn
       return run[0].count == 16 && run[1].count == 16 && key0 + 31 <= place_lo &&
              (a.window == 0 || int64_t(key0) > int64_t(place_hi) - a.window);
     };
-    // Zeros for the values that are not finite; whether the wave has any.
+    // Zeros for the values that are not finite; whether the wave has any.  Adding one
+    // to an exponent of all ones reaches the sign bit, and no other does.
+    constexpr uint32_t kTop = kSize == 1 ? 0x7F7F7F7Fu : (__is_same(Cache, F16) ? 0x7C007C00u : 0x7F807F80u);
+    constexpr uint32_t kOne = kSize == 1 ? 0x01010101u : (__is_same(Cache, F16) ? 0x04000400u : 0x00800080u);
+    constexpr uint32_t kSign = kSize == 1 ? 0x80808080u : 0x80008000u;
     auto tame_values = [&]() {
       uint32_t any = 0;
 #pragma unroll
@@ -283,17 +260,18 @@ __global__ __launch_bounds__(64 * W, (kMinWaves<D, MT>)) void stream_kernel(Attn
 #pragma unroll
         for (int k = 0; k < 8; ++k)
 #pragma unroll
-          for (int e = 0; e < (Chunks<D>::per_lane(c) * kSize + 3) / 4; ++e) {
-            constexpr uint32_t top = kSize == 1 ? 0x7Fu : (__is_same(Cache, F16) ? 0x7C00u : 0x7F80u);
-            constexpr uint32_t whole = kSize == 1 ? 0xFFu : 0xFFFFu;
+          for (int e = 0; e < (Chunks<D>::per_lane(c) * kSize + 3) / 4; ++e) any |= (vf[c][k][e] & kTop) + kOne;
+      if (__builtin_expect(__ballot((any & kSign) != 0) == 0, 1)) return false;
 #pragma unroll
-            for (int bit = 0; bit < 32; bit += 8 * kSize)
-              if ((vf[c][k][e] >> bit & top) == top) {
-                any = 1;
-                vf[c][k][e] &= ~(whole << bit);
-              }
+      for (int c = 0; c < Chunks<D>::count; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int e = 0; e < (Chunks<D>::per_lane(c) * kSize + 3) / 4; ++e) {
+            const uint32_t odd = ((vf[c][k][e] & kTop) + kOne) & kSign;        // top bit of each such value
+            vf[c][k][e] &= ~(odd | (odd - (odd >> (kSize == 1 ? 7 : 15))));
           }
-      return __ballot(any != 0) != 0;
+      return true;
     };
     // What tame_values left out, added where a row sees it.
     auto add_wild = [&](int key0, const Run& run) {
@@ -328,6 +306,53 @@ __global__ __launch_bounds__(64 * W, (kMinWaves<D, MT>)) void stream_kernel(Attn
       load_k(run);
       load_v(run);
     }
+    __syncthreads();                                             // the last rows are done with LDS
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const uint32_t r = (i * W + wave) * 4 + g4;
+      float lift = 1.f;
+      if constexpr (kSplit) {
+        // 2^13 <= |q| 2^up < 2^14: high parts normal, low parts down to 2^-39 of the largest.
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(qx[i][j][0][k]), fabsf(qx[i][j][1][k])));
+        top = row16_top(top);
+        const int e = int((word(top) >> 23) & 255) - 127;
+        const int up = top > 0.f ? min(13 - e, 126) : 0;
+        lift = __builtin_ldexpf(1.f, up);
+        if (r16 == 0 && r < MT * 16) back[r] = __builtin_ldexpf(1.f, -up);
+      }
+      const int mt = r >> 4, rr = r & 15;
+#pragma unroll
+      for (int j = 0; j < kUnits; ++j) {
+        const int u = r16 + 16 * j;
+        if (u >= D / 8 || r >= MT * 16) continue;
+        const bool pairs = kSize == 1 && u < 8 * (D / 64);
+        const int t = pairs ? 2 * (u / 8) + (u & 1) : u / 4;
+        const int g = pairs ? (u % 8) / 2 : u % 4;
+        const f32x4_t y = qx[i][j][0] * lift, z = qx[i][j][1] * lift;
+        qf[(mt * kSteps + t) * 64 + g * 16 + rr] =
+            u32x4_t{pack2(QK(), y[0], y[1]), pack2(QK(), y[2], y[3]), pack2(QK(), z[0], z[1]), pack2(QK(), z[2], z[3])};
+        if constexpr (kSplit)
+          qf[((MT + mt) * kSteps + t) * 64 + g * 16 + rr] =
+              u32x4_t{pack2_rest(QK(), y[0], y[1]), pack2_rest(QK(), y[2], y[3]),
+                      pack2_rest(QK(), z[0], z[1]), pack2_rest(QK(), z[2], z[3])};
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      scale[mt] = a.scale;
+      if constexpr (kSplit) scale[mt] *= back[mt * 16 + r16];
+      if constexpr (kSize == 1) scale[mt] *= a.k_scale[head];
+      m[mt] = kNone;
+      sum[mt] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) o[mt][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+
     bool wild = false;
     for (int j = 0; j < mine; ++j) {
       const int key0 = lo + (j * W + wave) * 32;
@@ -342,7 +367,7 @@ __global__ __launch_bounds__(64 * W, (kMinWaves<D, MT>)) void stream_kernel(Attn
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             sc[mt][h] = mfma(QK(), k, qf[(mt * kSteps + t) * 64 + lane], sc[mt][h]);
-            if constexpr (kSplitQ)
+            if constexpr (kSplit)
               sc[mt][h] = mfma(QK(), k, qf[((MT + mt) * kSteps + t) * 64 + lane], sc[mt][h]);
           }
         }
@@ -378,7 +403,7 @@ __global__ __launch_bounds__(64 * W, (kMinWaves<D, MT>)) void stream_kernel(Attn
         }
         sum[mt] = sum[mt] * shrink + total;
         pf[mt] = u32x4_t{pack2(PV(), x[0], x[1]), pack2(PV(), x[2], x[3]), pack2(PV(), x[4], x[5]), pack2(PV(), x[6], x[7])};
-        if constexpr (kSplitP)
+        if constexpr (kSplit)
           pl[mt] = u32x4_t{pack2_rest(PV(), x[0], x[1]), pack2_rest(PV(), x[2], x[3]),
                            pack2_rest(PV(), x[4], x[5]), pack2_rest(PV(), x[6], x[7])};
 #pragma unroll
@@ -403,7 +428,7 @@ __global__ __launch_bounds__(64 * W, (kMinWaves<D, MT>)) void stream_kernel(Attn
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
               o[mt][tile] = mfma(PV(), v, pf[mt], o[mt][tile]);
-              if constexpr (kSplitP) o[mt][tile] = mfma(PV(), v, pl[mt], o[mt][tile]);
+              if constexpr (kSplit) o[mt][tile] = mfma(PV(), v, pl[mt], o[mt][tile]);
             }
           }
         }
@@ -415,7 +440,7 @@ __global__ __launch_bounds__(64 * W, (kMinWaves<D, MT>)) void stream_kernel(Attn
     }
 
     // Rare: once more over the tiles whose rows differ in what they see.
-    if (wild) {
+    if (__builtin_expect(wild, 0)) {
       for (int j = 0; j < mine; ++j) {
         runs(j, run);
         const int key0 = lo + (j * W + wave) * 32;
@@ -425,142 +450,147 @@ __global__ __launch_bounds__(64 * W, (kMinWaves<D, MT>)) void stream_kernel(Attn
       }
     }
 
-    // Join the waves: the upper half leaves its state, the lower half takes it in.
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) sum[mt] = over_groups_sum(sum[mt]);
-#pragma unroll
-    for (int live = W / 2; live > 0; live >>= 1) {
-      __syncthreads();                                           // q and the last states are done with
-      if (wave >= live && wave < 2 * live) {
-        float* to = join + size_t(wave - live) * (kRegs + 2 * MT) * 64 + lane;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-          for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) to[((mt * kTiles + i) * 4 + r) * 64] = o[mt][i][r];
-          to[(kRegs + 2 * mt) * 64] = m[mt];
-          to[(kRegs + 2 * mt + 1) * 64] = sum[mt];
-        }
-      }
-      __syncthreads();
-      if (wave < live) {
-        const float* from = join + size_t(wave) * (kRegs + 2 * MT) * 64 + lane;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const float m2 = from[(kRegs + 2 * mt) * 64], s2 = from[(kRegs + 2 * mt + 1) * 64];
-          const float top = fmaxf(m[mt], m2), base = top == kNone ? 0.f : top;
-          const float f1 = __builtin_amdgcn_exp2f(m[mt] - base), f2 = __builtin_amdgcn_exp2f(m2 - base);
-          m[mt] = top;
-          sum[mt] = sum[mt] * f1 + s2 * f2;
-#pragma unroll
-          for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              o[mt][i][r] = o[mt][i][r] * f1 + from[((mt * kTiles + i) * 4 + r) * 64] * f2;
-        }
-      }
-    }
-    if (wave != 0) continue;
-    // Lane (r16, g4) holds row r16 and, of chunk c, components start + (4 g4 + r) n + 0 .. n - 1.
+    // Join the waves.  Lane (r16, g4) holds row r16 and, of chunk c, components
+    // start + (4 g4 + r) n + 0 .. n - 1.
+    __syncthreads();                                             // q is done with
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const int64_t row = row0 + mt * 16 + r16;
-      if (row >= rows) continue;
-      const int64_t token = s.q0 + row / group;
-      const int qh = head * group + int(row % group);
-      const float vs = kSize == 1 ? a.v_scale[head] : 1.f;
-      const float f = a.splits > 1 ? 1.f : (sum[mt] > 0.f || sum[mt] != sum[mt] ? vs / sum[mt] : 0.f);
-      float* part = a.part + ((token * p.q_heads + qh) * a.splits + split) * (D + 4);
-      act_t* dst = static_cast<act_t*>(a.out) + token * a.o_token + qh * a.o_head;
+      sum[mt] = over_groups_sum(sum[mt]);
+      if (uint32_t(mt * 16 + r16) >= live_rows) continue;
+      float* to = states + (wave * (MT * 16) + mt * 16 + r16) * kState;
 #pragma unroll
       for (int c = 0; c < Chunks<D>::count; ++c) {
+        constexpr int kLeast = 2;
         const int n = Chunks<D>::per_lane(c);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int at = Chunks<D>::start(c) + (4 * g4 + r) * n;
-          if (n >= 4) {
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int i = 0; i < n; i += 4) {
-              const int t0 = Chunks<D>::tile(c) + i;
-              const f32x4_t y = f32x4_t{o[mt][t0][r], o[mt][t0 + 1][r], o[mt][t0 + 2][r], o[mt][t0 + 3][r]} * f;
-              if (a.splits > 1) store4(F32(), part + 4 + at + i, y);
-              else store4(Act(), dst + at + i, y);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < n; ++i) {
-              const float y = o[mt][Chunks<D>::tile(c) + i][r] * f;
-              if (a.splits > 1) part[4 + at + i] = y;
-              else dst[at + i] = act_t(y);
-            }
+          for (int i = 0; i < n; i += n < 4 ? kLeast : 4) {
+            const int t = Chunks<D>::tile(c) + i, at = Chunks<D>::start(c) + (4 * g4 + r) * n + i;
+            if (n >= 4)
+              *reinterpret_cast<f32x4_t*>(to + at) =
+                  f32x4_t{o[mt][t][r], o[mt][t + 1][r], o[mt][t + (n < 4 ? 0 : 2)][r], o[mt][t + (n < 4 ? 0 : 3)][r]};
+            else
+              *reinterpret_cast<float2*>(to + at) = float2{o[mt][t][r], o[mt][t + 1][r]};
           }
-        }
       }
-      if (a.splits > 1 && g4 == 0) {
-        part[0] = m[mt];
-        part[1] = sum[mt];
+      if (g4 == 0) {
+        to[D] = m[mt];
+        to[D + 1] = sum[mt];
+      }
+    }
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < live_rows * (D / 4); i += 64 * W) {
+      const uint32_t r = i / (D / 4), c = i % (D / 4) * 4;
+      const float* from = states + r * kState;
+      float top = kNone, all = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) top = fmaxf(top, from[w * (MT * 16) * kState + D]);
+      const float base = top == kNone ? 0.f : top;
+      f32x4_t y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float* at = from + w * (MT * 16) * kState;
+        const float f = __builtin_amdgcn_exp2f(at[D] - base);    // 0 where the wave had no key for the row
+        all += at[D + 1] * f;
+        y += *reinterpret_cast<const f32x4_t*>(at + c) * f;
+      }
+      const uint32_t row = row0 + r, token = row / group;
+      const int qh = head * group + (row - token * group);
+      const int64_t at = s.q0 + token;
+      if (a.splits > 1) {
+        float* part = a.part + ((at * p.q_heads + qh) * a.splits + split) * (D + 4);
+        store4(F32(), part + 4 + c, y);
+        if (c == 0) {
+          part[0] = top;
+          part[1] = all;
+        }
+      } else {
+        const float vs = kSize == 1 ? a.v_scale[head] : 1.f;
+        const float f = all > 0.f || all != all ? vs / all : 0.f;
+        store4(Act(), static_cast<act_t*>(a.out) + at * a.o_token + qh * a.o_head + c, y * f);
       }
     }
   }
 }
 
-// Join the parts of a row: one wave for each new token and head.
-template <class Act, int D>
+// Join the parts of a row (a new token and head).  G groups of L lanes, four components
+// to a lane, take every G-th part; then their states meet in LDS.
+template <class Act, int D, int G>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
+  constexpr int L = D <= 64 ? 16 : (D <= 128 ? 32 : 64);
+  constexpr int kRows = 256 / (L * G);
+  __shared__ float states[G > 1 ? G : 1][D + 4];
   const Pages& p = a.pages;
-  const int lane = threadIdx.x & 63;
-  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (row >= int64_t(p.tokens) * p.q_heads) return;
-  const int token = int(row / p.q_heads), qh = int(row % p.q_heads);
-  const int b = owner(p, token);
-  if (b >= p.batch) return;
-  const Seq s = sequence(p, b);
-  if (token < s.q0 || token >= s.q0 + s.q_len) return;
-  const int parts = parts_of(s, a.window, a.splits, a.split_keys).count;
-  const float* part = a.part + row * a.splits * (D + 4);
-  float m = kNone;
-  for (int i = lane; i < parts; i += 64) m = fmaxf(m, part[size_t(i) * (D + 4)]);
+  const int lane = threadIdx.x % L, g = threadIdx.x / L % G;
+  const uint32_t row = blockIdx.x * kRows + threadIdx.x / (L * G);
+  const int token = int(row / uint32_t(p.q_heads)), qh = int(row % uint32_t(p.q_heads));
+  int b = 0, parts = 0;
+  constexpr int kPerWave = G == 1 ? 64 / L : 1;                  // rows of a wave
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-  const float base = m == kNone ? 0.f : m;
-  constexpr int kPer = (D + 63) / 64;
-  float sum = 0.f, o[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) o[i] = 0.f;
-  for (int i = 0; i < parts; ++i) {
-    const float* at = part + size_t(i) * (D + 4);
-    const float f = __builtin_amdgcn_exp2f(at[0] - base);
-    // A part in which this row sees no key has nothing to add, whatever it holds.
-    if (at[0] == kNone) continue;
-    sum += at[1] * f;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (lane + 64 * j < D) o[j] += at[4 + lane + 64 * j] * f;
+  for (int i = 0; i < kPerWave; ++i) {
+    const int t = __builtin_amdgcn_readlane(token, i * L);
+    const int of = t < p.tokens ? owner(p, t) : p.batch;
+    if (kPerWave == 1 || int(threadIdx.x & 63) / L == i) b = of;
   }
-  const float vs = a.v_scale ? a.v_scale[qh / (p.q_heads / p.kv_heads)] : 1.f;
+  bool live = token < p.tokens && b < p.batch;
+  if (live) {
+    const Seq s = sequence(p, b);
+    live = token >= s.q0 && token < s.q0 + s.q_len;
+    parts = live ? parts_of(s, a.window, a.splits, a.split_keys).count : 0;
+  }
+  const float* part = a.part + int64_t(row) * a.splits * (D + 4);
+  const int c = lane * 4;
+  float m = kNone;
+#pragma unroll 4
+  for (int i = g; i < parts; i += G) m = fmaxf(m, part[i * (D + 4)]);
+  float base = m == kNone ? 0.f : m;
+  float sum = 0.f;
+  f32x4_t y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int i = g; i < parts; i += G) {
+    const float* at = part + i * (D + 4);
+    const float f = __builtin_amdgcn_exp2f(at[0] - base);        // 0 for a part with no key for the row
+    sum += at[1] * f;
+    if (c < D) y += load4(F32(), at + 4 + c) * f;
+  }
+  if constexpr (G > 1) {
+    if (c < D) *reinterpret_cast<f32x4_t*>(&states[g][c]) = y;
+    if (lane == 0) {
+      states[g][D] = m;
+      states[g][D + 1] = sum;
+    }
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int i = 0; i < G; ++i) m = fmaxf(m, states[i][D]);
+    base = m == kNone ? 0.f : m;
+    sum = 0.f;
+    y = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const float f = __builtin_amdgcn_exp2f(states[i][D] - base);
+      sum += states[i][D + 1] * f;
+      if (c < D) y += *reinterpret_cast<const f32x4_t*>(&states[i][c]) * f;
+    }
+  }
+  if (!live || c >= D) return;
+  const float vs = a.v_scale ? a.v_scale[qh / int(a.group)] : 1.f;
   const float f = sum > 0.f || sum != sum ? vs / sum : 0.f;
   typedef typename Act::elem act_t;
-  act_t* dst = static_cast<act_t*>(a.out) + token * a.o_token + qh * a.o_head;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (lane + 64 * j < D) dst[lane + 64 * j] = act_t(o[j] * f);
+  store4(Act(), static_cast<act_t*>(a.out) + int64_t(token) * a.o_token + qh * a.o_head + c, y * f);
 }
 
-constexpr int kWaves = 4;
-
-template <class Act, class Cache, int D, int MT>
+template <class Act, class Cache, int D, int MT, int W>
 hipError_t launch_stream(const AttnArgs& a, const AttnPlan& plan, hipStream_t stream) {
-  constexpr size_t q_bytes = size_t(__is_same(Act, F32) ? 2 : 1) * MT * (D / 32) * 1024;
-  constexpr size_t join_bytes = size_t(kWaves / 2) * (MT * (D / 16) * 4 + 2 * MT) * 256;
-  constexpr size_t lds = q_bytes > join_bytes ? q_bytes : join_bytes;
-  auto fn = stream_kernel<Act, Cache, D, MT, kWaves>;
+  constexpr size_t lds = StreamLds<Act, D, MT, W>::bytes;
+  auto fn = stream_kernel<Act, Cache, D, MT, W>;
   if (lds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(fn, dim3(plan.splits, plan.steps * a.pages.kv_heads, a.pages.batch), dim3(64 * kWaves), lds,
+  hipLaunchKernelGGL(fn, dim3(plan.splits, plan.steps * a.pages.kv_heads, a.pages.batch), dim3(64 * W), lds,
                      stream, a);
   return hipGetLastError();
 }
@@ -568,9 +598,9 @@ hipError_t launch_stream(const AttnArgs& a, const AttnPlan& plan, hipStream_t st
 template <class Act, class Cache, int D>
 hipError_t launch_rows(const AttnArgs& a, const AttnPlan& plan, hipStream_t stream) {
   if constexpr (D <= 128) {
-    if (plan.row_tiles == 2) return launch_stream<Act, Cache, D, 2>(a, plan, stream);
+    if (plan.row_tiles == 2) return launch_stream<Act, Cache, D, 2, 4>(a, plan, stream);
   }
-  return launch_stream<Act, Cache, D, 1>(a, plan, stream);
+  return launch_stream<Act, Cache, D, 1, 4>(a, plan, stream);
 }
 
 template <class Act, class Cache>
@@ -593,17 +623,28 @@ hipError_t launch_streaming(const AttnArgs& a, const AttnPlan& plan, int act, in
   return narrow ? launch_dim<BF16, E4M3>(a, plan, stream) : launch_dim<BF16, BF16>(a, plan, stream);
 }
 
-template <class Act>
+template <class Act, int D>
 hipError_t launch_join(const AttnArgs& a, hipStream_t stream) {
-  const dim3 grid(uint32_t((int64_t(a.pages.tokens) * a.pages.q_heads + 3) / 4));
-  switch (a.pages.head_dim) {
-    case 64: hipLaunchKernelGGL((join_kernel<Act, 64>), grid, dim3(256), 0, stream, a); break;
-    case 96: hipLaunchKernelGGL((join_kernel<Act, 96>), grid, dim3(256), 0, stream, a); break;
-    case 128: hipLaunchKernelGGL((join_kernel<Act, 128>), grid, dim3(256), 0, stream, a); break;
-    case 192: hipLaunchKernelGGL((join_kernel<Act, 192>), grid, dim3(256), 0, stream, a); break;
-    default: hipLaunchKernelGGL((join_kernel<Act, 256>), grid, dim3(256), 0, stream, a); break;
-  }
+  constexpr int L = D <= 64 ? 16 : (D <= 128 ? 32 : 64);
+  const int64_t rows = int64_t(a.pages.tokens) * a.pages.q_heads;
+  // A whole block for each row once there are parts for all of it.
+  if (a.splits > 8)
+    hipLaunchKernelGGL((join_kernel<Act, D, 256 / L>), dim3(uint32_t(rows)), dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((join_kernel<Act, D, 1>), dim3(uint32_t((rows + 256 / L - 1) / (256 / L))), dim3(256), 0,
+                       stream, a);
   return hipGetLastError();
+}
+
+template <class Act>
+hipError_t launch_join_dim(const AttnArgs& a, hipStream_t stream) {
+  switch (a.pages.head_dim) {
+    case 64: return launch_join<Act, 64>(a, stream);
+    case 96: return launch_join<Act, 96>(a, stream);
+    case 128: return launch_join<Act, 128>(a, stream);
+    case 192: return launch_join<Act, 192>(a, stream);
+    default: return launch_join<Act, 256>(a, stream);
+  }
 }
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -651,9 +692,9 @@ hipError_t launch_paged_attention(const AttnArgs& a, const AttnPlan& plan, int a
   const hipError_t e = plan.tiled ? launch_attention_tiles(a, plan, act, cache, stream)
                                   : launch_streaming(a, plan, act, cache, stream);
   if (e != hipSuccess || plan.splits == 1) return e;
-  if (act == TQ2_TYPE_F32) return launch_join<F32>(a, stream);
-  if (act == TQ2_TYPE_F16) return launch_join<F16>(a, stream);
-  return launch_join<BF16>(a, stream);
+  if (act == TQ2_TYPE_F32) return launch_join_dim<F32>(a, stream);
+  if (act == TQ2_TYPE_F16) return launch_join_dim<F16>(a, stream);
+  return launch_join_dim<BF16>(a, stream);
 }
 
 }  // namespace tq2

@@ -44,6 +44,7 @@ struct AttnArgs {
   float* part;                           // partial outputs, nullptr if splits == 1
   float scale;                           // of the scores, times log2 e
   int32_t window;                        // 0: none
+  uint32_t group;                        // query heads of a key head
   int32_t splits;                        // parts of a sequence's keys
   int32_t split_keys;                    // least keys of a part, a multiple of 32
 };

@@ -32,14 +32,16 @@ namespace tq2 {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kRows = kTileRows;
-static_assert(kRows == 32 * kWaves, "32 rows a wave");
+static_assert(kTileRows == 32 * kWaves, "32 rows a wave");
 constexpr int kKeys = 64;                        // keys of a tile: one 16-key run per wave
 constexpr float kSlack = 8.f;                    // log2 of the growth that is left unscaled
+
+constexpr int kAhead = 4;                        // reads of keys in front of their matrix steps
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t* lds_s16x4_t;
 typedef __attribute__((address_space(3))) const u32x4_t* lds_u32x4_t;
+typedef __attribute__((address_space(3))) unsigned char* lds_byte_t;
 
 // Where 16-byte chunk c of row r of a tile lies: slot within the row.
 template <int D>
@@ -58,20 +60,30 @@ __device__ __forceinline__ void load_to_lds(rsrc_t r, uint32_t off, uint32_t at)
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                ::"s"(at), "v"(off), "s"(r) : "memory");
 }
+// The larger of two; NaN if one is (fmaxf would first quiet its operands).
+__device__ __forceinline__ float largest(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // Every load to LDS of this wave is in, then every wave's.
 __device__ __forceinline__ void tile_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-__device__ __forceinline__ u32x4_t lds_values(uint32_t at, int far) {
-  const s16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_s16x4_t(at));
-  const s16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_s16x4_t(at + far));
+// 16 bytes of a key at + off; four values of a component at + off and as many at
+// + off + far.
+__device__ __forceinline__ u32x4_t lds_keys(uint32_t at, int off) {
+  return *reinterpret_cast<lds_u32x4_t>(reinterpret_cast<lds_byte_t>(at) + off);
+}
+__device__ __forceinline__ u32x4_t lds_values(uint32_t at, int off, int far) {
+  const lds_byte_t from = reinterpret_cast<lds_byte_t>(at) + off;
+  const s16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4_t>(from));
+  const s16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4_t>(from + far));
   const u32x2_t u = __builtin_bit_cast(u32x2_t, x), v = __builtin_bit_cast(u32x2_t, y);
   return u32x4_t{u[0], u[1], v[0], v[1]};
 }
 
+// Waves per SIMD that the register budget aims at.
 template <class Act, int D>
-constexpr int kMinWaves = (D <= 64 || (D <= 128 && !__is_same(Act, F32))) ? 2 : 1;
+constexpr int kMinWaves = D <= 64 || (D <= 128 && !__is_same(Act, F32)) ? 2 : 1;
 
 template <class Act, class Cache, int D>
 __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(AttnArgs a, int steps) {
@@ -84,6 +96,7 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
   constexpr int kSize = int(sizeof(cache_t));
   constexpr int kSteps = D / 16;                                 // matrix steps of a score
   constexpr int kTiles = D / 32;                                 // 32-component tiles of the output
+  constexpr int kRows = kTileRows;
   constexpr int kRowBytes = 2 * D;
   constexpr int kTileBytes = kKeys * kRowBytes;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];  // K, K, V, V, flag
@@ -92,7 +105,7 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
   const Pages& p = a.pages;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r32 = lane & 31, h = lane >> 5;
-  const int group = p.q_heads / p.kv_heads;
+  const uint32_t group = a.group;
   // Key heads vary fastest: with 8 of them each XCD's cache holds one head.
   // Later tokens, which see more keys, come first.
   uint32_t id = blockIdx.x;
@@ -103,7 +116,7 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
   const int step = steps - 1 - int(id % steps);
   const int b = id / steps;
   const Seq s = sequence(p, b);
-  const int64_t rows = int64_t(s.q_len) * group;
+  const uint32_t rows = uint32_t(s.q_len) * group;               // below 2^31
   const Parts parts = parts_of(s, a.window, a.splits, a.split_keys);
   if (split >= parts.count) return;
 
@@ -112,7 +125,7 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
   const cache_t* vbase = static_cast<const cache_t*>(a.v_cache) + head * p.v_head;
   const uint32_t ktok = uint32_t(p.k_token) * kSize, vtok = uint32_t(p.v_token) * kSize;
 
-  for (int64_t row0 = int64_t(step) * kRows; row0 < rows; row0 += int64_t(steps) * kRows) {
+  for (uint32_t row0 = uint32_t(step) * kRows; row0 < rows; row0 += uint32_t(steps) * kRows) {
     const int last = int(row0 + kRows < rows ? kRows : rows - row0) - 1;
     const int block_hi = s.first + int((row0 + last) / group), block_lo = s.first + int(row0 / group);
     const int start = parts.base + split * parts.per;
@@ -126,60 +139,59 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
     const int tiles = hi > lo ? (hi - lo + kKeys - 1) / kKeys : 0;
 
     // The wave's rows, and q in operand order: components 16 t + 8 h + 0 .. 7 of row r32.
-    const int64_t row = row0 + wave * 32 + r32;
-    const bool live = row < rows;
-    const int64_t wave_row = row0 + wave * 32;
-    const int64_t wave_end = wave_row + 31 < rows ? wave_row + 31 : rows - 1;
+    const uint32_t wave_row = row0 + wave * 32;
+    const uint32_t wave_end = wave_row + 32 <= rows ? wave_row + 31 : rows - 1;
     const int place_lo = s.first + int(wave_row / group);
     const int place_hi = wave_row < rows ? s.first + int(wave_end / group) : -1;
+    const uint32_t row = wave_row + r32;
+    const bool live = row < rows;
     const int place = live ? s.first + int(row / group) : -1;
-    const int64_t below64 = a.window ? int64_t(place) - a.window : -1;
-    const int below = below64 < -1 ? -1 : int(below64);          // keys up to here are out of the window
-    u32x4_t q[kSteps], q2[kSplit ? kSteps : 1];
+    const int64_t token = s.q0 + row / group;
+    const int qh = head * group + row % group;
+    const int64_t out_of = a.window ? int64_t(place) - a.window : -1;
+    const int below = out_of < -1 ? -1 : int(out_of);            // keys up to here are out of the window
     float scale = a.scale;
     if constexpr (kSize == 1) scale *= a.k_scale[head];
-    {
-      const act_t* src = static_cast<const act_t*>(a.q) +
-                         (live ? (s.q0 + row / group) * a.q_token + (head * group + row % group) * a.q_head : 0) + 8 * h;
-      f32x4_t x[kSplit ? kSteps : 1][2];
-      float lift = 1.f;
-      if constexpr (kSplit) {
-        float top = 0.f;
-#pragma unroll
-        for (int t = 0; t < kSteps; ++t) {
-          x[t][0] = x[t][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-          if (live) {
-            x[t][0] = load4(Act(), src + t * 16);
-            x[t][1] = load4(Act(), src + t * 16 + 4);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(x[t][0][j]), fabsf(x[t][1][j])));
-        }
-        const float2 both = halves32(top);
-        top = fmaxf(both.x, both.y);
-        const int e = int((word(top) >> 23) & 255) - 127;
-        const int up = top > 0.f ? min(13 - e, 126) : 0;
-        lift = __builtin_ldexpf(1.f, up);
-        scale *= __builtin_ldexpf(1.f, -up);
-      }
+    u32x4_t q[kSteps], q2[kSplit ? kSteps : 1];
+    const act_t* src = static_cast<const act_t*>(a.q) + (live ? token * a.q_token + qh * a.q_head : 0) + 8 * h;
+    float lift = 1.f;
+    f32x4_t x[kSplit ? kSteps : 1][2];
+    if constexpr (kSplit) {
+      float top = 0.f;
 #pragma unroll
       for (int t = 0; t < kSteps; ++t) {
-        if constexpr (kSplit) {
-          const f32x4_t y = x[t][0] * lift, z = x[t][1] * lift;
-          q[t] = u32x4_t{pack2(QK(), y[0], y[1]), pack2(QK(), y[2], y[3]), pack2(QK(), z[0], z[1]), pack2(QK(), z[2], z[3])};
-          q2[t] = u32x4_t{pack2_rest(QK(), y[0], y[1]), pack2_rest(QK(), y[2], y[3]),
-                          pack2_rest(QK(), z[0], z[1]), pack2_rest(QK(), z[2], z[3])};
-        } else {
-          q[t] = live ? *reinterpret_cast<const u32x4_t*>(src + t * 16) : u32x4_t{0, 0, 0, 0};
+        x[t][0] = x[t][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        if (live) {
+          x[t][0] = load4(Act(), src + t * 16);
+          x[t][1] = load4(Act(), src + t * 16 + 4);
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(x[t][0][j]), fabsf(x[t][1][j])));
+      }
+      const float2 both = halves32(top);
+      top = fmaxf(both.x, both.y);
+      const int e = int((word(top) >> 23) & 255) - 127;
+      const int up = top > 0.f ? min(13 - e, 126) : 0;
+      lift = __builtin_ldexpf(1.f, up);
+      scale *= __builtin_ldexpf(1.f, -up);
+    }
+#pragma unroll
+    for (int t = 0; t < kSteps; ++t) {
+      if constexpr (kSplit) {
+        const f32x4_t y = x[t][0] * lift, z = x[t][1] * lift;
+        q[t] = u32x4_t{pack2(QK(), y[0], y[1]), pack2(QK(), y[2], y[3]), pack2(QK(), z[0], z[1]), pack2(QK(), z[2], z[3])};
+        q2[t] = u32x4_t{pack2_rest(QK(), y[0], y[1]), pack2_rest(QK(), y[2], y[3]),
+                        pack2_rest(QK(), z[0], z[1]), pack2_rest(QK(), z[2], z[3])};
+      } else {
+        q[t] = live ? *reinterpret_cast<const u32x4_t*>(src + t * 16) : u32x4_t{0, 0, 0, 0};
       }
     }
+    float m = kNone, sum = 0.f;
     f32x16_t o[kTiles];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
-    float m = kNone, sum = 0.f;
 
     // Loads of a tile: wave w fills the 16 rows of run w.
     int ids = -1;                                                // page of run `lane` of the next 16 tiles
@@ -241,19 +253,17 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
     };
     // Operand addresses in a tile.  Keys: chunk 2 t + h of row r32, whose low bits the
     // exclusive or turns; the others, and the second 32 rows, are constant offsets.
-    constexpr int kTurn = D == 96 ? 4 : 8;                       // chunks within one turn
-    auto key_at = [&](int t, int kt) -> uint32_t {
-      const int c = 2 * t + h;
-      return uint32_t(r32 * kRowBytes + (Place<D>::key(r32, c & (kTurn - 1)) + (2 * t & ~(kTurn - 1))) * 16 +
-                      kt * 32 * kRowBytes);
-    };
-    // Values: lane l16 of a 16-lane group reads 8 bytes of row 4 h + l16 / 4.
-    const int l16 = lane & 15, vrow = 4 * h + (l16 >> 2);
-    auto value_at = [&](int t, int dt) -> uint32_t {
-      const int pair = (dt * 2 + ((lane >> 4) & 1)) ^ Place<D>::value_turn(l16 >> 2);
-      return uint32_t((16 * t + vrow) * kRowBytes + pair * 32 + (l16 & 3) * 8);
-    };
-
+    // Values: lane l16 of a 16-lane group reads 8 bytes of row 4 h + l16 / 4, and so on.
+    constexpr int kTurn = D == 96 ? 4 : 8;                       // key chunks within one turn
+    constexpr int kPairs = D == 128 || D == 256 ? 2 : 1;         // value tiles within one turn
+    const int l16 = lane & 15;
+    uint32_t key_at[kTurn / 2], value_at[kPairs];
+#pragma unroll
+    for (int t = 0; t < kTurn / 2; ++t) key_at[t] = lds + r32 * kRowBytes + Place<D>::key(r32, 2 * t + h) * 16;
+#pragma unroll
+    for (int dt = 0; dt < kPairs; ++dt)
+      value_at[dt] = lds + 2 * kTileBytes + (4 * h + (l16 >> 2)) * kRowBytes + (l16 & 3) * 8 +
+                     ((dt * 2 + ((lane >> 4) & 1)) ^ Place<D>::value_turn(l16 >> 2)) * 32;
     // The wave's 16 rows of values: zeros for what is not finite, and the flag.
     auto tame = [&](int buf) {
       constexpr uint32_t kTop = __is_same(PV, F16) ? 0x7C00u : 0x7F80u;
@@ -311,19 +321,32 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
       const bool clean = gone == 0 && key0 + kKeys - 1 <= place_lo && key0 + kKeys <= hi &&
                          (a.window == 0 || int64_t(key0) > int64_t(place_hi) - a.window);
       if (some) {
-        const uint32_t at_k = lds + buf * kTileBytes, at_v = at_k + 2 * kTileBytes;
+        // Scores.  Reads of keys run kAhead in front of the matrix steps that take them.
         f32x16_t x[2];
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
+        for (int r = 0; r < 16; ++r) x[0][r] = x[1][r] = 0.f;
+        u32x4_t kf[2 * kSteps];
+        auto read_key = [&](int i) {                             // step i / 2 of the 32 keys i % 2
+          kf[i] = lds_keys(key_at[i / 2 % (kTurn / 2)] + buf * kTileBytes,
+                           (i & 1) * 32 * kRowBytes + i / 2 / (kTurn / 2) * kTurn * 16);
+        };
 #pragma unroll
-          for (int r = 0; r < 16; ++r) x[kt][r] = 0.f;
+        for (int i = 0; i < kAhead; ++i) read_key(i);
 #pragma unroll
-          for (int t = 0; t < kSteps; ++t) {
-            const u32x4_t k = *lds_u32x4_t(at_k + key_at(t, kt));
-            x[kt] = mfma(QK(), k, q[t], x[kt]);
-            if constexpr (kSplit) x[kt] = mfma(QK(), k, q2[t], x[kt]);
-          }
+        for (int i = 0; i < 2 * kSteps; ++i) {
+          if (i + kAhead < 2 * kSteps) read_key(i + kAhead);
+          __builtin_amdgcn_sched_barrier(0);
+          x[i & 1] = mfma(QK(), kf[i], q[i / 2], x[i & 1]);
+          if constexpr (kSplit) x[i & 1] = mfma(QK(), kf[i], q2[i / 2], x[i & 1]);
+          __builtin_amdgcn_sched_barrier(0);
         }
+        u32x4_t vf[2][kTiles];
+        auto read_value = [&](int t, int dt) {
+          vf[t & 1][dt] = lds_values(value_at[dt % kPairs] + buf * kTileBytes,
+                                     16 * t * kRowBytes + dt / kPairs * kPairs * 64, 8 * kRowBytes);
+        };
+#pragma unroll
+        for (int dt = 0; dt < kTiles; ++dt) read_value(0, dt);
         if (!clean) {
           const int upto = (place < hi ? place : hi - 1) - key0 - 4 * h, over = below - key0 - 4 * h;
 #pragma unroll
@@ -338,9 +361,9 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) top = fmaxf(top, x[kt][r]);
+          for (int r = 0; r < 16; r += 2) top = largest(largest(x[kt][r], x[kt][r + 1]), top);
         const float2 both = halves32(top);
-        top = fmaxf(both.x, both.y) * scale;
+        top = largest(both.x, both.y) * scale;
         if (__ballot(top > m + kSlack) != 0) {
           const float grown = fmaxf(m, top);
           const float shrink = grown == kNone ? 1.f : __builtin_amdgcn_exp2f(m - grown);
@@ -350,32 +373,32 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
           for (int i = 0; i < kTiles; ++i) o[i] = o[i] * shrink;
         }
         const float base = m == kNone ? 0.f : m - kLift;
+        // Probabilities, two at a time: those of the second 32 keys, and the reads of the
+        // next step's values, lie between the matrix steps of the first 32.
         u32x4_t pf[4], pl[kSplit ? 4 : 1];
-        float total = 0.f;
+        auto probabilities = [&](int kt, int i) {
+          const float u = __builtin_amdgcn_exp2f(__builtin_fmaf(x[kt][2 * i], scale, -base));
+          const float v = __builtin_amdgcn_exp2f(__builtin_fmaf(x[kt][2 * i + 1], scale, -base));
+          sum += u + v;
+          pf[kt * 2 + (i >> 2)][i & 3] = pack2(PV(), u, v);
+          if constexpr (kSplit) pl[kt * 2 + (i >> 2)][i & 3] = pack2_rest(PV(), u, v);
+        };
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            x[kt][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[kt][r], scale, -base));
-            total += x[kt][r];
-          }
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              pf[kt * 2 + t][e] = pack2(PV(), x[kt][8 * t + 2 * e], x[kt][8 * t + 2 * e + 1]);
-              if constexpr (kSplit) pl[kt * 2 + t][e] = pack2_rest(PV(), x[kt][8 * t + 2 * e], x[kt][8 * t + 2 * e + 1]);
-            }
-          }
-        }
-        sum += total;
+        for (int i = 0; i < 8; ++i) probabilities(0, i);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
           for (int dt = 0; dt < kTiles; ++dt) {
-            const u32x4_t v = lds_values(at_v + value_at(t, dt), 8 * kRowBytes);
-            o[dt] = mfma(PV(), v, pf[t], o[dt]);
-            if constexpr (kSplit) o[dt] = mfma(PV(), v, pl[t], o[dt]);
+            const int slot = t * kTiles + dt;
+            if (t < 3) read_value(t + 1, dt);
+            __builtin_amdgcn_sched_barrier(0);
+            o[dt] = mfma(PV(), vf[t & 1][dt], pf[t], o[dt]);
+            if constexpr (kSplit) o[dt] = mfma(PV(), vf[t & 1][dt], pl[t], o[dt]);
+            if (t < 2) {
+#pragma unroll
+              for (int i = slot * 8 / (2 * kTiles); i < (slot + 1) * 8 / (2 * kTiles); ++i) probabilities(1, i);
+            }
+            __builtin_amdgcn_sched_barrier(0);
           }
       }
       gone = next_gone;
@@ -390,7 +413,6 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
         if (page < 0) continue;
         const int in = key & ((1 << p.page_shift) - 1);
         const cache_t* v = vbase + page * p.v_page + in * p.v_token + 4 * h;
-        const bool sees = key <= place && key > below;
 #pragma unroll
         for (int dt = 0; dt < kTiles; ++dt)
 #pragma unroll
@@ -400,18 +422,17 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
             float x;
             if constexpr (kSize == 1) x = __builtin_amdgcn_cvt_f32_fp8(w, 0);
             else x = float(w);
-            if (sees && !(fabsf(x) < __builtin_inff())) o[dt][r] += x;
+            if (fabsf(x) < __builtin_inff()) continue;
+            if (key <= place && key > below) o[dt][r] += x;
           }
       }
     }
     // Lane (r32, h) holds components 32 dt + 8 i + 4 h + 0 .. 3 of row r32.
     const float2 both = halves32(sum);
-    sum = both.x + both.y;
+    const float all = both.x + both.y;
     if (!live) continue;
-    const int64_t token = s.q0 + row / group;
-    const int qh = head * group + int(row % group);
     const float vs = kSize == 1 ? a.v_scale[head] : 1.f;
-    const float f = a.splits > 1 ? 1.f : (sum > 0.f || sum != sum ? vs / sum : 0.f);
+    const float f = a.splits > 1 ? 1.f : (all > 0.f || all != all ? vs / all : 0.f);
     float* part = a.part + ((token * p.q_heads + qh) * a.splits + split) * (D + 4);
     act_t* dst = static_cast<act_t*>(a.out) + token * a.o_token + qh * a.o_head;
 #pragma unroll
@@ -425,7 +446,7 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
       }
     if (a.splits > 1 && h == 0) {
       part[0] = m;
-      part[1] = sum;
+      part[1] = all;
     }
   }
 }

@@ -117,6 +117,8 @@ int check_attention_sizes(const tq2_paged_attention_args& a) {
   if (!size_ok(a.max_q, 0, kMaxDim) || !size_ok(a.max_kv, 0, (int64_t(1) << 31) - 1) ||
       !size_ok(a.window, 0, (int64_t(1) << 31) - 1))
     return TQ2_ERR_INVALID;
+  // Rows and heads are counted in 31 bits.
+  if (a.cache.tokens * a.cache.q_heads >= (int64_t(1) << 31) - 4096) return TQ2_ERR_INVALID;
   return TQ2_OK;
 }
 
@@ -280,6 +282,7 @@ int tq2_paged_attention(const tq2_paged_attention_args* args, void* stream) {
   g.part = plan.splits > 1 ? static_cast<float*>(a.workspace) : nullptr;
   g.scale = float(a.scale * 1.4426950408889634);                 // scores as exponents of two
   g.window = int32_t(a.window);
+  g.group = uint32_t(c.q_heads / c.kv_heads);
   g.splits = plan.splits;
   g.split_keys = plan.split_keys;
   return launch_status(tq2::launch_paged_attention(g, plan, int(c.act_type), int(c.cache_type),

@@ -132,7 +132,8 @@ size_t tq2_paged_attention_workspace_bytes(const tq2_paged_attention_args* args)
  * are and the probabilities are rounded to the cache's type (binary16 for
  * e4m3), half a step each.
  * Activations, caches and workspace: 16-byte aligned, strides multiples of 16
- * bytes; 16 tokens of a page lie within 2^31 bytes.  The workspace's content
+ * bytes; 16 tokens of a page lie within 2^31 bytes; tokens * q_heads is below
+ * 2^31 - 4096.  The workspace's content
  * needs no preparation and means nothing afterwards.
  * tokens == 0 is a no-op.  Errors: INVALID (null pointer, size out of range, a
  * workspace that is too small, types or head_dim not listed), SHAPE, ALIGN,
