@@ -6,6 +6,7 @@ Usage: ``python -m gemv_tq2_g128_amd.build`` or ``build()`` from Python.
 import os
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -39,17 +40,39 @@ def hipcc_path():
 
 PROBE_LIB_NAME = "libtq2_probe.so"
 PROBE_SOURCES = ["tq2_probe.hip"]
+BINDING_NAME = "_binding.so"
+BINDING_SOURCE = "tq2_binding.cpp"
 
 
 def build(verbose: bool = False) -> str:
     """Compile every HIP source into ``libtq2.so`` (and the benchmark's
-    reference kernels into ``libtq2_probe.so``); returns the library path."""
+    reference kernels into ``libtq2_probe.so``, the tensor marshalling into
+    ``_binding.so``); returns the library path."""
     _compile(PROBE_SOURCES, PROBE_LIB_NAME, verbose)
-    return _compile(SOURCES, LIB_NAME, verbose)
+    lib = _compile(SOURCES, LIB_NAME, verbose)
+    _compile_binding(verbose)
+    return lib
+
+
+def _compile_binding(verbose):
+    """The host-only Python module, against PyTorch's headers and libtq2.so."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    out = os.path.join(PKG_DIR, BINDING_NAME)
+    tmp = out + ".tmp%d" % os.getpid()
+    includes = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+          "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+          *("-I" + i for i in includes), os.path.join(CSRC, BINDING_SOURCE), "-o", tmp,
+          "-L" + PKG_DIR, "-l:" + LIB_NAME, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu",
+          "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"], verbose)
+    os.replace(tmp, out)
 
 
 def _run(cmd, verbose):
-    """Run one hipcc command; its output, or RuntimeError."""
+    """Run one compiler command; its output, or RuntimeError."""
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
@@ -57,7 +80,7 @@ def _run(cmd, verbose):
     noise = "is not a recognized feature for this target"
     msg = "\n".join(l for l in res.stdout.splitlines() if noise not in l)
     if res.returncode != 0:
-        raise RuntimeError("hipcc failed (%d):\n%s" % (res.returncode, msg))
+        raise RuntimeError("%s failed (%d):\n%s" % (os.path.basename(cmd[0]), res.returncode, msg))
     if verbose and msg.strip():
         print(msg)
 
@@ -74,7 +97,7 @@ def _compile(sources, lib_name, verbose):
         with ThreadPoolExecutor(max_workers=min(len(cmds), 8)) as pool:
             list(pool.map(lambda c: _run(c, verbose), cmds))
         try:
-            _run([hipcc_path(), *HIPCC_FLAGS, *objs, "-o", tmp], verbose)
+            _run([hipcc_path(), *HIPCC_FLAGS, "-Wl,-soname," + lib_name, *objs, "-o", tmp], verbose)
         except RuntimeError:
             if os.path.exists(tmp):
                 os.remove(tmp)

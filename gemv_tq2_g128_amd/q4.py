@@ -2,14 +2,16 @@
 
 A weight of [n, k] is two plain tensors: ``codes`` uint8 [n, k / 2] (weight 2j
 of a row in the low nibble of byte j) and ``scales`` float16 [n, k / group]; its
-value is (code - 8) * scale.  Argument marshalling only, as in ``tq2``.
+value is (code - 8) * scale.  Argument marshalling only, as in ``tq2``: tensors go
+through the compiled module ``_binding`` (csrc/tq2_binding.cpp).
 """
 
 from __future__ import annotations
 
 import ctypes
 
-from .tq2 import _check, _launch, _one_device, _require, _torch, lib
+from .tq2 import _result, lib     # first: it loads torch and libtq2, which _binding needs
+from . import _binding            # isort: skip
 
 EXPORTED_SYMBOLS = ("tq2_q4_gemv",)
 MAX_M = 16                      # TQ2_Q4_MAX_M (include/tq2_q4.h)
@@ -30,25 +32,4 @@ def gemv(codes, scales, x, residual=None, out=None):
     """out[m, n] = residual[m, n] + sum_k x[m, k] * (code[n, k] - 8) * scale[n, k // group];
     x is f32 [m, k] (or [k], for an out of [n]) with m <= MAX_M.  The group is
     k / scales.shape[1]: 32, 64 or 128."""
-    torch = _torch()
-    if codes.dim() != 2 or scales.dim() != 2 or x.dim() not in (1, 2):
-        raise ValueError("codes and scales must be matrices, x a matrix or a vector")
-    n, k = codes.shape[0], 2 * codes.shape[1]
-    m = x.shape[0] if x.dim() == 2 else 1
-    per_row = scales.shape[1]
-    if per_row == 0 or k % per_row or k // per_row not in GROUPS:
-        raise ValueError("scales must be [n, k / group] with a group of 32, 64 or 128")
-    _require(codes, torch.uint8, n * k // 2, "codes")
-    _require(scales, torch.float16, n * per_row, "scales")
-    _require(x, torch.float32, m * k, "x")
-    if residual is not None:
-        _require(residual, torch.float32, m * n, "residual")
-    if out is None:
-        out = torch.empty(x.shape[:-1] + (n,), dtype=torch.float32, device=x.device)
-    _require(out, torch.float32, m * n, "out")
-    dev = _one_device(("x", x), ("codes", codes), ("scales", scales), ("residual", residual),
-                      ("out", out))
-    _check(_launch(dev, gemv_ptr, codes.data_ptr(), scales.data_ptr(), x.data_ptr(),
-                   residual.data_ptr() if residual is not None else 0, out.data_ptr(), m, n, k,
-                   k // per_row), "q4_gemv")
-    return out
+    return _result(_binding.q4_gemv(codes, scales, x, residual, out), "q4_gemv")

@@ -311,18 +311,16 @@ def _one_device(*named):
 def _launch(dev, fn, *args):
     """Run a raw call with `dev` as the current device and its current stream:
     a launch on the null stream goes to the current device."""
-    return _launch_on(dev.index, fn, *args)
-
-
-def _launch_on(index: int, fn, *args):
-    """_launch for a device index.  Entering a device context and making a
-    Stream object take longer than a small kernel, so neither happens where the
-    device is the current one already."""
     torch = _torch()
-    if torch.cuda.current_device() == index:
-        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    with torch.cuda.device(index):
-        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(dev):
+        return fn(*args, _stream_handle(dev))
+
+
+def _result(value, where: str):
+    """What a call of the compiled module gives: its output, or a status."""
+    if type(value) is int:
+        raise TQ2Error(value, where)
+    return value
 
 
 def reformat_aos_to_soa(aos, n: int, k: int, out=None, fmt: str = "tq2"):
