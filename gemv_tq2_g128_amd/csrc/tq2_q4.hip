@@ -37,6 +37,7 @@ namespace {
 
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 8;
@@ -85,8 +86,8 @@ template <int MT>
 struct Shape {
   __host__ __device__ static int columns(int m) { return MT == 8 ? 2 * m : 32; }
   __host__ __device__ static size_t x_bytes(int kb, int m) { return size_t(kb) * 256 * columns(m); }
-  __host__ __device__ static size_t bytes(int kb, int m, int rt) {
-    return x_bytes(kb, m) + size_t(kb) * 64 + size_t(2) * kWaves * rt * MT * 64;
+  __host__ __device__ static size_t bytes(int kb, int m, bool sums) {
+    return x_bytes(kb, m) + size_t(kb) * 64 + (sums ? size_t(2) * kWaves * MT * 64 : 0);
   }
 };
 
@@ -130,42 +131,117 @@ __device__ __forceinline__ void stage_x(const float* __restrict__ x, int m, int6
   }
 }
 
-template <int G>
+// N consecutive 128-wide blocks of K of the lane's row: its 16 bytes of each, and the
+// scales of all, which lie side by side.  (One load of up to 16 bytes for several
+// blocks' scales: a load of its own for each cost 19 of 66 us at 131072 x 4096.)
+template <int G, int N>
 struct Codes {
-  u32x4_t w;
-  uint32_t d[G == 32 ? 2 : 1];                  // binary16 scales of the lane's row, 128 / G of them
+  u32x4_t w[N];
+  uint32_t d[N * (64 / G) + (G == 128 ? N / 2 + 1 : 0)];  // words of scales; G == 128: from bit `down` on
+  uint32_t down;
 };
 
-template <int G>
-__device__ __forceinline__ void load_codes(const uint8_t* __restrict__ codes,
-                                           const uint16_t* __restrict__ scales, uint32_t code_off,
-                                           uint32_t scale_off, Codes<G>& c) {
-  c.w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(codes + code_off));
+// Past the range of either resource: zeros.
+constexpr uint32_t kNowhere = 0x80000000u;
+
+// codes and scales of 16 rows or, at the end, fewer.  The word that holds the last scale
+// is in range as a whole.
+struct Rows {
+  rsrc_t codes, scales;
+};
+__device__ __forceinline__ Rows rows_at(const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scales,
+                                        int64_t row0, uint32_t live, int64_t row_bytes, int64_t row_scales) {
+  return Rows{make_rsrc(codes + row0 * row_bytes, live * uint32_t(row_bytes)),
+              make_rsrc(scales + row0 * row_scales, (live * uint32_t(row_scales) * 2 + 3) & ~3u)};
+}
+
+// Every load is issued, whether the row or the block of K exists or not (those give
+// zeros): behind a branch the count of loads in flight would be unknown, and each wait
+// would take in the loads of the next step too.  kb: the first block, of which the lane
+// takes the bytes at code_off + 64 kb; `count` of them exist.
+template <int G, int N>
+__device__ __forceinline__ void load_codes(const Rows& rows, uint32_t code_off, uint32_t scale_off, uint32_t kb,
+                                           int count, Codes<G, N>& c) {
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    c.w[j] = __builtin_amdgcn_raw_buffer_load_b128(rows.codes, j < count ? code_off + (kb + j) * 64 : kNowhere, 0,
+                                                   kStreamOnce);
+  const uint32_t at = count > 0 ? scale_off + kb * (256 / G) : kNowhere;
   if constexpr (G == 128) {
-    c.d[0] = scales[scale_off];
-  } else if constexpr (G == 64) {
-    c.d[0] = *reinterpret_cast<const uint32_t*>(scales + scale_off);
+    // Two-byte scales may start in the middle of a word, where buffer loads do not: the
+    // words around them, moved down by half a word there.
+    uint32_t w[N / 2 + 1];
+    if constexpr (N == 4) {
+      const u32x2_t d = __builtin_amdgcn_raw_buffer_load_b64(rows.scales, at & ~3u, 0, 0);
+      w[0] = d[0];
+      w[1] = d[1];
+    } else {
+      const u32x4_t d = __builtin_amdgcn_raw_buffer_load_b128(rows.scales, at & ~3u, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = d[i];
+    }
+    w[N / 2] = __builtin_amdgcn_raw_buffer_load_b32(rows.scales, (at & ~3u) + N * 2, 0, 0);
+    c.down = (at & 2) * 8;
+#pragma unroll
+    for (int i = 0; i <= N / 2; ++i) c.d[i] = w[i];
   } else {
-    const uint2 d = *reinterpret_cast<const uint2*>(scales + scale_off);
-    c.d[0] = d.x;
-    c.d[1] = d.y;
+#pragma unroll
+    for (int i = 0; i < N * (256 / G) / 16; ++i) {
+      const u32x4_t d = __builtin_amdgcn_raw_buffer_load_b128(rows.scales, at + i * 16, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c.d[4 * i + e] = d[e];
+    }
   }
 }
 
-template <int G>
-__device__ __forceinline__ float scale_of(const Codes<G>& c, int s) {
-  if constexpr (G == 128) return float(__builtin_bit_cast(_Float16, uint16_t(c.d[0])));
-  const int i = G == 64 ? s >> 1 : s;           // group of 32-wide step s
-  return float(__builtin_bit_cast(_Float16, uint16_t(c.d[i >> 1] >> (16 * (i & 1)))));
+// The scale of 32-wide step s of block j.
+template <int G, int N>
+__device__ __forceinline__ float scale_of(const Codes<G, N>& c, int j, int s) {
+  const int i = j * (128 / G) + s / (G / 32);
+  uint32_t w = c.d[i >> 1];
+  if constexpr (G == 128) w = __builtin_amdgcn_alignbit(c.d[(i >> 1) + 1], w, c.down);
+  return float(__builtin_bit_cast(_Float16, uint16_t(w >> (16 * (i & 1)))));
 }
 
-template <int G, int MT, int RT>
+// One 128-wide block of K (block j of c): the codes' four matrix steps against x, scaled
+// into acc (rows 4 g4 + r of x, weight row r16).
+template <int G, int MT, int N>
+__device__ __forceinline__ void multiply(Codes<G, N>& c, int j, const half8_t* __restrict__ a, const float4_t& back,
+                                         int cols, float (&acc)[4]) {
+  if constexpr (G != 128) transpose4(c.w[j]);
+  float4_t sum;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const half8_t a0 = a[size_t(s) * 4 * cols];
+    const half8_t b = decode8(c.w[j][s]);
+    const bool fresh = s % (G / 32) == 0;                 // a group's first step
+    const bool whole = (s + 1) % (G / 32) == 0;           // and its last
+    sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, b, fresh ? float4_t{0.f, 0.f, 0.f, 0.f} : sum, 0, 0, 0);
+    if constexpr (MT == 16)
+      sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[size_t(s) * 4 * cols + 16], b, sum, 0, 0, 0);
+    if (whole) {
+      const float d = scale_of<G, N>(c, j, s);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(d * back[r], sum[r], acc[r]);
+    }
+  }
+}
+
+// The column of the matrix operand x that the lane's row reads.
+template <int MT>
+__device__ __forceinline__ int operand_column(int r16, int m) {
+  if (MT == 8) return (r16 & 7) < m ? (r16 >> 3) * m + (r16 & 7) : 0;
+  return r16 < m ? r16 : 0;
+}
+
+// K split over the waves: one step of 16 weight rows at a time.
+template <int G, int MT>
 __global__ __launch_bounds__(kThreads, 2) void q4_kernel(
     const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scales,
     const float* __restrict__ x, const float* __restrict__ residual, float* __restrict__ out,
     int m, int n, int64_t k, int pass_kb) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
   const int cols = Shape<MT>::columns(m);
   half8_t* xf = reinterpret_cast<half8_t*>(smem);
@@ -173,8 +249,8 @@ __global__ __launch_bounds__(kThreads, 2) void q4_kernel(
   const int first = min(all_kb, pass_kb);
   float* xs = reinterpret_cast<float*>(smem + Shape<MT>::x_bytes(first, m));
   float* red = xs + first * 16;
-  const int col = MT == 8 ? ((r16 & 7) < m ? (r16 >> 3) * m + (r16 & 7) : 0) : (r16 < m ? r16 : 0);
-  const int steps = (n + RT * 16 - 1) / (RT * 16);
+  const int col = operand_column<MT>(r16, m);
+  const int steps = (n + 15) / 16;
   const int64_t row_bytes = k >> 1, row_scales = k / G;
 
   for (int pass = 0; pass < all_kb; pass += pass_kb) {
@@ -182,96 +258,56 @@ __global__ __launch_bounds__(kThreads, 2) void q4_kernel(
     const int nk = (kbs + kWaves - 1) / kWaves;           // <= kMaxKb
     const int kb0 = wave * nk;
     const int mine = max(0, min(nk, kbs - kb0));
-    Codes<G> c[2][kMaxKb][RT];
-    auto load = [&](int step, Codes<G> (&into)[kMaxKb][RT]) {
-      const int64_t row0 = int64_t(step) * (RT * 16);
-      const uint8_t* cb = codes + row0 * row_bytes;
-      const uint16_t* sb = scales + row0 * row_scales;
-#pragma unroll
-      for (int j = 0; j < kMaxKb; ++j) {
-        if (j >= mine) continue;
-        const uint32_t kb = uint32_t(pass + kb0 + j);
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          // Rows past the end read the last row; their sums are not stored.
-          const uint32_t r = uint32_t(min(int64_t(t * 16 + r16), n - 1 - row0));
-          load_codes<G>(cb, sb, r * uint32_t(row_bytes) + kb * 64 + g4 * 16,
-                        r * uint32_t(row_scales) + kb * (128 / G), into[j][t]);
-        }
-      }
+    Codes<G, kMaxKb> c[2];
+    auto load = [&](int step, Codes<G, kMaxKb>& into) {
+      const int64_t row0 = int64_t(step < steps ? step : 0) * 16;
+      const uint32_t live = step < steps ? uint32_t(min(int64_t(16), n - row0)) : 0;
+      load_codes<G, kMaxKb>(rows_at(codes, scales, row0, live, row_bytes, row_scales),
+                            r16 * uint32_t(row_bytes) + g4 * 16, r16 * uint32_t(row_scales) * 2,
+                            uint32_t(pass + kb0), mine, into);
+    };
+    // The thread's output of a step, and what is added to it; loaded in front of the
+    // next step's codes, so that its wait does not take them in.
+    const int on = threadIdx.x & 15, om = threadIdx.x >> 4;
+    const float* add = pass > 0 ? out : residual;
+    auto load_add = [&](int step) {
+      const int64_t row = int64_t(step) * 16 + on;
+      return add && om < m && row < n ? add[size_t(om) * size_t(n) + size_t(row)] : 0.f;
     };
     int parity = 0;
-    auto compute = [&](int step, Codes<G> (&from)[kMaxKb][RT]) {
-      float acc[RT][4];
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[t][r] = 0.f;
+    auto compute = [&](int step, Codes<G, kMaxKb>& from, float added) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < kMaxKb; ++j) {
         if (j >= mine) continue;
         const int kb = kb0 + j;
-        const float4_t back = *reinterpret_cast<const float4_t*>(xs + kb * 16 + g4 * 4);
-        if constexpr (G != 128) {
-#pragma unroll
-          for (int t = 0; t < RT; ++t) transpose4(from[j][t].w);
-        }
-        float4_t sum[RT];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const half8_t* a = xf + (size_t(kb * 4 + s) * 4 + g4) * cols + col;
-          const half8_t a0 = a[0];
-          half8_t a1;
-          if constexpr (MT == 16) a1 = a[16];
-          const bool fresh = s % (G / 32) == 0;           // a group's first step
-          const bool whole = (s + 1) % (G / 32) == 0;     // and its last
-#pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            const half8_t b = decode8(from[j][t].w[s]);
-            sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                a0, b, fresh ? float4_t{0.f, 0.f, 0.f, 0.f} : sum[t], 0, 0, 0);
-            if constexpr (MT == 16)
-              sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, b, sum[t], 0, 0, 0);
-            if (whole) {
-              const float d = scale_of<G>(from[j][t], s);
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                acc[t][r] = __builtin_fmaf(d * back[r], sum[t][r], acc[t][r]);
-            }
-          }
-        }
+        multiply<G, MT, kMaxKb>(from, j, xf + (size_t(kb) * 16 + g4) * cols + col,
+                                *reinterpret_cast<const float4_t*>(xs + kb * 16 + g4 * 4), cols, acc);
       }
-      // Partial sums [wave][tile][row of x][weight row] of this step; lane
-      // groups 0 and 1 (MT == 8) or all four hold rows 4 g4 .. 4 g4 + 3.
-      float* buf = red + parity * (kWaves * RT * MT * 16);
+      // Partial sums [wave][row of x][weight row] of this step; lane groups 0 and 1
+      // (MT == 8) or all four hold rows 4 g4 .. 4 g4 + 3.
+      float* buf = red + parity * (kWaves * MT * 16);
       parity ^= 1;
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float v = acc[t][r];
-          if constexpr (MT == 8) v += __shfl_xor(v, 32);  // hi + lo
-          if (MT == 16 || g4 < 2) buf[((wave * RT + t) * MT + g4 * 4 + r) * 16 + r16] = v;
-        }
+      for (int r = 0; r < 4; ++r) {
+        float v = acc[r];
+        if constexpr (MT == 8) v += __shfl_xor(v, 32);    // hi + lo
+        if (MT == 16 || g4 < 2) buf[(wave * MT + g4 * 4 + r) * 16 + r16] = v;
       }
       __syncthreads();
       // A buffer is written again two steps on, behind the next step's barrier.
-      const int o = threadIdx.x, on = o & 15, om = (o >> 4) % MT, ot = (o >> 4) / MT;
-      const int64_t row = int64_t(step) * (RT * 16) + ot * 16 + on;
-      if (ot < RT && om < m && row < n) {
+      const int64_t row = int64_t(step) * 16 + on;
+      if (om < m && row < n) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) v += buf[((w * RT + ot) * MT + om) * 16 + on];
-        const size_t at = size_t(om) * size_t(n) + size_t(row);
-        if (pass > 0) v += out[at];
-        else if (residual) v += residual[at];
-        out[at] = v;
+        for (int w = 0; w < kWaves; ++w) v += buf[(w * MT + om) * 16 + on];
+        out[size_t(om) * size_t(n) + size_t(row)] = v + added;
       }
     };
 
     // The first step's codes are in flight while x is converted (the grid has no
-    // more blocks than steps).  Every wave
-    // takes part in each step's barrier: the walk is uniform over the block.
+    // more blocks than steps).  Every wave takes part in each step's barrier: the
+    // walk is uniform over the block.
     int step = blockIdx.x;
     load(step, c[0]);
     if (pass > 0) __syncthreads();                        // the last step has read x and red
@@ -279,26 +315,113 @@ __global__ __launch_bounds__(kThreads, 2) void q4_kernel(
     __syncthreads();
     const int hop = gridDim.x;
     while (step < steps) {
-      if (step + hop < steps) load(step + hop, c[1]);
-      compute(step, c[0]);
+      float added = load_add(step);
+      load(step + hop, c[1]);
+      compute(step, c[0], added);
       step += hop;
       if (step >= steps) break;
-      if (step + hop < steps) load(step + hop, c[0]);
-      compute(step, c[1]);
+      added = load_add(step);
+      load(step + hop, c[0]);
+      compute(step, c[1], added);
       step += hop;
     }
   }
 }
 
-template <int G, int MT, int RT>
+// Rows split over the waves: each walks over tiles of 16 weight rows and all of K by
+// itself, kFlight blocks of K ahead of its matrix steps, with no barrier.
+constexpr int kFlight = 8;
+
+template <int G, int MT>
+__global__ __launch_bounds__(kThreads, 2) void q4_tall_kernel(
+    const uint8_t* __restrict__ codes, const uint16_t* __restrict__ scales,
+    const float* __restrict__ x, const float* __restrict__ residual, float* __restrict__ out,
+    int m, int n, int64_t k, int pass_kb) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, g4 = lane >> 4;
+  const int cols = Shape<MT>::columns(m);
+  half8_t* xf = reinterpret_cast<half8_t*>(smem);
+  const int all_kb = int(k >> 7);
+  float* xs = reinterpret_cast<float*>(smem + Shape<MT>::x_bytes(min(all_kb, pass_kb), m));
+  const int col = operand_column<MT>(r16, m);
+  const int tiles = (n + 15) / 16, hop = gridDim.x * kWaves;
+  const int64_t row_bytes = k >> 1, row_scales = k / G;
+  const uint32_t row_code = r16 * uint32_t(row_bytes) + g4 * 16, row_scale = r16 * uint32_t(row_scales) * 2;
+
+  for (int pass = 0; pass < all_kb; pass += pass_kb) {
+    const int kbs = min(pass_kb, all_kb - pass);
+    const int rounds = (kbs + kFlight - 1) / kFlight;     // of a tile
+    const float* add = pass > 0 ? out : residual;
+    Codes<G, kFlight> c[2];
+    auto load = [&](int tile, int round, Codes<G, kFlight>& into) {
+      const int64_t row0 = int64_t(tile < tiles ? tile : 0) * 16;
+      const uint32_t live = tile < tiles ? uint32_t(min(int64_t(16), n - row0)) : 0;
+      load_codes<G, kFlight>(rows_at(codes, scales, row0, live, row_bytes, row_scales), row_code, row_scale,
+                             uint32_t(pass + round * kFlight), kbs - round * kFlight, into);
+    };
+    float acc[4], added[4];
+    auto compute = [&](int round, Codes<G, kFlight>& from) {
+#pragma unroll
+      for (int j = 0; j < kFlight; ++j) {
+        const int kb = round * kFlight + j;
+        if (kb >= kbs) continue;
+        multiply<G, MT, kFlight>(from, j, xf + (size_t(kb) * 16 + g4) * cols + col,
+                                 *reinterpret_cast<const float4_t*>(xs + kb * 16 + g4 * 4), cols, acc);
+      }
+    };
+    // Lane groups 0 and 1 (MT == 8) or all four hold rows 4 g4 + r of x.
+    auto begin = [&](int tile) {
+      const int64_t row = int64_t(tile) * 16 + r16;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        acc[r] = 0.f;
+        added[r] = add && g4 * 4 + r < m && row < n ? add[size_t(g4 * 4 + r) * size_t(n) + size_t(row)] : 0.f;
+      }
+    };
+    auto end = [&](int tile) {
+      const int64_t row = int64_t(tile) * 16 + r16;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float v = acc[r];
+        if constexpr (MT == 8) v += __shfl_xor(v, 32);    // hi + lo
+        if (g4 * 4 + r < m && row < n) out[size_t(g4 * 4 + r) * size_t(n) + size_t(row)] = v + added[r];
+      }
+    };
+
+    int tile = blockIdx.x * kWaves + wave, round = 0;
+    load(tile, 0, c[0]);
+    if (pass > 0) __syncthreads();                        // every wave has read x
+    stage_x<G, MT>(x, m, k, int64_t(pass) * 128, kbs, xf, xs);
+    __syncthreads();
+    auto walk = [&](Codes<G, kFlight>& now, Codes<G, kFlight>& then) {
+      const bool last = round + 1 == rounds;
+      const int next = last ? tile + hop : tile, next_round = last ? 0 : round + 1;
+      if (round == 0) begin(tile);
+      load(next, next_round, then);
+      compute(round, now);
+      if (last) end(tile);
+      tile = next;
+      round = next_round;
+    };
+    while (tile < tiles) {
+      walk(c[0], c[1]);
+      if (tile >= tiles) break;
+      walk(c[1], c[0]);
+    }
+  }
+}
+
+template <int G, int MT>
 hipError_t launch(const Q4Args& a, hipStream_t stream) {
   const int all_kb = int(a.k >> 7);
   const int pass_kb = MT == 8 ? kWaves * kMaxKb : kWaves * kMaxKb / 2;
-  const size_t lds = Shape<MT>::bytes(all_kb < pass_kb ? all_kb : pass_kb, int(a.m), RT);
-  const int steps = int((a.n + RT * 16 - 1) / (RT * 16));
+  const bool tall = a.n >= 16384;
+  const size_t lds = Shape<MT>::bytes(all_kb < pass_kb ? all_kb : pass_kb, int(a.m), !tall);
+  const int64_t tiles = (a.n + 15) / 16, steps = tall ? (tiles + kWaves - 1) / kWaves : tiles;
   const int per_cu = lds <= 80 * 1024 ? 2 : 1;
-  const int grid = steps < 256 * per_cu ? steps : 256 * per_cu;
-  auto fn = q4_kernel<G, MT, RT>;
+  const int grid = steps < 256 * per_cu ? int(steps) : 256 * per_cu;
+  auto fn = tall ? q4_tall_kernel<G, MT> : q4_kernel<G, MT>;
   if (lds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
@@ -311,11 +434,7 @@ hipError_t launch(const Q4Args& a, hipStream_t stream) {
 
 template <int G>
 hipError_t launch_group(const Q4Args& a, hipStream_t stream) {
-  if (a.m > 8) return launch<G, 16, 1>(a, stream);
-  // Two row tiles per step share the operand reads of x once every CU has
-  // work for them; below that one tile per step fills more CUs.
-  if (a.n >= 32 * 512) return launch<G, 8, 2>(a, stream);
-  return launch<G, 8, 1>(a, stream);
+  return a.m > 8 ? launch<G, 16>(a, stream) : launch<G, 8>(a, stream);
 }
 
 }  // namespace
