@@ -525,6 +525,29 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
   const int lane = threadIdx.x % L, g = threadIdx.x / L % G;
   const uint32_t row = blockIdx.x * kRows + threadIdx.x / (L * G);
   const int token = int(row / uint32_t(p.q_heads)), qh = int(row % uint32_t(p.q_heads));
+  const float* part = a.part + int64_t(row) * a.splits * (D + 4);
+  const int c = lane * 4;
+  // Parts are read kBatch at a time, the first ones before it is known how many the row
+  // has (the workspace holds a.splits of them).
+  constexpr int kBatch = 8;
+  float pm[kBatch], ps[kBatch];
+  f32x4_t py[kBatch];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * G;
+      pm[j] = kNone;
+      ps[j] = 0.f;
+      py[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      if (i < a.splits && token < p.tokens && c < D) {
+        const float* at = part + i * (D + 4);
+        pm[j] = at[0];
+        ps[j] = at[1];
+        py[j] = load4(F32(), at + 4 + c);
+      }
+    }
+  };
+  fetch(g);
   int b = 0, parts = 0;
   constexpr int kPerWave = G == 1 ? 64 / L : 1;                  // rows of a wave
 #pragma unroll
@@ -539,20 +562,26 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
     live = token >= s.q0 && token < s.q0 + s.q_len;
     parts = live ? parts_of(s, a.window, a.splits, a.split_keys).count : 0;
   }
-  const float* part = a.part + int64_t(row) * a.splits * (D + 4);
-  const int c = lane * 4;
-  float m = kNone;
-#pragma unroll 4
-  for (int i = g; i < parts; i += G) m = fmaxf(m, part[i * (D + 4)]);
-  float base = m == kNone ? 0.f : m;
-  float sum = 0.f;
+  float m = kNone, base = 0.f, sum = 0.f;
   f32x4_t y = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int i = g; i < parts; i += G) {
-    const float* at = part + i * (D + 4);
-    const float f = __builtin_amdgcn_exp2f(at[0] - base);        // 0 for a part with no key for the row
-    sum += at[1] * f;
-    if (c < D) y += load4(F32(), at + 4 + c) * f;
+  for (int i0 = g; i0 < parts; i0 += kBatch * G) {
+    if (i0 > g) fetch(i0);
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (i0 + j * G < parts) top = fmaxf(top, pm[j]);
+    base = top == kNone ? 0.f : top;
+    const float shrink = __builtin_amdgcn_exp2f(m - base);
+    m = top;
+    sum *= shrink;
+    y *= shrink;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (i0 + j * G >= parts) continue;
+      const float f = __builtin_amdgcn_exp2f(pm[j] - base);      // 0 for a part with no key for the row
+      sum += ps[j] * f;
+      y += py[j] * f;
+    }
   }
   if constexpr (G > 1) {
     if (c < D) *reinterpret_cast<f32x4_t*>(&states[g][c]) = y;
@@ -672,10 +701,24 @@ AttnPlan plan_attention(const tq2_paged_attention_args& a) {
     per = up(up(keys, splits), 128) * 128;
     if (per < 512) per = 512;
   } else {
-    // Enough blocks for every CU several times over, but at least 128 keys each,
-    // a tile for every wave.
-    per = up(up(keys * blocks, 4096), 128) * 128;
-    if (per < 128) per = 128;
+    // 1, 2, 4 or 8 tiles of 32 keys for each of a block's four waves, by the least time:
+    // two blocks fit on a CU, a block takes about 4.5 us to start and end and 1.4 us a
+    // tile, and joining parts takes 4 us and about 0.1 us a part (measured).  Longer
+    // parts leave CUs idle at the end of ragged batches: 4 sequences of up to 131,071
+    // tokens take 131 us with 1024 keys a part, 143 with 2048, 159 with 4096.
+    double least = 0.0;
+    per = 128;
+    for (int64_t tiles = 1; tiles <= 8; tiles *= 2) {
+      const int64_t parts = up(keys, 128 * tiles), rounds = up(blocks * (parts < 1 ? 1 : parts), 512);
+      const double time = double(rounds) * (4.5 + 1.4 * double(tiles)) + (parts > 1 ? 4.0 + 0.1 * double(parts) : 0.0);
+      if (tiles == 1 || time < least) {
+        least = time;
+        per = 128 * tiles;
+      }
+    }
+    // Sequences enough to fill the card by themselves, none so long that the others wait
+    // for it: nothing to join (64 of up to 8192 tokens: 239 us, 254 in parts of 1024).
+    if (blocks >= 512 && keys <= 8192) per = 8192;
   }
   splits = keys < 1 ? 1 : up(keys, per);
   if (splits > 512) splits = 512;
