@@ -166,7 +166,7 @@ int tq2_kv_append(const tq2_kv_append_args* args, void* stream) {
   }
   if (sum != a.rot / 2) return TQ2_ERR_INVALID;
   if (!(a.eps >= 0.0)) return TQ2_ERR_INVALID;
-  if (c.tokens == 0) return TQ2_OK;
+  if (c.tokens == 0 || c.batch == 0) return TQ2_OK;              // no row has a sequence
   st = check_cache_arrays(c);
   if (st != TQ2_OK) return st;
   if (!a.k || !a.v || (a.q != nullptr) != (a.q_out != nullptr) || (a.rot > 0 && !a.freqs))
@@ -229,7 +229,9 @@ int tq2_kv_append(const tq2_kv_append_args* args, void* stream) {
 }
 
 size_t tq2_paged_attention_workspace_bytes(const tq2_paged_attention_args* args) {
-  if (!args || check_attention_sizes(*args) != TQ2_OK || args->cache.tokens == 0) return 0;
+  if (!args || check_attention_sizes(*args) != TQ2_OK || args->cache.tokens == 0 ||
+      args->cache.batch == 0)
+    return 0;
   return tq2::plan_attention(*args).workspace;
 }
 
@@ -240,7 +242,7 @@ int tq2_paged_attention(const tq2_paged_attention_args* args, void* stream) {
   int st = check_attention_sizes(a);
   if (st != TQ2_OK) return st;
   if (!(a.scale > 0.0) || !(a.scale <= 3e38)) return TQ2_ERR_INVALID;
-  if (c.tokens == 0) return TQ2_OK;
+  if (c.tokens == 0 || c.batch == 0) return TQ2_OK;              // no row has a sequence
   st = check_cache_arrays(c);
   if (st != TQ2_OK) return st;
   if (!a.q || !a.out) return TQ2_ERR_INVALID;

@@ -96,7 +96,7 @@ typedef struct tq2_kv_append_args {
  * section i lies in); q goes to q_out, k and v to their place in the cache,
  * rounded once (e4m3: value / scale, clamped to +-448).
  * Activations and caches: 16-byte aligned, strides multiples of 16 bytes.
- * tokens == 0 is a no-op.  Errors: INVALID (null pointer, size out of range,
+ * tokens == 0 or batch == 0 is a no-op.  Errors: INVALID (null pointer, size out of range,
  * a pair of types or head_dim that is not listed, sections that do not sum to
  * rot / 2), SHAPE (page not a power of two, rot not a multiple of 8, q_heads
  * not a multiple of kv_heads), ALIGN, ALIAS (q_out or a cache overlaps another
@@ -135,7 +135,7 @@ size_t tq2_paged_attention_workspace_bytes(const tq2_paged_attention_args* args)
  * bytes; 16 tokens of a page lie within 2^31 bytes; tokens * q_heads is below
  * 2^31 - 4096.  The workspace's content
  * needs no preparation and means nothing afterwards.
- * tokens == 0 is a no-op.  Errors: INVALID (null pointer, size out of range, a
+ * tokens == 0 or batch == 0 is a no-op.  Errors: INVALID (null pointer, size out of range, a
  * workspace that is too small, types or head_dim not listed), SHAPE, ALIGN,
  * ALIAS (out overlaps a cache, the workspace or a part of q), DEVICE, LAUNCH. */
 int tq2_paged_attention(const tq2_paged_attention_args* args, void* stream);

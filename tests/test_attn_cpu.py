@@ -116,6 +116,9 @@ def test_append_aliasing(over):
 def test_append_without_tokens_is_a_no_op():
     assert append(tokens=0, batch=0, k=0, v=0, table=0, q=0, k_new=0, v_new=0) == tq2.TQ2_OK
     assert append(tokens=0, batch=0, page=24) == tq2.TQ2_ERR_SHAPE
+    assert append(tokens=7, batch=0, cu_q=A + 12 * G, k=0, table=0) == tq2.TQ2_OK     # rows without a sequence
+    assert attention(tokens=7, batch=0, cu_q=A + 12 * G, k=0, table=0) == tq2.TQ2_OK
+    assert attention(attn.paged_attention_workspace_bytes_ptr, tokens=7, batch=0, cu_q=A, max_kv=5000) == 0
 
 
 E8 = dict(cache_type=E4M3, k_scale=A + 9 * G, v_scale=A + 10 * G)
