@@ -20,10 +20,9 @@
 // more than 2^8 since the last time; until then probabilities run up to 2^8, which
 // f32 sums and (with the lift of 2^7) binary16 words hold as exactly.
 //
-// LDS.  Rows of keys lie 16-byte chunk by chunk under an exclusive or with the row
-// number, so that 8 rows' chunks lie in 8 bank groups; rows of values by pairs of
-// chunks, so that the four rows of a transpose read do.  The loads apply it on the
-// address they read from.
+// LDS.  Rows of keys lie 16-byte chunk by chunk, rows of values by 64 bytes, under an
+// exclusive or with the row number that keeps the rows read together in different banks.
+// The loads apply it on the address they read from.
 //
 // f32 q, e4m3 caches and masks as in the streaming form.
 #include "tq2_attn_device.h"
@@ -43,16 +42,22 @@ typedef __attribute__((address_space(3))) s16x4_t* lds_s16x4_t;
 typedef __attribute__((address_space(3))) const u32x4_t* lds_u32x4_t;
 typedef __attribute__((address_space(3))) unsigned char* lds_byte_t;
 
-// Where 16-byte chunk c of row r of a tile lies: slot within the row.
+// Where 16-byte chunk c of row r of a tile lies within its row.  LDS has 256 bytes of
+// banks: 16 rows' chunks c of keys, and the two neighbouring 32-byte pieces of four rows
+// of values that half a wave's transpose read takes, have to lie in different ones.
 template <int D>
 struct Place {
   static constexpr int chunks = D / 8;
-  __device__ __forceinline__ static int key(int r, int c) { return D == 96 ? c ^ (r & 3) : c ^ (r & 7); }
-  // By pairs, so that a transpose read's 32 bytes stay together.
-  __device__ __forceinline__ static int value_turn(int r) {
-    return D == 96 ? 0 : (D == 64 || D == 192 ? (r >> 1) & 1 : r & 3);
+  static constexpr int key_turn = D == 96 ? 4 : (D == 64 || D == 192 ? 8 : 16);  // chunks a turn moves among
+  __device__ __forceinline__ static int key(int r, int c) {
+    return c ^ (D == 96 ? (r >> 2) & 3 : (D == 64 || D == 192 ? (r >> 1) & 7 : r & 15));
   }
-  __device__ __forceinline__ static int value(int r, int c) { return c ^ (value_turn(r) << 1); }
+  // Values by 64 bytes: a 32-component tile of the output.
+  static constexpr int value_turn = D == 96 ? 1 : (D == 64 || D == 192 ? 2 : 4);
+  __device__ __forceinline__ static int value_tile(int r, int dt) {
+    return dt ^ (D == 96 ? 0 : (D == 64 || D == 192 ? (r >> 1) & 1 : r & 3));
+  }
+  __device__ __forceinline__ static int value(int r, int c) { return value_tile(r, c >> 2) * 4 + (c & 3); }
 };
 
 // 16 bytes a lane from base + off to LDS at + 16 * lane; past the range: zeros.
@@ -254,16 +259,15 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
     // Operand addresses in a tile.  Keys: chunk 2 t + h of row r32, whose low bits the
     // exclusive or turns; the others, and the second 32 rows, are constant offsets.
     // Values: lane l16 of a 16-lane group reads 8 bytes of row 4 h + l16 / 4, and so on.
-    constexpr int kTurn = D == 96 ? 4 : 8;                       // key chunks within one turn
-    constexpr int kPairs = D == 128 || D == 256 ? 2 : 1;         // value tiles within one turn
+    constexpr int kTurn = Place<D>::key_turn, kValueTurn = Place<D>::value_turn;
     const int l16 = lane & 15;
-    uint32_t key_at[kTurn / 2], value_at[kPairs];
+    uint32_t key_at[kTurn / 2], value_at[kValueTurn];
 #pragma unroll
     for (int t = 0; t < kTurn / 2; ++t) key_at[t] = lds + r32 * kRowBytes + Place<D>::key(r32, 2 * t + h) * 16;
 #pragma unroll
-    for (int dt = 0; dt < kPairs; ++dt)
+    for (int dt = 0; dt < kValueTurn; ++dt)
       value_at[dt] = lds + 2 * kTileBytes + (4 * h + (l16 >> 2)) * kRowBytes + (l16 & 3) * 8 +
-                     ((dt * 2 + ((lane >> 4) & 1)) ^ Place<D>::value_turn(l16 >> 2)) * 32;
+                     Place<D>::value_tile(l16 >> 2, dt) * 64 + ((lane >> 4) & 1) * 32;
     // The wave's 16 rows of values: zeros for what is not finite, and the flag.
     auto tame = [&](int buf) {
       constexpr uint32_t kTop = __is_same(PV, F16) ? 0x7C00u : 0x7F80u;
@@ -342,8 +346,8 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
         }
         u32x4_t vf[2][kTiles];
         auto read_value = [&](int t, int dt) {
-          vf[t & 1][dt] = lds_values(value_at[dt % kPairs] + buf * kTileBytes,
-                                     16 * t * kRowBytes + dt / kPairs * kPairs * 64, 8 * kRowBytes);
+          vf[t & 1][dt] = lds_values(value_at[dt % kValueTurn] + buf * kTileBytes,
+                                     16 * t * kRowBytes + dt / kValueTurn * kValueTurn * 64, 8 * kRowBytes);
         };
 #pragma unroll
         for (int dt = 0; dt < kTiles; ++dt) read_value(0, dt);
