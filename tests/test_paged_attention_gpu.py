@@ -308,3 +308,59 @@ def test_append_then_attend(attn):
     whole = chunks([n])
     for sizes in ([1] * n, [30, 1, 44], [74, 1]):
         assert float((chunks(sizes) - whole).abs().max()) < 2e-5, sizes
+
+
+def test_pages_far_apart(attn):
+    """Pages beyond 2^32 elements: append and both forms of attention address them in 64 bits."""
+    d, far = 64, (1 << 32) + 4096
+    held = [torch.empty(far + 2048, dtype=torch.float16, device="cuda") for _ in range(2)]
+    kc, vc = (t.as_strided((2, 1, 16, d), (far, 1024, 64, 1)) for t in held)
+    near = [torch.empty(2, 1, 16, d, dtype=torch.float16, device="cuda") for _ in range(2)]
+    gen = torch.Generator().manual_seed(17)
+    n = 30
+    q, k, v = (torch.randn(n, h, d, generator=gen).half().cuda() for h in (2, 1, 1))
+    lens, cu = torch.tensor([n]).int().cuda(), torch.tensor([0, n]).int().cuda()
+    table = torch.tensor([[1, 0]]).int().cuda()
+    outs = []
+    for a, b in ((kc, vc), near):
+        attn.kv_append(k, v, a, b, lens, table, cu_q=cu)
+        outs.append([attn.paged_attention(q, a, b, lens, table, cu_q=cu),
+                     attn.paged_attention(q[-1:], a, b, lens, table)])
+    assert torch.equal(kc[1, 0, 3], near[0][1, 0, 3]) and torch.equal(vc[0, 0, 13], near[1][0, 0, 13])
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+def test_refusals_name_the_argument(attn):
+    c = make(18, "f16", "f16")
+    base = dict(q=c["q"].cuda(), k_cache=c["k"].cuda(), v_cache=c["v"].cuda(), kv_len=torch.tensor(c["kv_len"]).int().cuda(),
+                table=c["table"].cuda())
+    for over, match in ((dict(kv_len=base["kv_len"].long()), "kv_len must have dtype"),
+                        (dict(table=base["table"].long()), "table must be an int32 matrix"),
+                        (dict(table=base["table"].cpu()), "table must be a device tensor"),
+                        (dict(kv_len=base["kv_len"][:2]), "kv_len must be contiguous with 3"),
+                        (dict(cu_q=base["kv_len"]), "cu_q must be contiguous with 4"),
+                        (dict(v_cache=base["v_cache"].bfloat16()), "must have one dtype"),
+                        (dict(v_cache=base["v_cache"][:, :1]), "k_cache and v_cache must be"),
+                        (dict(k_cache=base["k_cache"].transpose(2, 3), v_cache=base["v_cache"].transpose(2, 3)), "head_dim"),
+                        (dict(out=base["q"].float()), "out must have dtype"),
+                        (dict(out=base["q"][:2]), "out must be"),
+                        (dict(k_scale=torch.ones(3, device="cuda")), "k_scale must be contiguous with 2")):
+        with pytest.raises(ValueError, match=match):
+            attn.paged_attention(**{**base, **over})
+    with pytest.raises(TypeError, match="window must be an integer"):
+        attn.paged_attention(**base, window="3")
+    for over in (dict(window=-1), dict(scale=0.0), dict(k_scale=torch.ones(2, device="cuda")),
+                 dict(q=base["q"].bfloat16())):
+        with pytest.raises(RuntimeError, match="paged_attention"):
+            attn.paged_attention(**{**base, **over})
+    k = base["q"][:, :2]
+    rest = (base["k_cache"], base["v_cache"], base["kv_len"], base["table"])
+    for over, match in ((dict(q_out=base["q"]), "q_out without q"), (dict(freqs=torch.ones(64, device="cuda")), "freqs must have dtype"),
+                        (dict(positions=torch.zeros(2, 3, device="cuda").int()), "one section for each"),
+                        (dict(q=base["q"][0]), "q must be"), (dict(q_norm=torch.ones(64, device="cuda")), "q_norm must be contiguous")):
+        with pytest.raises(ValueError, match=match):
+            attn.kv_append(k, k, *rest, **over)
+    with pytest.raises(ValueError, match="heads for this cache"):
+        attn.kv_append(base["q"], base["q"], *rest)
+    with pytest.raises(TypeError, match="sections must be"):
+        attn.kv_append(k, k, *rest, positions=torch.zeros(3, device="cuda").int(), sections=7)

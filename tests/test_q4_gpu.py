@@ -83,6 +83,43 @@ def test_weight_rows(q4, n):
     check(q4, make(n + 1, 8, n, 384, 32), "m8 n%d" % n)
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("m,k", [(1, 128), (5, 1152), (8, 4224), (9, 2304), (16, 1280)])
+def test_many_weight_rows(q4, m, k, group):
+    """Tiles walked by single waves: columns that end inside a round, one pass over K and several, a last tile that
+    ends early."""
+    check(q4, make(m + k, m, 16407, k, group, residual=m != 5), "tall m%d k%d g%d" % (m, k, group))
+
+
+def test_inputs_at_the_end_of_their_memory(q4):
+    """Scales and codes whose last row ends with the allocation, an odd number of scales in a row."""
+    for n in (5, 16405):
+        c = make(n, 2, n, 1152, 128)
+        codes, scales = dev(c["codes"]), dev(c["scales"])
+        y = q4.gemv(codes, scales, dev(c["x"])).cpu().numpy()
+        ref, s = expected(c)
+        assert np.all(np.abs(y - ref) <= TOL * s), n
+
+
+def test_refusals_name_the_argument(q4):
+    codes = torch.zeros(8, 128, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(8, 2, dtype=torch.float16, device="cuda")
+    x = torch.zeros(2, 256, device="cuda")
+    for args, more, match in (((codes.int(), scales, x), {}, "codes must have dtype"),
+                              ((codes, scales.float(), x), {}, "scales must have dtype"),
+                              ((codes, scales, x.double()), {}, "x must have dtype"),
+                              ((codes, scales, x[:, ::2]), {}, "x must be contiguous"),
+                              ((codes, scales, x), dict(residual=x[:1]), "residual must be contiguous"),
+                              ((codes, scales, x), dict(out=x), "out must be contiguous"),
+                              ((codes.cpu(), scales, x), {}, "codes must be a device tensor")):
+        with pytest.raises(ValueError, match=match):
+            q4.gemv(*args, **more)
+    with pytest.raises(TypeError, match="x must be a torch.Tensor"):
+        q4.gemv(codes, scales, None)
+    with pytest.raises(RuntimeError, match="q4_gemv"):
+        q4.gemv(codes, scales, torch.zeros(17, 256, device="cuda"))
+
+
 @pytest.mark.parametrize("m", [1, 8, 16])
 def test_magnitudes_of_x(q4, m):
     """Rows of x sixty binary orders apart keep their own accuracy."""
