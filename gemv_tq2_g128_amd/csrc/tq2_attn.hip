@@ -696,10 +696,26 @@ AttnPlan plan_attention(const tq2_paged_attention_args& a) {
   const int64_t blocks = c.batch * c.kv_heads * plan.steps;
   int64_t per, splits;
   if (plan.tiled) {
-    // Two blocks for each CU, of at least 512 keys.
-    splits = up(512, blocks);
-    per = up(up(keys, splits), 128) * 128;
-    if (per < 512) per = 512;
+    // The number of parts with the least time: a block takes about 4.5 us to start and
+    // end and 1.9 us for 64 keys of 128 components in 16 bits, twice that in 32; two
+    // blocks fit on a CU, or one of wide heads; parts that are joined cost 6 us and
+    // their way to memory and back at 3 TB/s (measured; 36 rows over 1,000 keys: 12.5 us in
+    // parts of 128 keys, 19.4 of 512; 1,200 rows over 300 keys: 14.3 us whole, 22.6 in two).
+    const bool wide = c.act_type == TQ2_TYPE_F32;
+    const int64_t slots = c.head_dim > 128 || (wide && c.head_dim > 64) ? 256 : 512;
+    const double tile = 1.9 * double(c.head_dim) / 128.0 * (wide ? 2.0 : 1.0);
+    const double joined = double(c.tokens) * double(c.q_heads) * double(c.head_dim + 4) * 8.0 / 3e6;
+    double least = 0.0;
+    per = 128;
+    for (int64_t parts = 1; parts <= 64; parts += parts < 4 ? 1 : parts / 2) {
+      const int64_t each = keys < 1 ? 128 : up(up(keys, parts), 128) * 128, count = keys < 1 ? 1 : up(keys, each);
+      const double time = double(up(blocks * count, slots)) * (4.5 + tile * double(each) / 64.0) +
+                          (count > 1 ? 6.0 + joined * double(count) : 0.0);
+      if (parts == 1 || time < least) {
+        least = time;
+        per = each;
+      }
+    }
   } else {
     // 1, 2, 4 or 8 tiles of 32 keys for each of a block's four waves, by the least time:
     // two blocks fit on a CU, a block takes about 4.5 us to start and end and 1.4 us a

@@ -14,14 +14,16 @@
 // Accumulation is f32: the codes of one group are summed by the matrix core,
 // then scaled by d (one lane holds one weight row) and by the power of two.
 //
-// Work split.  A block of 8 waves owns all of K for a step of RT * 16 weight
-// rows; each wave takes an eighth of the 128-wide blocks of K, and the eight
-// partial sums meet in LDS.  x is converted once per block into LDS in
-// operand order, so a wave's inner loop is: one 16-byte load per lane (a row
-// segment of 64 bytes per row and 128-wide block, next to the one the same wave
-// reads for the following block), four LDS operand reads shared by RT row
-// tiles, decode, MFMA.  Blocks walk over row steps, with the next step's
-// codes in flight before the present step is computed.
+// Work split.  x is converted once per block into LDS in operand order; a wave's
+// inner loop is one 16-byte load per lane (a row segment of 64 bytes for each of 16
+// rows and 128-wide block of K), four LDS operand reads, decode, MFMA.  q4_kernel
+// splits K: a block of 8 waves walks over steps of 16 weight rows, each wave takes
+// an eighth of the 128-wide blocks, and the eight partial sums meet in LDS.
+// q4_tall_kernel, for many rows, gives each wave tiles of 16 rows and all of K, with
+// no barrier.  Both have the next step's codes in flight before the present one is
+// computed.  131072 x 4096, eight rows of x: 64 us (4.4 TB/s, 48 us without the
+// arithmetic and the scales); 4096 x 4096, one row: 5.3 us, most of it the launch
+// and one trip to memory after another.
 //
 // Groups.  A lane's 16 bytes are 32 consecutive weights.  For group 128 any
 // order of k inside the 128-wide block will do, so word s of lane group g
@@ -416,7 +418,10 @@ template <int G, int MT>
 hipError_t launch(const Q4Args& a, hipStream_t stream) {
   const int all_kb = int(a.k >> 7);
   const int pass_kb = MT == 8 ? kWaves * kMaxKb : kWaves * kMaxKb / 2;
-  const bool tall = a.n >= 16384;
+  // Rows over the waves once there are two tiles for each of 2048 waves: 131072 x 4096 takes
+  // 62 us at one row of x (67 with K split) and 69 us at eight (82), 65536 x 4096 38 (37) and
+  // 39 (44), 32768 x 4096 in groups of 32 27 (24) and 31 (31).
+  const bool tall = a.n >= 65536;
   const size_t lds = Shape<MT>::bytes(all_kb < pass_kb ? all_kb : pass_kb, int(a.m), !tall);
   const int64_t tiles = (a.n + 15) / 16, steps = tall ? (tiles + kWaves - 1) / kWaves : tiles;
   const int per_cu = lds <= 80 * 1024 ? 2 : 1;
