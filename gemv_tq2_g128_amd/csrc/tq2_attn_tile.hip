@@ -65,9 +65,11 @@ struct Place {
   __device__ __forceinline__ static int value(int r, int c) { return value_tile(r, c >> 2) * 4 + (c & 3); }
 };
 
-// 16 bytes a lane from base + off to LDS at + 16 * lane; past the range: zeros.
+// 16 bytes a lane from base + off to LDS at + 16 * lane; past the range: zeros.  The
+// compiler does not see the load: the five wait states that it would put between a
+// vector instruction's write of a resource word (a lane read) and the load are here.
 __device__ __forceinline__ void load_to_lds(rsrc_t r, uint32_t off, uint32_t at) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                ::"s"(at), "v"(off), "s"(r) : "memory");
 }
 // The larger of two; NaN if one is (fmaxf would first quiet its operands).
