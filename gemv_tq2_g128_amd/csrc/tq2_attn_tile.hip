@@ -164,6 +164,10 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
     const int below = out_of < -1 ? -1 : int(out_of);            // keys up to here are out of the window
     float scale = a.scale;
     if constexpr (kSize == 1) scale *= a.k_scale[head];
+    // Scores meet the mask and the maximum before they meet the scale, which therefore has to
+    // be positive: a negative one turns q's sign, and zero becomes the least number, which
+    // leaves every score at 0 and a masked one at -infinity.
+    const bool turned = kSize == 1 && scale < 0.f;
     u32x4_t q[kSteps], q2[kSplit ? kSteps : 1];
     const act_t* src = static_cast<const act_t*>(a.q) + (live ? token * a.q_token + qh * a.q_head : 0) + 8 * h;
     float lift = 1.f;
@@ -184,9 +188,10 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
       top = fmaxf(both.x, both.y);
       const int e = int((word(top) >> 23) & 255) - 127;
       const int up = top > 0.f ? min(13 - e, 126) : 0;
-      lift = __builtin_ldexpf(1.f, up);
+      lift = turned ? -__builtin_ldexpf(1.f, up) : __builtin_ldexpf(1.f, up);
       scale *= __builtin_ldexpf(1.f, -up);
     }
+    scale = scale == 0.f ? 0x1p-149f : fabsf(scale);
 #pragma unroll
     for (int t = 0; t < kSteps; ++t) {
       if constexpr (kSplit) {
@@ -196,6 +201,7 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
                         pack2_rest(QK(), z[0], z[1]), pack2_rest(QK(), z[2], z[3])};
       } else {
         q[t] = live ? *reinterpret_cast<const u32x4_t*>(src + t * 16) : u32x4_t{0, 0, 0, 0};
+        if constexpr (kSize == 1) q[t] ^= turned ? 0x80008000u : 0u;
       }
     }
     float m = kNone, sum = 0.f;

@@ -241,7 +241,8 @@ int tq2_paged_attention(const tq2_paged_attention_args* args, void* stream) {
   const tq2_paged_cache& c = a.cache;
   int st = check_attention_sizes(a);
   if (st != TQ2_OK) return st;
-  if (!(a.scale > 0.0) || !(a.scale <= 3e38)) return TQ2_ERR_INVALID;
+  const double scale = a.scale * 1.4426950408889634;             // scores as exponents of two
+  if (!(a.scale > 0.0) || !(scale <= double(__FLT_MAX__))) return TQ2_ERR_INVALID;
   if (c.tokens == 0 || c.batch == 0) return TQ2_OK;              // no row has a sequence
   st = check_cache_arrays(c);
   if (st != TQ2_OK) return st;
@@ -282,7 +283,7 @@ int tq2_paged_attention(const tq2_paged_attention_args* args, void* stream) {
   g.o_token = a.out_token_stride;
   g.o_head = a.out_head_stride;
   g.part = plan.splits > 1 ? static_cast<float*>(a.workspace) : nullptr;
-  g.scale = float(a.scale * 1.4426950408889634);                 // scores as exponents of two
+  g.scale = float(scale);
   g.window = int32_t(a.window);
   g.group = uint32_t(c.q_heads / c.kv_heads);
   g.splits = plan.splits;

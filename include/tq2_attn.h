@@ -14,7 +14,8 @@
  * table[b * table_stride + n / page].  Sequence b holds kv_len[b] tokens, the
  * new ones of the present call included.
  * 8-bit caches hold e4m3 codes of value / scale with one f32 scale per key
- * head.
+ * head.  tq2_paged_attention multiplies by any finite scale, also zero (the
+ * codes count as zeros) and negative ones; tq2_kv_append divides by it.
  *
  * New tokens.  cu_q[b] .. cu_q[b + 1] are the rows of q, k, v and out that
  * belong to sequence b, in order; they are the last tokens of the sequence.
@@ -112,7 +113,7 @@ typedef struct tq2_paged_attention_args {
   int64_t max_q;             /* most new tokens of a sequence, most tokens of one: the launch is */
   int64_t max_kv;            /* shaped for them; larger ones in cu_q and kv_len are still done */
   int64_t window;            /* a token sees itself and window - 1 before it; 0: all before it */
-  double scale;              /* of the scores, usually 1 / sqrt(head_dim) */
+  double scale;              /* of the scores, usually 1 / sqrt(head_dim): above 0, below 2^127 */
   void* workspace;           /* NULL if none is needed */
   int64_t workspace_bytes;
 } tq2_paged_attention_args;
