@@ -684,77 +684,7 @@ hipError_t launch_join_dim(const AttnArgs& a, hipStream_t stream) {
   }
 }
 
-int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 }  // namespace
-
-AttnPlan plan_attention(const tq2_paged_attention_args& a) {
-  const tq2_paged_cache& c = a.cache;
-  AttnPlan plan;
-  const int64_t max_q = a.max_q < 1 ? 1 : (a.max_q < c.tokens ? a.max_q : c.tokens);
-  const int64_t rows = max_q * (c.q_heads / c.kv_heads);
-  // The tiled form reads keys and values once for 128 rows: 64 rows over 16 caches of 4,096
-  // take 64 us (103 streaming), 36 rows over 4 of them 27 (35).
-  plan.tiled = rows > 32;
-  // Two row tiles share the loads of keys and values; wider heads' outputs leave no registers for a second.
-  plan.row_tiles = rows <= 16 || c.head_dim > 128 ? 1 : 2;
-  const int64_t steps = up(rows, plan.tiled ? kTileRows : plan.row_tiles * 16);
-  const int64_t room = (plan.tiled ? int64_t(1) << 20 : 65535) / c.kv_heads;  // of the grid
-  plan.steps = int32_t(steps < room ? steps : room);
-  const int64_t span = a.window ? a.window + max_q + 31 : a.max_kv;   // that a sequence's rows see
-  const int64_t keys = span < a.max_kv ? span : a.max_kv;
-  const int64_t blocks = c.batch * c.kv_heads * plan.steps;
-  int64_t per, splits;
-  if (plan.tiled) {
-    // The number of parts with the least time: a block takes about 4.5 us to start and
-    // end and 1.9 us for 64 keys of 128 components in 16 bits, twice that in 32; two
-    // blocks fit on a CU, or one of wide heads; parts that are joined cost 6 us and
-    // their way to memory and back at 3 TB/s (measured; 36 rows over 1,000 keys: 12.5 us in
-    // parts of 128 keys, 19.4 of 512; 1,200 rows over 300 keys: 14.3 us whole, 22.6 in two).
-    const bool wide = c.act_type == TQ2_TYPE_F32;
-    const int64_t slots = c.head_dim > 128 || (wide && c.head_dim > 64) ? 256 : 512;
-    const double tile = 1.9 * double(c.head_dim) / 128.0 * (wide ? 2.0 : 1.0);
-    const double joined = double(c.tokens) * double(c.q_heads) * double(c.head_dim + 4) * 8.0 / 3e6;
-    double least = 0.0;
-    per = 128;
-    for (int64_t parts = 1; parts <= 64; parts += parts < 4 ? 1 : parts / 2) {
-      const int64_t each = keys < 1 ? 128 : up(up(keys, parts), 128) * 128, count = keys < 1 ? 1 : up(keys, each);
-      const double time = double(up(blocks * count, slots)) * (4.5 + tile * double(each) / 64.0) +
-                          (count > 1 ? 6.0 + joined * double(count) : 0.0);
-      if (parts == 1 || time < least) {
-        least = time;
-        per = each;
-      }
-    }
-  } else {
-    // 1, 2, 4 or 8 tiles of 32 keys for each of a block's four waves, by the least time:
-    // two blocks fit on a CU, a block takes about 4.5 us to start and end and 1.4 us a
-    // tile, and joining parts takes 4 us and about 0.1 us a part (measured).  Longer
-    // parts leave CUs idle at the end of ragged batches: 4 sequences of up to 131,071
-    // tokens take 131 us with 1024 keys a part, 143 with 2048, 159 with 4096.
-    double least = 0.0;
-    per = 128;
-    for (int64_t tiles = 1; tiles <= 8; tiles *= 2) {
-      const int64_t parts = up(keys, 128 * tiles), rounds = up(blocks * (parts < 1 ? 1 : parts), 512);
-      const double time = double(rounds) * (4.5 + 1.4 * double(tiles)) + (parts > 1 ? 4.0 + 0.1 * double(parts) : 0.0);
-      if (tiles == 1 || time < least) {
-        least = time;
-        per = 128 * tiles;
-      }
-    }
-    // Sequences enough to fill the card by themselves, none so long that the others wait
-    // for it: nothing to join (64 of up to 8192 tokens: 239 us, 254 in parts of 1024).
-    if (blocks >= 512 && keys <= 8192) per = 8192;
-  }
-  splits = keys < 1 ? 1 : up(keys, per);
-  if (splits > 512) splits = 512;
-  plan.splits = int32_t(splits);
-  plan.split_keys = int32_t(per);
-  const int64_t most = (int64_t(1) << 31) - 1;                   // blocks of the tiled form
-  while (plan.tiled && plan.steps > 1 && c.batch * c.kv_heads * plan.steps * splits > most) plan.steps /= 2;
-  plan.workspace = splits == 1 ? 0 : size_t(c.tokens) * size_t(c.q_heads) * size_t(splits) * size_t(c.head_dim + 4) * 4;
-  return plan;
-}
 
 hipError_t launch_paged_attention(const AttnArgs& a, const AttnPlan& plan, int act, int cache,
                                   hipStream_t stream) {

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "../../include/tq2_attn.h"
+#include "tq2_attn_plan.h"
 #include "tq2_pages.h"
 
 namespace tq2 {
@@ -49,17 +50,6 @@ struct AttnArgs {
   int32_t split_keys;                    // least keys of a part, a multiple of 32
 };
 
-constexpr int kTileRows = 128;           // of a block of the tiled form
-
-// How a call is laid out; from sizes alone.
-struct AttnPlan {
-  bool tiled;                            // the form for many rows (new tokens times heads of a key head)
-  int32_t row_tiles;                     // streaming form: 16-row tiles of a step
-  int32_t steps;                         // steps of max_q new tokens
-  int32_t splits, split_keys;
-  size_t workspace;                      // bytes
-};
-AttnPlan plan_attention(const tq2_paged_attention_args& a);
 // Arguments are already validated: tokens >= 1.
 hipError_t launch_attention_tiles(const AttnArgs& a, const AttnPlan& plan, int act, int cache,
                                   hipStream_t stream);

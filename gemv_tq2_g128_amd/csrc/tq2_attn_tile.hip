@@ -125,8 +125,8 @@ __global__ __launch_bounds__(64 * kWaves, (kMinWaves<Act, D>)) void tile_kernel(
   id /= p.kv_heads;
   const int split = id % a.splits;
   id /= a.splits;
-  const int step = steps - 1 - int(id % steps);
-  const int b = id / steps;
+  const int step = steps - 1 - int(id);
+  const int b = blockIdx.y;
   const Seq s = sequence(p, b);
   const uint32_t rows = uint32_t(s.q_len) * group;               // below 2^31
   const Parts parts = parts_of(s, a.window, a.splits, a.split_keys);
@@ -477,8 +477,8 @@ hipError_t launch(const AttnArgs& a, const AttnPlan& plan, hipStream_t stream) {
                                              hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
     if (e != hipSuccess) return e;
   }
-  const int64_t blocks = int64_t(a.pages.kv_heads) * plan.splits * plan.steps * a.pages.batch;
-  hipLaunchKernelGGL(fn, dim3(uint32_t(blocks)), dim3(64 * kWaves), lds, stream, a, plan.steps);
+  const Grid grid = tile_grid(plan, a.pages.kv_heads, a.pages.batch);
+  hipLaunchKernelGGL(fn, dim3(grid.x, grid.y, grid.z), dim3(64 * kWaves), lds, stream, a, plan.steps);
   return hipGetLastError();
 }
 

@@ -1,0 +1,94 @@
+"""CPU checks of how an attention call is laid out (csrc/tq2_attn_plan.h, compiled for the host)."""
+
+import ctypes
+import os
+import random
+import subprocess
+
+import pytest
+
+pytest.importorskip("torch")
+from gemv_tq2_g128_amd import attn  # noqa: E402
+from tests.test_attn_cpu import A, BF16, CACHE, E4M3, F16, F32, G, ROOT, cache_fields  # noqa: E402
+
+HARNESS = r"""
+#include "tq2_attn_plan.h"
+extern "C" void plan(const tq2_paged_attention_args* a, int64_t* out) {
+  const tq2::AttnPlan p = tq2::plan_attention(*a);
+  const int64_t all[] = {p.tiled, p.row_tiles, p.steps, p.splits, p.split_keys, int64_t(p.workspace)};
+  for (int64_t v : all) *out++ = v;
+}
+extern "C" void tile_grid(int64_t splits, int64_t steps, int64_t kv_heads, int64_t batch, int64_t* out) {
+  tq2::AttnPlan p{};
+  p.splits = int32_t(splits), p.steps = int32_t(steps);
+  const tq2::Grid g = tq2::tile_grid(p, kv_heads, batch);
+  out[0] = g.x, out[1] = g.y, out[2] = g.z;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def host(tmp_path_factory):
+    at = tmp_path_factory.mktemp("plan")
+    (at / "plan.cc").write_text(HARNESS)
+    subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-Wall", "-Werror", "-fsanitize=undefined",
+                    "-fno-sanitize-recover", "-I", os.path.join(ROOT, "gemv_tq2_g128_amd", "csrc"),
+                    str(at / "plan.cc"), "-o", str(at / "plan.so")], check=True)
+    return ctypes.CDLL(str(at / "plan.so"))
+
+
+class Plan:
+    def __init__(self, host, max_q, max_kv, window=0, **over):
+        e8 = dict(k_scale=A, v_scale=A) if over.get("cache_type") == E4M3 else {}
+        self.cache = cache_fields(**{**e8, **over})
+        tail = attn._ATTENTION.pack(A, A + G, 0, 0, 0, 0, max_q, max_kv, window, 0.1, 0, 0)
+        args = attn._CACHE.pack(*(self.cache[n] for n in CACHE)) + tail
+        out = (ctypes.c_int64 * 6)()
+        host.plan(args, out)
+        self.tiled, self.row_tiles, self.steps, self.splits, self.split_keys, self.workspace = out
+        assert self.workspace == attn.paged_attention_workspace_bytes_ptr(args)
+
+
+def grid(fn, *args):
+    out = (ctypes.c_int64 * 3)()
+    fn(*(ctypes.c_int64(a) for a in args), out)
+    return tuple(out)
+
+
+def launchable(g, threads=256):
+    x, y, z = g
+    return 1 <= x and x * threads < 1 << 32 and 1 <= y <= 65535 and 1 <= z <= 65535
+
+
+@pytest.mark.parametrize("batch,each,heads", [(1024, 64, (32, 8)), (256, 512, (64, 8)), (512, 128, (64, 8)),
+                                              (1024, 32, (64, 8)), (4096, 2, (64, 8)), (65535, 1, (64, 8)),
+                                              (65535, 16384, (1024, 1024)), (1, 1 << 20, (1024, 1))])
+def test_many_sequences_without_a_longest(host, batch, each, heads):
+    """max_q left at all of q's rows: the grid can still be launched, and no more blocks start than are worth it."""
+    p = Plan(host, batch * each, 4096, batch=batch, tokens=batch * each, cu_q=A, q_heads=heads[0], kv_heads=heads[1])
+    assert p.tiled
+    g = grid(host.tile_grid, p.splits, p.steps, heads[1], batch)
+    assert launchable(g)
+    assert g[0] * g[1] * g[2] <= max(1 << 19, batch * heads[1] * p.splits)
+
+
+def test_plans_in_range(host):
+    """Any sizes that a call accepts: the grid of the tiled form can be launched."""
+    rng = random.Random(3)
+
+    def wide(most):
+        return min(most, int(2 ** rng.uniform(0, most.bit_length())))
+
+    for _ in range(4000):
+        kv_heads = wide(1024)
+        q_heads = kv_heads * rng.randrange(1, 1024 // kv_heads + 1)
+        batch = wide(65535)
+        act, cache = rng.choice([(F32, F16), (F32, E4M3), (F16, F16), (BF16, BF16), (BF16, E4M3)])
+        tokens = min(wide(1 << 30), ((1 << 31) - 4097) // q_heads)
+        max_kv = rng.choice([0, wide((1 << 31) - 1), (1 << 31) - 1])
+        p = Plan(host, rng.choice([0, 1, wide(1 << 30), tokens]), max_kv, rng.choice([0, wide((1 << 31) - 1)]),
+                 batch=batch, tokens=tokens, cu_q=A, q_heads=q_heads, kv_heads=kv_heads, act_type=act, cache_type=cache,
+                 head_dim=rng.choice([64, 96, 128, 192, 256]))
+        assert p.steps >= 1 and 1 <= p.splits <= 512
+        if p.tiled:
+            assert launchable(grid(host.tile_grid, p.splits, p.steps, kv_heads, batch))
