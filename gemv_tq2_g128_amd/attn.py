@@ -65,8 +65,9 @@ def paged_attention(q, k_cache, v_cache, kv_len, table, cu_q=None, max_q=None, m
     """softmax(scale * q K^T) V of q [tokens, q_heads, head_dim] over the cache, each token seeing its sequence up to
     itself (the last ``window`` tokens of that, if given); rows that see nothing give zeros.
 
-    ``max_q`` and ``max_kv``, the most new tokens and the most tokens of a sequence, shape the launch (by default all
-    of q and all that the table holds); larger ones are still done.  ``scale`` is 1 / sqrt(head_dim) by default.
-    ``out`` may be q itself."""
+    ``max_q`` and ``max_kv``, the most new tokens and the most tokens of a sequence, shape the launch; larger ones are
+    still done.  By default they are all of q and all that the table holds, which is right for one sequence and slow for
+    many: a decode batch given with ``cu_q`` takes the form for prompts unless ``max_q`` says 1.  ``scale`` is
+    1 / sqrt(head_dim) by default.  ``out`` may be q itself."""
     return _result(_binding.paged_attention(q, k_cache, v_cache, kv_len, table, cu_q, k_scale, v_scale, max_q, max_kv,
                                             window, scale, out), "paged_attention")

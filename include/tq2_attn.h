@@ -111,7 +111,8 @@ typedef struct tq2_paged_attention_args {
   int64_t q_token_stride, q_head_stride;
   int64_t out_token_stride, out_head_stride;
   int64_t max_q;             /* most new tokens of a sequence, most tokens of one: the launch is */
-  int64_t max_kv;            /* shaped for them; larger ones in cu_q and kv_len are still done */
+  int64_t max_kv;            /* shaped for them; larger ones in cu_q and kv_len are still done, and */
+                             /* far too large values cost time (blocks that find no work) */
   int64_t window;            /* a token sees itself and window - 1 before it; 0: all before it */
   double scale;              /* of the scores, usually 1 / sqrt(head_dim): above 0, below 2^127 */
   void* workspace;           /* NULL if none is needed */
