@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/tq2_attn.h"
+#include "tq2_pages.h"
 
 namespace tq2 {
 
@@ -50,8 +51,9 @@ inline AttnPlan plan_attention(const tq2_paged_attention_args& a) {
   // Steps past the room of the grid are walked over by its blocks.
   const int64_t room = plan.tiled ? kTileBlocks / (c.kv_heads * c.batch) : 65535 / c.kv_heads;
   plan.steps = int32_t(steps < room ? steps : (room < 1 ? 1 : room));
-  const int64_t span = a.window ? a.window + max_q + 31 : a.max_kv;   // that a sequence's rows see
-  const int64_t keys = span < a.max_kv ? span : a.max_kv;
+  const int64_t span = a.window ? a.window + max_q + 31 : a.max_kv;  // that a sequence's rows see
+  const int64_t most = a.max_kv < kMaxKeys ? a.max_kv : kMaxKeys;
+  const int64_t keys = span < most ? span : most;
   const int64_t blocks = c.batch * c.kv_heads * plan.steps;
   int64_t per, splits;
   if (plan.tiled) {

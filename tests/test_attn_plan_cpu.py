@@ -73,7 +73,7 @@ def test_many_sequences_without_a_longest(host, batch, each, heads):
 
 
 def test_plans_in_range(host):
-    """Any sizes that a call accepts: the grid of the tiled form can be launched."""
+    """Any sizes that a call accepts: the grid of the tiled form can be launched and the parts fit their fields."""
     rng = random.Random(3)
 
     def wide(most):
@@ -89,6 +89,14 @@ def test_plans_in_range(host):
         p = Plan(host, rng.choice([0, 1, wide(1 << 30), tokens]), max_kv, rng.choice([0, wide((1 << 31) - 1)]),
                  batch=batch, tokens=tokens, cu_q=A, q_heads=q_heads, kv_heads=kv_heads, act_type=act, cache_type=cache,
                  head_dim=rng.choice([64, 96, 128, 192, 256]))
-        assert p.steps >= 1 and 1 <= p.splits <= 512
+        assert p.steps >= 1 and 1 <= p.splits <= 512 and p.split_keys >= 128 and p.split_keys % 32 == 0
         if p.tiled:
             assert launchable(grid(host.tile_grid, p.splits, p.steps, kv_heads, batch))
+
+
+@pytest.mark.parametrize("max_q", [1, 64, 5000])
+def test_the_longest_cache(host, max_q):
+    """Keys of a part stay in 31 bits where max_kv is the largest that is taken."""
+    for max_kv in ((1 << 31) - 1, (1 << 31) - 200, 0x7FFF0000):
+        p = Plan(host, max_q, max_kv, batch=60000, tokens=max_q * 60000, cu_q=A)
+        assert 128 <= p.split_keys <= 0x7FFF0000 and (p.split_keys * p.splits >= 0x7FFF0000 or p.splits == 512)
