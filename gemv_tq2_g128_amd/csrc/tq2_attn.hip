@@ -531,8 +531,10 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
   __shared__ float states[G > 1 ? G : 1][D + 4];
   const Pages& p = a.pages;
   const int lane = threadIdx.x % L, g = threadIdx.x / L % G;
-  const uint32_t row = blockIdx.x * kRows + threadIdx.x / (L * G);
-  const int token = int(row / uint32_t(p.q_heads)), qh = int(row % uint32_t(p.q_heads));
+  const uint32_t row = (blockIdx.y * gridDim.x + blockIdx.x) * kRows + threadIdx.x / (L * G);
+  // Rows past the last one: no token.
+  const bool there = row < uint32_t(p.tokens) * uint32_t(p.q_heads);
+  const int token = there ? int(row / uint32_t(p.q_heads)) : p.tokens, qh = int(row % uint32_t(p.q_heads));
   const float* part = a.part + int64_t(row) * a.splits * (D + 4);
   const int c = lane * 4;
   // Parts are read kBatch at a time, the first ones before it is known how many the row
@@ -665,11 +667,11 @@ hipError_t launch_join(const AttnArgs& a, hipStream_t stream) {
   constexpr int L = D <= 64 ? 16 : (D <= 128 ? 32 : 64);
   const int64_t rows = int64_t(a.pages.tokens) * a.pages.q_heads;
   // A whole block for each row once there are parts for all of it.
+  const Grid grid = join_grid(a.splits > 8 ? rows : pieces(rows, 256 / L));
   if (a.splits > 8)
-    hipLaunchKernelGGL((join_kernel<Act, D, 256 / L>), dim3(uint32_t(rows)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((join_kernel<Act, D, 256 / L>), dim3(grid.x, grid.y), dim3(256), 0, stream, a);
   else
-    hipLaunchKernelGGL((join_kernel<Act, D, 1>), dim3(uint32_t((rows + 256 / L - 1) / (256 / L))), dim3(256), 0,
-                       stream, a);
+    hipLaunchKernelGGL((join_kernel<Act, D, 1>), dim3(grid.x, grid.y), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 

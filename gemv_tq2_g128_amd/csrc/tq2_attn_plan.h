@@ -112,4 +112,10 @@ inline Grid tile_grid(const AttnPlan& plan, int64_t kv_heads, int64_t batch) {
   return Grid{uint32_t(kv_heads * plan.splits * plan.steps), uint32_t(batch), 1};
 }
 
+// Blocks of the join, numbered along x first; a few past the last one are left over.
+inline Grid join_grid(int64_t blocks) {
+  const int64_t y = pieces(blocks, int64_t(1) << 20);
+  return Grid{uint32_t(pieces(blocks, y)), uint32_t(y), 1};
+}
+
 }  // namespace tq2

@@ -24,6 +24,10 @@ extern "C" void tile_grid(int64_t splits, int64_t steps, int64_t kv_heads, int64
   const tq2::Grid g = tq2::tile_grid(p, kv_heads, batch);
   out[0] = g.x, out[1] = g.y, out[2] = g.z;
 }
+extern "C" void join_grid(int64_t blocks, int64_t* out) {
+  const tq2::Grid g = tq2::join_grid(blocks);
+  out[0] = g.x, out[1] = g.y, out[2] = g.z;
+}
 """
 
 
@@ -100,3 +104,12 @@ def test_the_longest_cache(host, max_q):
     for max_kv in ((1 << 31) - 1, (1 << 31) - 200, 0x7FFF0000):
         p = Plan(host, max_q, max_kv, batch=60000, tokens=max_q * 60000, cu_q=A)
         assert 128 <= p.split_keys <= 0x7FFF0000 and (p.split_keys * p.splits >= 0x7FFF0000 or p.splits == 512)
+
+
+@pytest.mark.parametrize("blocks", [1, 5, (1 << 20) - 1, 1 << 20, (1 << 20) + 1, 1 << 24, (1 << 24) + 7, 99999989,
+                                    (1 << 31) - 4097])
+def test_join_grid(host, blocks):
+    """Every block is there, few are left over (their rows stay below 2^32), and the launch is one that can be made."""
+    g = grid(host.join_grid, blocks)
+    assert launchable(g) and g[2] == 1
+    assert 0 <= g[0] * g[1] - blocks < 2048
