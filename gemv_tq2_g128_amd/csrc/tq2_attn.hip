@@ -531,7 +531,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
   __shared__ float states[G > 1 ? G : 1][D + 4];
   const Pages& p = a.pages;
   const int lane = threadIdx.x % L, g = threadIdx.x / L % G;
-  const uint32_t row = (blockIdx.y * gridDim.x + blockIdx.x) * kRows + threadIdx.x / (L * G);
+  const uint32_t row = ((blockIdx.y << kRowShift) + blockIdx.x) * kRows + threadIdx.x / (L * G);
   // Rows past the last one: no token.
   const bool there = row < uint32_t(p.tokens) * uint32_t(p.q_heads);
   const int token = there ? int(row / uint32_t(p.q_heads)) : p.tokens, qh = int(row % uint32_t(p.q_heads));
@@ -667,7 +667,7 @@ hipError_t launch_join(const AttnArgs& a, hipStream_t stream) {
   constexpr int L = D <= 64 ? 16 : (D <= 128 ? 32 : 64);
   const int64_t rows = int64_t(a.pages.tokens) * a.pages.q_heads;
   // A whole block for each row once there are parts for all of it.
-  const Grid grid = join_grid(a.splits > 8 ? rows : pieces(rows, 256 / L));
+  const Grid grid = row_grid(a.splits > 8 ? rows : pieces(rows, 256 / L));
   if (a.splits > 8)
     hipLaunchKernelGGL((join_kernel<Act, D, 256 / L>), dim3(grid.x, grid.y), dim3(256), 0, stream, a);
   else

@@ -73,7 +73,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendArgs a) {
   __shared__ int64_t at_k[T], at_v[T];           // offset of the token in the caches, kNowhere or kUnowned
   const Pages& p = a.pages;
   const int wave = threadIdx.x >> 6;
-  const int t0 = blockIdx.x * T;
+  const int t0 = ((blockIdx.z << kRowShift) + blockIdx.x) * T;
   // One wave finds a token's sequence, its place and its angles.
   for (int i = wave; i < T; i += kThreads / 64) {
     const int t = t0 + i;
@@ -200,12 +200,8 @@ template <class Act, class Cache, int G, int T>
 hipError_t launch(const AppendArgs& a, hipStream_t stream) {
   const int heads = (a.q ? a.pages.q_heads : 0) + 2 * a.pages.kv_heads;
   const int rounds = (heads * G + kThreads - 1) / kThreads;
-  const int blocks = (a.pages.tokens + T - 1) / T;
-  // Few tokens: their heads are spread until there are eight blocks for each CU (1,640
-  // tokens of 48 heads: 8.2 us, with sixteen 9.1).
-  const int share = 2048 / blocks;
-  const int y = share < 1 ? 1 : (share < rounds ? share : rounds);
-  hipLaunchKernelGGL((kv_append_kernel<Act, Cache, G, T>), dim3(blocks, y), dim3(kThreads), 0, stream, a);
+  const Grid grid = append_grid(a.pages.tokens, T, rounds);
+  hipLaunchKernelGGL((kv_append_kernel<Act, Cache, G, T>), dim3(grid.x, grid.y, grid.z), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 

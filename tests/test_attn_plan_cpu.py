@@ -24,8 +24,12 @@ extern "C" void tile_grid(int64_t splits, int64_t steps, int64_t kv_heads, int64
   const tq2::Grid g = tq2::tile_grid(p, kv_heads, batch);
   out[0] = g.x, out[1] = g.y, out[2] = g.z;
 }
-extern "C" void join_grid(int64_t blocks, int64_t* out) {
-  const tq2::Grid g = tq2::join_grid(blocks);
+extern "C" void append_grid(int64_t tokens, int64_t per_block, int64_t rounds, int64_t* out) {
+  const tq2::Grid g = tq2::append_grid(tokens, per_block, rounds);
+  out[0] = g.x, out[1] = g.y, out[2] = g.z;
+}
+extern "C" void row_grid(int64_t blocks, int64_t* out) {
+  const tq2::Grid g = tq2::row_grid(blocks);
   out[0] = g.x, out[1] = g.y, out[2] = g.z;
 }
 """
@@ -108,8 +112,18 @@ def test_the_longest_cache(host, max_q):
 
 @pytest.mark.parametrize("blocks", [1, 5, (1 << 20) - 1, 1 << 20, (1 << 20) + 1, 1 << 24, (1 << 24) + 7, 99999989,
                                     (1 << 31) - 4097])
-def test_join_grid(host, blocks):
-    """Every block is there, few are left over (their rows stay below 2^32), and the launch is one that can be made."""
-    g = grid(host.join_grid, blocks)
+def test_row_grid(host, blocks):
+    """Every block is there, less than a row is left over (16 rows of q each: below 2^32), and it can be launched."""
+    g = grid(host.row_grid, blocks)
     assert launchable(g) and g[2] == 1
-    assert 0 <= g[0] * g[1] - blocks < 2048
+    assert 0 <= g[0] * g[1] - blocks < 1 << 20 and (g[1] == 1) == (blocks <= 1 << 20)
+
+
+@pytest.mark.parametrize("per_block", [1, 4])
+@pytest.mark.parametrize("tokens", [1, 7, 255, 4096, 1 << 22, (1 << 22) + 1, 1 << 26, (1 << 26) + 5, 1 << 30])
+def test_append_grid(host, tokens, per_block):
+    """Every token has a block, the kernel's token numbers stay in 31 bits, and the launch is one that can be made."""
+    for rounds in (1, 3, 384):
+        x, y, z = grid(host.append_grid, tokens, per_block, rounds)
+        assert launchable((x, y, z)) and 1 <= y <= rounds
+        assert tokens <= x * z * per_block < 1 << 31 and (z == 1 or x == 1 << 20)
