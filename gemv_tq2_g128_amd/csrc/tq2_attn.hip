@@ -36,7 +36,7 @@
 //
 // Parts.  Long sequences are cut into parts of keys, one block each, whose states
 // join_kernel puts together.  Measured: 64 sequences of up to 8,192 tokens, bf16:
-// 234 us, 4.7 TB/s; 4 of up to 131,071, e4m3: 130 us, 5.6 TB/s; one token over 1,001
+// 188 us, 5.9 TB/s; 4 of up to 131,071, e4m3: 130 us, 5.6 TB/s; one token over 1,001
 // keys: 9.3 us in 8 parts, a chain of trips to memory (length, page, keys, parts).
 #include "tq2_attn_device.h"
 
@@ -115,9 +115,10 @@ __global__ __launch_bounds__(64 * W, (kMinWaves<D, MT>)) void stream_kernel(Attn
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
   const uint32_t group = a.group;
-  const int head = blockIdx.y % p.kv_heads;
-  const int split = blockIdx.x;
-  const int b = blockIdx.z;
+  const int head = blockIdx.x % p.kv_heads;
+  const int split = blockIdx.z;
+  const int b = blockIdx.y;
+  if (b >= p.batch) return;
   const Seq s = sequence(p, b);
   const uint32_t rows = uint32_t(s.q_len) * group;               // below 2^31
   const Parts parts = parts_of(s, a.window, a.splits, a.split_keys);
@@ -125,7 +126,7 @@ __global__ __launch_bounds__(64 * W, (kMinWaves<D, MT>)) void stream_kernel(Attn
   const int start = parts.base + split * parts.per;
   const int part_end = s.keys - start < parts.per ? s.keys : start + parts.per;
 
-  for (uint32_t row0 = blockIdx.y / p.kv_heads * (MT * 16); row0 < rows; row0 += gridDim.y / p.kv_heads * (MT * 16)) {
+  for (uint32_t row0 = blockIdx.x / p.kv_heads * (MT * 16); row0 < rows; row0 += gridDim.x / p.kv_heads * (MT * 16)) {
     // Keys of this part that any of the rows sees.
     const uint32_t live_rows = rows - row0 < MT * 16 ? rows - row0 : MT * 16;
     const int place_lo = s.first + int(row0 / group), place_hi = s.first + int((row0 + live_rows - 1) / group);
@@ -629,8 +630,8 @@ hipError_t launch_stream(const AttnArgs& a, const AttnPlan& plan, hipStream_t st
                                              hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(fn, dim3(plan.splits, plan.steps * a.pages.kv_heads, a.pages.batch), dim3(64 * W), lds,
-                     stream, a);
+  const Grid grid = stream_grid(plan, a.pages.kv_heads, a.pages.batch);
+  hipLaunchKernelGGL(fn, dim3(grid.x, grid.y, grid.z), dim3(64 * W), lds, stream, a);
   return hipGetLastError();
 }
 

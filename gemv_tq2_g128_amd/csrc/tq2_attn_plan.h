@@ -93,9 +93,6 @@ inline AttnPlan plan_attention(const tq2_paged_attention_args& a) {
         per = 128 * tiles;
       }
     }
-    // Sequences enough to fill the card by themselves, none so long that the others wait
-    // for it: nothing to join (64 of up to 8192 tokens: 239 us, 254 in parts of 1024).
-    if (blocks >= 512 && keys <= 8192) per = 8192;
   }
   splits = keys < 1 ? 1 : pieces(keys, per);
   if (splits > 512) splits = 512;
@@ -110,6 +107,17 @@ inline AttnPlan plan_attention(const tq2_paged_attention_args& a) {
 // Key heads vary fastest, then parts, then steps; sequences have an axis of their own.
 inline Grid tile_grid(const AttnPlan& plan, int64_t kv_heads, int64_t batch) {
   return Grid{uint32_t(kv_heads * plan.splits * plan.steps), uint32_t(batch), 1};
+}
+
+// Blocks of the streaming form: key heads (and row steps) along x, sequences along y, parts
+// along z.  Blocks go round the 8 dies and the 4 engines of each by their number, whether
+// they find work or not, and short sequences have fewer parts: with parts fastest, those of
+// 64 sequences of up to 8,192 tokens (one to eight parts) crowded the first dies (260 us in
+// parts of 1024 keys, 188 now; with all at 8,192 346 both ways).  The number of sequences is
+// rounded up to an odd one: 131,071 tokens beside three short sequences would leave all
+// blocks with work on one engine of each die (240 us, 113 now).
+inline Grid stream_grid(const AttnPlan& plan, int64_t kv_heads, int64_t batch) {
+  return Grid{uint32_t(plan.steps * kv_heads), uint32_t(plan.splits > 1 ? batch | 1 : batch), uint32_t(plan.splits)};
 }
 
 // Blocks numbered along x and then y, 2^20 to a row: block (y << kRowShift) + x, with no

@@ -24,6 +24,12 @@ extern "C" void tile_grid(int64_t splits, int64_t steps, int64_t kv_heads, int64
   const tq2::Grid g = tq2::tile_grid(p, kv_heads, batch);
   out[0] = g.x, out[1] = g.y, out[2] = g.z;
 }
+extern "C" void stream_grid(int64_t splits, int64_t steps, int64_t kv_heads, int64_t batch, int64_t* out) {
+  tq2::AttnPlan p{};
+  p.splits = int32_t(splits), p.steps = int32_t(steps);
+  const tq2::Grid g = tq2::stream_grid(p, kv_heads, batch);
+  out[0] = g.x, out[1] = g.y, out[2] = g.z;
+}
 extern "C" void append_grid(int64_t tokens, int64_t per_block, int64_t rounds, int64_t* out) {
   const tq2::Grid g = tq2::append_grid(tokens, per_block, rounds);
   out[0] = g.x, out[1] = g.y, out[2] = g.z;
@@ -81,7 +87,7 @@ def test_many_sequences_without_a_longest(host, batch, each, heads):
 
 
 def test_plans_in_range(host):
-    """Any sizes that a call accepts: the grid of the tiled form can be launched and the parts fit their fields."""
+    """Any sizes that a call accepts: the grid can be launched and the parts fit their fields."""
     rng = random.Random(3)
 
     def wide(most):
@@ -98,8 +104,7 @@ def test_plans_in_range(host):
                  batch=batch, tokens=tokens, cu_q=A, q_heads=q_heads, kv_heads=kv_heads, act_type=act, cache_type=cache,
                  head_dim=rng.choice([64, 96, 128, 192, 256]))
         assert p.steps >= 1 and 1 <= p.splits <= 512 and p.split_keys >= 128 and p.split_keys % 32 == 0
-        if p.tiled:
-            assert launchable(grid(host.tile_grid, p.splits, p.steps, kv_heads, batch))
+        assert launchable(grid(host.tile_grid if p.tiled else host.stream_grid, p.splits, p.steps, kv_heads, batch))
 
 
 @pytest.mark.parametrize("max_q", [1, 64, 5000])
@@ -127,3 +132,33 @@ def test_append_grid(host, tokens, per_block):
         x, y, z = grid(host.append_grid, tokens, per_block, rounds)
         assert launchable((x, y, z)) and 1 <= y <= rounds
         assert tokens <= x * z * per_block < 1 << 31 and (z == 1 or x == 1 << 20)
+
+
+@pytest.mark.parametrize("kv_heads", [1, 2, 8, 16])
+@pytest.mark.parametrize("lengths", [[8] + [1] * 63, [128] + [8] * 3, [64] + [1] * 15, [16, 1] * 8, list(range(1, 65)),
+                                     [32] * 4, [16] * 31, [512], [5, 4, 3, 2, 1]])
+def test_parts_spread_over_the_card(host, kv_heads, lengths):
+    """Blocks with work (part i of a sequence of more than i parts) are shared evenly by the places that a block's
+    number gives it: 8 dies of 32 CUs, and 4 engines in each; or there is a CU for each."""
+    splits, batch = max(lengths), len(lengths)
+    x, y, z = grid(host.stream_grid, splits, 1, kv_heads, batch)
+    assert (x, z) == (kv_heads, splits) and y >= batch
+    for places in (8, 32):
+        held = [0] * places
+        for b, count in enumerate(lengths):
+            for part in range(count):
+                for head in range(kv_heads):
+                    held[(head + x * (b + y * part)) % places] += 1
+        mean = sum(held) / places
+        assert max(held) <= max(1.35 * mean + 2, 256 / places), (places, held)
+
+
+def test_neighbours_are_cut_alike(host):
+    """No size is an exception: parts of a batch hardly longer, or of one sequence more, are hardly other parts."""
+    for batch in (48, 63, 64, 65, 80, 128, 256):
+        for keys in (4000, 6000, 8191, 8192, 8193, 12000, 16384, 40000):
+            here = Plan(host, 1, keys, batch=batch, tokens=batch, q_heads=32, kv_heads=8, act_type=BF16, cache_type=BF16)
+            for more, longer in ((1, 0), (0, 1), (-1, 0), (0, -1)):
+                there = Plan(host, 1, keys + longer, batch=batch + more, tokens=batch + more, q_heads=32, kv_heads=8,
+                             act_type=BF16, cache_type=BF16)
+                assert abs(here.splits - there.splits) <= 1, (batch, keys, here.splits, there.splits)
