@@ -55,6 +55,7 @@ inline AttnPlan plan_attention(const tq2_paged_attention_args& a) {
   const int64_t most = a.max_kv < kMaxKeys ? a.max_kv : kMaxKeys;
   const int64_t keys = span < most ? span : most;
   const int64_t blocks = c.batch * c.kv_heads * plan.steps;
+  const double joined = double(c.tokens) * double(c.q_heads) * double(c.head_dim + 4) * 8.0 / 3e6;  // us a part
   int64_t per, splits;
   if (plan.tiled) {
     // The number of parts with the least time: a block takes about 4.5 us to start and
@@ -65,7 +66,6 @@ inline AttnPlan plan_attention(const tq2_paged_attention_args& a) {
     const bool wide = c.act_type == TQ2_TYPE_F32;
     const int64_t slots = c.head_dim > 128 || (wide && c.head_dim > 64) ? 256 : 512;
     const double tile = 1.9 * double(c.head_dim) / 128.0 * (wide ? 2.0 : 1.0);
-    const double joined = double(c.tokens) * double(c.q_heads) * double(c.head_dim + 4) * 8.0 / 3e6;
     double least = 0.0;
     per = 128;
     for (int64_t parts = 1; parts <= 64; parts += parts < 4 ? 1 : parts / 2) {
@@ -80,19 +80,25 @@ inline AttnPlan plan_attention(const tq2_paged_attention_args& a) {
   } else {
     // 1, 2, 4 or 8 tiles of 32 keys for each of a block's four waves, by the least time:
     // two blocks fit on a CU, a block takes about 4.5 us to start and end and 1.4 us a
-    // tile, and joining parts takes 4 us and about 0.1 us a part (measured).  Longer
-    // parts leave CUs idle at the end of ragged batches: 4 sequences of up to 131,071
-    // tokens take 131 us with 1024 keys a part, 143 with 2048, 159 with 4096.
+    // tile, and joining parts takes 4 us and their way to memory and back at 3 TB/s
+    // (measured).  Longer parts leave CUs idle at the end of ragged batches: 16 sequences of
+    // up to 16,000 tokens take 102 us with 1024 keys a part, 113 with 2048, 129 with 4096.
     double least = 0.0;
     per = 128;
     for (int64_t tiles = 1; tiles <= 8; tiles *= 2) {
-      const int64_t parts = pieces(keys, 128 * tiles), rounds = pieces(blocks * (parts < 1 ? 1 : parts), 512);
-      const double time = double(rounds) * (4.5 + 1.4 * double(tiles)) + (parts > 1 ? 4.0 + 0.1 * double(parts) : 0.0);
+      const int64_t parts = keys < 1 ? 1 : pieces(keys, 128 * tiles), rounds = pieces(blocks * parts, 512);
+      const double time = double(rounds) * (4.5 + 1.4 * double(tiles)) + (parts > 1 ? 4.0 + joined * double(parts) : 0.0);
       if (tiles == 1 || time < least) {
         least = time;
         per = 128 * tiles;
       }
     }
+    // No more than a dozen blocks for each place on the card, which bounds the parts'
+    // memory: ragged batches' ends even out by themselves there (1,024 sequences of up to
+    // 2,048 tokens whole 684 us, in two parts 705, all of that length 1301 and 1380; 128 of
+    // up to 8,192 in parts of 1408 keys 358, of 1024 341, all of that length 645 and 647).
+    const int64_t dozen = 12 * 512 / blocks, each = pieces(pieces(keys, dozen < 1 ? 1 : dozen), 128) * 128;
+    if (per < each) per = each;
   }
   splits = keys < 1 ? 1 : pieces(keys, per);
   if (splits > 512) splits = 512;

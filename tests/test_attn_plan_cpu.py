@@ -162,3 +162,13 @@ def test_neighbours_are_cut_alike(host):
                 there = Plan(host, 1, keys + longer, batch=batch + more, tokens=batch + more, q_heads=32, kv_heads=8,
                              act_type=BF16, cache_type=BF16)
                 assert abs(here.splits - there.splits) <= 1, (batch, keys, here.splits, there.splits)
+
+
+@pytest.mark.parametrize("max_kv", [8192, 131072, 1 << 20])
+@pytest.mark.parametrize("batch", [1, 16, 256, 1024, 4096, 65535])
+def test_memory_of_the_parts(host, batch, max_kv):
+    """However long the table says that sequences may be, a decode step's parts take no more than a dozen blocks'
+    states for each of the card's 512 places (26 MB for 8 rows of 128 components)."""
+    p = Plan(host, 1, max_kv, batch=batch, tokens=batch, q_heads=64, kv_heads=8, act_type=BF16, cache_type=BF16)
+    assert p.workspace <= 12 * 512 * 8 * 132 * 4
+    assert p.splits > 1 or batch * 8 * 2 > 12 * 512
