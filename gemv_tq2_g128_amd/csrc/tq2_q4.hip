@@ -210,7 +210,8 @@ __device__ __forceinline__ float scale_of(const Codes<G, N>& c, int j, int s) {
 }
 
 // One 128-wide block of K (block j of c): the codes' four matrix steps against x, scaled
-// into acc (rows 4 g4 + r of x, weight row r16).
+// into acc (rows 4 g4 + r of x, weight row r16).  The weight scale meets the sum before the
+// power of two does: their product alone would leave the normal numbers for x below 2^-113.
 template <int G, int MT, int N>
 __device__ __forceinline__ void multiply(Codes<G, N>& c, int j, const half8_t* __restrict__ a, const float4_t& back,
                                          int cols, float (&acc)[4]) {
@@ -228,7 +229,7 @@ __device__ __forceinline__ void multiply(Codes<G, N>& c, int j, const half8_t* _
     if (whole) {
       const float d = scale_of<G, N>(c, j, s);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(d * back[r], sum[r], acc[r]);
+      for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(d * sum[r], back[r], acc[r]);
     }
   }
 }
