@@ -35,7 +35,10 @@ extern "C" {
  * binary16); x, residual, out: 16-byte aligned.
  * Accuracy: weights and scales exact, x split into two binary16 parts under a
  * power of two per row and 128 columns, f32 sums: within 1e-5 * (sum_k |x w| +
- * |residual|).  A row of x with a non-finite value gives non-finite or NaN
+ * |residual|) + 2^-38 * sum_k X_k |w|, with X_k the largest |x| of k's 128
+ * columns (128 j .. 128 j + 127).  The second term counts where a column far
+ * above the others, by 2^16 and more, meets weights of almost zero.  Below 1e-33
+ * there is 2^-151 * sum_k |w| besides, and the steps of subnormal results.  A row of x with a non-finite value gives non-finite or NaN
  * outputs for that row alone.
  * m == 0 or n == 0 is a no-op.  Errors: INVALID (null pointer, size out of
  * range, m > TQ2_Q4_MAX_M, another group), SHAPE (k not a multiple of 128),

@@ -2,7 +2,8 @@
 
 Tolerance: 1e-5 * S as in test_q4_gpu.py (one rounding more, of scale times sum: 151 * 2^-24 = 9e-6), and where numbers
 are not normal, half the least step of f32, 2^-150, for each group and join that is added up, and half the least step of
-binary16 times the least power of two, 2^-25 * 2^-126, for each x.
+binary16 times the least power of two, 2^-25 * 2^-126, for each x.  An x far below the largest of its 128 columns keeps
+an error of 2^-25, half the least step of binary16, under a power of two that takes the largest to 2^13 at least: 2^-38 of it.
 """
 
 import numpy as np
@@ -43,3 +44,26 @@ def test_huge_rows(q4, group):  # noqa: F811
     ref, s = expected(c)
     y = q4.gemv(dev(c["codes"]), dev(c["scales"]), dev(c["x"])).cpu().numpy().astype(np.float64)
     assert np.all(np.abs(y - ref) <= TOL * s)
+
+
+@pytest.mark.parametrize("m", [2, 16])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_columns_far_above_the_others(q4, m, group):  # noqa: F811
+    """A column of 1e8 that adds nothing, because its weights or its group's scale are zero, and one that does."""
+    k, n = 512, 60
+    c = make(m + group, m, n, k, group)
+    c["x"][:, 5] = 1e8                                             # its codes are 8
+    c["codes"][:, 2] = c["codes"][:, 2] & 15 | 8 << 4
+    c["x"][:, 128 + 7] = -1e9                                      # its group's scale is zero
+    c["scales"][:, 128 // group] = 0
+    c["x"][1:, 300] = 1e6
+    ref, s = expected(c)
+    w = np.empty((n, k))
+    w[:, 0::2], w[:, 1::2] = (c["codes"] & 15) - 8.0, (c["codes"] >> 4) - 8.0
+    w = np.abs(w * np.repeat(c["scales"].astype(np.float64), group, axis=1))
+    top = np.abs(c["x"].astype(np.float64)).reshape(m, -1, 128).max(2).repeat(128, 1)
+    tol = TOL * s + 2.0 ** -38 * (top @ w.T)
+    y = q4.gemv(dev(c["codes"]), dev(c["scales"]), dev(c["x"])).cpu().numpy().astype(np.float64)
+    err = np.abs(y - ref)
+    print("far m%d g%d worst err / tol %.3f, err / S %.3g" % (m, group, (err / tol).max(), (err / s).max()), flush=True)
+    assert np.all(err <= tol)
