@@ -32,7 +32,9 @@ extern "C" {
  * be the same pointer as residual and must overlap nothing else.
  * group: 32, 64 or 128; k a multiple of 128 (and at most 2^21).
  * codes: 16-byte aligned; scales: 16-byte aligned (rows of k / group
- * binary16); x, residual, out: 16-byte aligned.
+ * binary16), readable up to a multiple of 4 bytes: with an odd number of them
+ * the two bytes after the last are loaded with it, whatever they hold; x,
+ * residual, out: 16-byte aligned.
  * Accuracy: weights and scales exact, x split into two binary16 parts under a
  * power of two per row and 128 columns, f32 sums: within 1e-5 * (sum_k |x w| +
  * |residual|) + 2^-38 * sum_k X_k |w|, with X_k the largest |x| of k's 128

@@ -67,3 +67,16 @@ def test_columns_far_above_the_others(q4, m, group):  # noqa: F811
     err = np.abs(y - ref)
     print("far m%d g%d worst err / tol %.3f, err / S %.3g" % (m, group, (err / tol).max(), (err / s).max()), flush=True)
     assert np.all(err <= tol)
+
+
+@pytest.mark.parametrize("n", [1, 5, 65541])
+@pytest.mark.parametrize("k", [128, 1152])
+def test_what_follows_the_scales_takes_no_part(q4, n, k):  # noqa: F811
+    """An odd number of scales: the last is loaded with the two bytes after it, here NaN."""
+    c = make(n + k, 3, n, k, 128)
+    count = n * (k // 128)
+    held = torch.full((count + 64,), float("nan"), dtype=torch.float16, device="cuda")
+    held[:count] = dev(c["scales"]).flatten()
+    y = q4.gemv(dev(c["codes"]), held[:count].reshape(n, k // 128), dev(c["x"])).cpu().numpy().astype(np.float64)
+    ref, s = expected(c)
+    assert np.all(np.abs(y - ref) <= TOL * s)
