@@ -39,6 +39,30 @@ size_t extent(int64_t bytes, int64_t dim, int64_t n0, int64_t s0, int64_t n1, in
   return size_t(all < most ? all : most);
 }
 
+// Whether no two of the `dim` elements at i * s0 + j * s1, i < n0, j < n1, overlap.
+bool apart(int64_t dim, int64_t n0, int64_t s0, int64_t n1, int64_t s1) {
+  if (s0 < s1) std::swap(s0, s1), std::swap(n0, n1);
+  if ((n0 > 1 && s0 < dim) || (n1 > 1 && s1 < dim)) return false;
+  if (n0 <= 1 || n1 <= 1) return true;
+  // Rows i apart along s0 lie within the other axis' reach for few i: at most n1.
+  const __int128 reach = __int128(n1 - 1) * s1 + dim;
+  for (int64_t i = 1; i < n0 && __int128(i) * s0 < reach; ++i) {
+    const __int128 off = __int128(i) * s0;
+    const int64_t j = int64_t(off / s1), past = int64_t(off % s1);
+    if (past < dim || (j + 1 < n1 && s1 - past < dim)) return false;
+  }
+  return true;
+}
+
+// Whether neighbours along an axis of a cache overlap.
+bool cache_apart(const tq2_paged_cache& c) {
+  const int64_t d = c.head_dim;
+  const auto ok = [&](int64_t page, int64_t head, int64_t token) {
+    return (c.pages <= 1 || page >= d) && (c.kv_heads <= 1 || head >= d) && (c.page <= 1 || token >= d);
+  };
+  return ok(c.k_page_stride, c.k_head_stride, c.k_token_stride) && ok(c.v_page_stride, c.v_head_stride, c.v_token_stride);
+}
+
 // Sizes and types of the cache; nothing is dereferenced.
 int check_cache_sizes(const tq2_paged_cache& c) {
   if (!size_ok(c.batch, 0, TQ2_ATTN_MAX_BATCH) || !size_ok(c.tokens, 0, kMaxDim) ||
@@ -195,6 +219,8 @@ int tq2_kv_append(const tq2_kv_append_args* args, void* stream) {
   if (a.q && !in_place &&
       (overlaps(a.q_out, ob, a.q, qb) || overlaps(a.q_out, ob, a.k, kb) || overlaps(a.q_out, ob, a.v, vb)))
     return TQ2_ERR_ALIAS;
+  if (!cache_apart(c) || (a.q && !apart(d, c.tokens, a.q_out_token_stride, c.q_heads, a.q_out_head_stride)))
+    return TQ2_ERR_ALIAS;
   st = check_device();
   if (st != TQ2_OK) return st;
   tq2::AppendArgs g;
@@ -262,6 +288,7 @@ int tq2_paged_attention(const tq2_paged_attention_args* args, void* stream) {
   const size_t ob = extent(ab, d, c.tokens, a.out_token_stride, c.q_heads, a.out_head_stride);
   const bool in_place = a.out == a.q && a.out_token_stride == a.q_token_stride && a.out_head_stride == a.q_head_stride;
   if (!in_place && overlaps(a.out, ob, a.q, qb)) return TQ2_ERR_ALIAS;
+  if (!apart(d, c.tokens, a.out_token_stride, c.q_heads, a.out_head_stride)) return TQ2_ERR_ALIAS;
   for (const auto& cache : {std::make_pair(c.k, k_extent(c)), std::make_pair(c.v, v_extent(c))})
     if (overlaps(cache.first, cache.second, a.out, ob) ||
         overlaps(cache.first, cache.second, a.workspace, plan.workspace))

@@ -101,7 +101,8 @@ typedef struct tq2_kv_append_args {
  * a pair of types or head_dim that is not listed, sections that do not sum to
  * rot / 2), SHAPE (page not a power of two, rot not a multiple of 8, q_heads
  * not a multiple of kv_heads), ALIGN, ALIAS (q_out or a cache overlaps another
- * operand), DEVICE, LAUNCH. */
+ * operand, rows of q_out overlap each other or neighbours along an axis of a
+ * cache do), DEVICE, LAUNCH. */
 int tq2_kv_append(const tq2_kv_append_args* args, void* stream);
 
 typedef struct tq2_paged_attention_args {
@@ -139,7 +140,8 @@ size_t tq2_paged_attention_workspace_bytes(const tq2_paged_attention_args* args)
  * needs no preparation and means nothing afterwards.
  * tokens == 0 or batch == 0 is a no-op.  Errors: INVALID (null pointer, size out of range, a
  * workspace that is too small, types or head_dim not listed), SHAPE, ALIGN,
- * ALIAS (out overlaps a cache, the workspace or a part of q), DEVICE, LAUNCH. */
+ * ALIAS (out overlaps a cache, the workspace or a part of q, or rows of out
+ * overlap each other), DEVICE, LAUNCH. */
 int tq2_paged_attention(const tq2_paged_attention_args* args, void* stream);
 
 #ifdef __cplusplus
