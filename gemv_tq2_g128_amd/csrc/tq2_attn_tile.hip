@@ -67,11 +67,16 @@ struct Place {
 
 // 16 bytes a lane from base + off to LDS at + 16 * lane; past the range: zeros.  The
 // compiler does not see the load: the five wait states that it would put between a
-// vector instruction's write of a resource word (a lane read) and the load are here.
+// vector instruction's write of a resource word (a lane read) and the load are here.  m0 is
+// named as written: the compiler keeps no value there (hence its warning), but must not
+// move this between a write of its own and the use.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_to_lds(rsrc_t r, uint32_t off, uint32_t at) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               ::"s"(at), "v"(off), "s"(r) : "memory");
+               ::"s"(at), "v"(off), "s"(r) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 // The larger of two; NaN if one is (fmaxf would first quiet its operands).
 __device__ __forceinline__ float largest(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
