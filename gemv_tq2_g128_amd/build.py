@@ -3,7 +3,9 @@
 Usage: ``python -m gemv_tq2_g128_amd.build`` or ``build()`` from Python.
 """
 
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -46,12 +48,22 @@ BINDING_SOURCE = "tq2_binding.cpp"
 
 def build(verbose: bool = False) -> str:
     """Compile every HIP source into ``libtq2.so`` (and the benchmark's
-    reference kernels into ``libtq2_probe.so``, the tensor marshalling into
-    ``_binding.so``); returns the library path."""
+    reference kernels into ``libtq2_probe.so``); returns the library path.
+    Where PyTorch is installed, the tensor marshalling of ``attn`` and ``q4``
+    is compiled into ``_binding.so`` as well; the C ABI does without it."""
     _compile(PROBE_SOURCES, PROBE_LIB_NAME, verbose)
     lib = _compile(SOURCES, LIB_NAME, verbose)
-    _compile_binding(verbose)
+    if importlib.util.find_spec("torch") is not None:
+        _compile_binding(verbose)
+    else:
+        print("PyTorch is not installed: %s is left out" % BINDING_NAME, flush=True)
     return lib
+
+
+def host_compiler():
+    """g++, or the clang++ that hipcc itself comes with."""
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    return shutil.which("g++") or os.path.join(rocm, "llvm", "bin", "clang++")
 
 
 def _compile_binding(verbose):
@@ -63,7 +75,7 @@ def _compile_binding(verbose):
     tmp = out + ".tmp%d" % os.getpid()
     includes = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                 os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]
-    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+    _run([host_compiler(), "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
           *("-I" + i for i in includes), os.path.join(CSRC, BINDING_SOURCE), "-o", tmp,
           "-L" + PKG_DIR, "-l:" + LIB_NAME, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu",
