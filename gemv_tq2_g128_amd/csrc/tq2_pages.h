@@ -50,7 +50,8 @@ TQ2_HD Seq sequence(const Pages& p, int32_t b) {
   hi = hi < lo ? lo : (hi > p.tokens ? p.tokens : hi);
   s.q0 = lo;
   s.q_len = hi - lo;
-  s.first = int32_t(int64_t(len) - (int64_t(end) - lo));
+  const int64_t first = int64_t(len) - (int64_t(end) - lo);  // at most len
+  s.first = first < INT32_MIN ? INT32_MIN : int32_t(first);
   int64_t room = int64_t(p.cols) << p.page_shift;
   if (room > kMaxKeys) room = kMaxKeys;
   s.keys = len < 0 ? 0 : (len > room ? int32_t(room) : len);
