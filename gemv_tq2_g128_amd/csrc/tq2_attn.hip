@@ -533,9 +533,8 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
   const Pages& p = a.pages;
   const int lane = threadIdx.x % L, g = threadIdx.x / L % G;
   const uint32_t row = ((blockIdx.y << kRowShift) + blockIdx.x) * kRows + threadIdx.x / (L * G);
-  // Rows past the last one: no token.
-  const bool there = row < uint32_t(p.tokens) * uint32_t(p.q_heads);
-  const int token = there ? int(row / uint32_t(p.q_heads)) : p.tokens, qh = int(row % uint32_t(p.q_heads));
+  const uint32_t tokens = uint32_t(p.tokens), token = row / uint32_t(p.q_heads);  // rows past the last one: no token
+  const int qh = int(row % uint32_t(p.q_heads));
   const float* part = a.part + int64_t(row) * a.splits * (D + 4);
   const int c = lane * 4;
   // Parts are read kBatch at a time, the first ones before it is known how many the row
@@ -550,7 +549,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
       pm[j] = kNone;
       ps[j] = 0.f;
       py[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      if (i < a.splits && token < p.tokens && c < D) {
+      if (i < a.splits && token < tokens && c < D) {
         const float* at = part + i * (D + 4);
         pm[j] = at[0];
         ps[j] = at[1];
@@ -563,14 +562,14 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
   constexpr int kPerWave = G == 1 ? 64 / L : 1;                  // rows of a wave
 #pragma unroll
   for (int i = 0; i < kPerWave; ++i) {
-    const int t = __builtin_amdgcn_readlane(token, i * L);
-    const int of = t < p.tokens ? owner(p, t) : p.batch;
+    const uint32_t t = __builtin_amdgcn_readlane(token, i * L);
+    const int of = t < tokens ? owner(p, int(t)) : p.batch;
     if (kPerWave == 1 || int(threadIdx.x & 63) / L == i) b = of;
   }
-  bool live = token < p.tokens && b < p.batch;
+  bool live = token < tokens && b < p.batch;
   if (live) {
     const Seq s = sequence(p, b);
-    live = token >= s.q0 && token < s.q0 + s.q_len;
+    live = int(token) >= s.q0 && int(token) < s.q0 + s.q_len;
     parts = live ? parts_of(s, a.window, a.splits, a.split_keys).count : 0;
   }
   float m = kNone, base = 0.f, sum = 0.f;
