@@ -86,7 +86,8 @@ int check_cache_sizes(const tq2_paged_cache& c) {
 
 // Pointers and strides of the cache.
 int check_cache_arrays(const tq2_paged_cache& c) {
-  if (!c.table || !c.kv_len || (c.pages > 0 && (!c.k || !c.v))) return TQ2_ERR_INVALID;
+  // An empty array has no address.
+  if ((c.table_cols > 0 && !c.table) || !c.kv_len || (c.pages > 0 && (!c.k || !c.v))) return TQ2_ERR_INVALID;
   const bool narrow = c.cache_type == TQ2_TYPE_E4M3;
   if (narrow != (c.k_scale != nullptr) || narrow != (c.v_scale != nullptr)) return TQ2_ERR_INVALID;
   const int64_t cb = type_bytes(c.cache_type);

@@ -52,7 +52,7 @@ typedef struct tq2_paged_cache {
   void* v;
   const float* k_scale;      /* f32 [kv_heads]: 8-bit caches only, else NULL */
   const float* v_scale;
-  const int32_t* table;      /* [batch, table_cols], rows table_stride apart */
+  const int32_t* table;      /* [batch, table_cols], rows table_stride apart; NULL if it has no columns */
   const int32_t* kv_len;     /* [batch] */
   const int32_t* cu_q;       /* [batch + 1] or NULL */
   int64_t batch;
