@@ -21,8 +21,8 @@
 // an eighth of the 128-wide blocks, and the eight partial sums meet in LDS.
 // q4_tall_kernel, for many rows, gives each wave tiles of 16 rows and all of K, with
 // no barrier.  Both have the next step's codes in flight before the present one is
-// computed.  131072 x 4096, eight rows of x: 64 us (4.4 TB/s, 48 us without the
-// arithmetic and the scales); 4096 x 4096, one row: 5.3 us, most of it the launch
+// computed.  131072 x 4096, eight rows of x: 63 us (4.5 TB/s, 48 us without the
+// arithmetic and the scales); 4096 x 4096, one row: 5.2 us, most of it the launch
 // and one trip to memory after another.
 //
 // Groups.  A lane's 16 bytes are 32 consecutive weights.  For group 128 any
@@ -423,10 +423,13 @@ template <int G, int MT>
 hipError_t launch(const Q4Args& a, hipStream_t stream) {
   const int all_kb = int(a.k >> 7);
   const int pass_kb = MT == 8 ? kWaves * kMaxKb : kWaves * kMaxKb / 2;
-  // Rows over the waves once there are two tiles for each of 2048 waves: 131072 x 4096 takes
-  // 62 us at one row of x (67 with K split) and 69 us at eight (82), 65536 x 4096 38 (37) and
-  // 39 (44), 32768 x 4096 in groups of 32 27 (24) and 31 (31).
-  const bool tall = a.n >= 65536;
+  // Rows over the waves once there are two tiles for each of 2048 waves; for four rows of x
+  // or fewer, where two blocks on a CU hide each other's joins, once there are eight.  K split
+  // and rows over the waves, K = 4096 in groups of 128 (us): 65536 rows, one of x 31.5 and 34.1,
+  // eight 39.3 and 35.8; 131072, one 58.7 and 58.1, four 63.9 both ways, eight 71.0 and 64.2; 200000,
+  // one 91.0 and 91.5, four 97.5 and 100.5; 262144, one 119.3 and 108.9, four 124.0 and 119.7.
+  // 49152 rows, eight of x: 31.5 and 34.3.
+  const bool tall = a.n >= (a.m > 4 ? 65536 : 262144);
   const size_t lds = Shape<MT>::bytes(all_kb < pass_kb ? all_kb : pass_kb, int(a.m), !tall);
   const int64_t tiles = (a.n + 15) / 16, steps = tall ? (tiles + kWaves - 1) / kWaves : tiles;
   const int per_cu = lds <= 80 * 1024 ? 2 : 1;
