@@ -37,7 +37,7 @@
 // Parts.  Long sequences are cut into parts of keys, one block each, whose states
 // join_kernel puts together.  Measured: 64 sequences of up to 8,192 tokens, bf16:
 // 188 us, 5.9 TB/s; 4 of up to 131,071, e4m3: 130 us, 5.6 TB/s; one token over 1,001
-// keys: 9.3 us in 8 parts, a chain of trips to memory (length, page, keys, parts).
+// keys: 9.6 us in 8 parts, a chain of trips to memory (length, page, keys, parts).
 #include "tq2_attn_device.h"
 
 namespace tq2 {

