@@ -54,7 +54,26 @@ bool apart(int64_t dim, int64_t n0, int64_t s0, int64_t n1, int64_t s1) {
   return true;
 }
 
-// Whether neighbours along an axis of a cache overlap.
+// Whether rows of two [tokens, heads, dim] arrays whose extents overlap meet; a and b are
+// taken as columns of one array (equal token strides), otherwise as meeting.  All in bytes.
+bool rows_meet(int64_t tokens, int64_t wide, const void* a, int64_t a_heads, int64_t a_token, int64_t a_head,
+               const void* b, int64_t b_heads, int64_t b_token, int64_t b_head) {
+  const int64_t period = tokens > 1 ? a_token : int64_t(1) << 62;
+  if (tokens > 1 && (a_token != b_token || a_token <= 0)) return true;
+  const int64_t from = int64_t(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  const auto place = [&](int64_t off) { return (off % period + period) % period; };
+  // Heads of b all past those of a within a token's row.
+  const __int128 a_end = __int128(a_heads - 1) * a_head + wide, b_span = __int128(b_heads - 1) * b_head + wide;
+  if (place(from) >= a_end && place(from) + b_span <= period) return false;
+  for (int64_t i = 0; i < a_heads; ++i)
+    for (int64_t j = 0; j < b_heads; ++j) {
+      const int64_t off = place(from + j * b_head - i * a_head);
+      if (off < wide || period - off < wide) return true;
+    }
+  return false;
+}
+
+// Whether neighbours along each axis of a cache lie apart.
 bool cache_apart(const tq2_paged_cache& c) {
   const int64_t d = c.head_dim;
   const auto ok = [&](int64_t page, int64_t head, int64_t token) {
@@ -214,11 +233,18 @@ int tq2_kv_append(const tq2_kv_append_args* args, void* stream) {
     if (overlaps(cache.first, cache.second, a.q, qb) || overlaps(cache.first, cache.second, a.k, kb) ||
         overlaps(cache.first, cache.second, a.v, vb) || overlaps(cache.first, cache.second, a.q_out, ob))
       return TQ2_ERR_ALIAS;
-  // In place, q_out's extent is q's own, which k and v may share as columns of one array.
+  // In place, q_out's extent is q's own, which k and v may share as other columns of one array.
   const bool in_place = a.q_out == a.q && a.q_out_token_stride == a.q_token_stride &&
                         a.q_out_head_stride == a.q_head_stride;
   if (a.q && !in_place &&
       (overlaps(a.q_out, ob, a.q, qb) || overlaps(a.q_out, ob, a.k, kb) || overlaps(a.q_out, ob, a.v, vb)))
+    return TQ2_ERR_ALIAS;
+  const auto meets_q = [&](const void* in, size_t bytes, int64_t token, int64_t head) {
+    return overlaps(a.q, qb, in, bytes) && rows_meet(c.tokens, d * ab, a.q, c.q_heads, a.q_token_stride * ab,
+                                                     a.q_head_stride * ab, in, c.kv_heads, token * ab, head * ab);
+  };
+  if (a.q && in_place && (meets_q(a.k, kb, a.k_token_stride, a.k_head_stride) ||
+                          meets_q(a.v, vb, a.v_token_stride, a.v_head_stride)))
     return TQ2_ERR_ALIAS;
   if (!cache_apart(c) || (a.q && !apart(d, c.tokens, a.q_out_token_stride, c.q_heads, a.q_out_head_stride)))
     return TQ2_ERR_ALIAS;

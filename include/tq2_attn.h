@@ -75,7 +75,7 @@ typedef struct tq2_kv_append_args {
   const void* q;             /* [tokens, q_heads, head_dim], or NULL: k and v only */
   const void* k;             /* [tokens, kv_heads, head_dim] */
   const void* v;
-  void* q_out;               /* may be q itself (same strides) */
+  void* q_out;               /* may be q itself (same strides), k and v other columns of its array */
   int64_t q_token_stride, q_head_stride;
   int64_t k_token_stride, k_head_stride;
   int64_t v_token_stride, v_head_stride;
