@@ -13,7 +13,7 @@ Q = A + 4 * G
 
 
 def in_place(**over):
-    return append(**{**dict(q=Q, q_out=Q, q_ts=1024, o_ts=1024, k_ts=1024, v_ts=1024, k_new=Q + 2048, v_new=Q + 3072),
+    return append(**{**dict(q=Q, q_out=Q, q_ts=1024, o_ts=1024, k_ts=1024, v_ts=1024, k_new=Q + 2048, v_new=Q + 2048 + 1024),
                      **over})
 
 
