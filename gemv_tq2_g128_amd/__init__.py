@@ -6,5 +6,7 @@
   importing it raises if the library has not been built;
 * ``q4``      -- 4-bit matrix-vector products with group scales (``include/tq2_q4.h``);
 * ``attn``    -- the paged key/value cache: appending with rotation, and
-  attention over it (``include/tq2_attn.h``).
+  attention over it (``include/tq2_attn.h``);
+* ``moe``     -- mixtures of experts: the router, and the chosen experts'
+  feed-forward on 4-bit or ternary weights (``include/tq2_moe.h``).
 """
