@@ -8,5 +8,7 @@
 * ``attn``    -- the paged key/value cache: appending with rotation, and
   attention over it (``include/tq2_attn.h``);
 * ``moe``     -- mixtures of experts: the router, and the chosen experts'
-  feed-forward on 4-bit or ternary weights (``include/tq2_moe.h``).
+  feed-forward on 4-bit or ternary weights (``include/tq2_moe.h``);
+* ``sampling`` -- the next token from logits: temperature, top-k, min-p and
+  top-p (``include/tq2_sample.h``).
 """

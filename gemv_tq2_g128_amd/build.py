@@ -18,7 +18,8 @@ INCLUDE = os.path.join(os.path.dirname(PKG_DIR), "include")
 LIB_NAME = "libtq2.so"
 SOURCES = ["tq2_api.hip", "tq2_reformat.hip", "tq2_gemv.hip", "tq2_gemm.hip", "tq2_q4.hip",
            "tq2_kv_append.hip", "tq2_attn.hip", "tq2_attn_tile.hip",
-           "tq2_layer_api.hip", "tq2_route.hip", "tq2_moe.hip", "tq2_moe_api.hip"]
+           "tq2_layer_api.hip", "tq2_route.hip", "tq2_moe.hip", "tq2_moe_api.hip",
+           "tq2_sample.hip", "tq2_sample_api.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -1,5 +1,5 @@
 // Python module `_binding`: torch tensors into the argument structs of tq2_attn.h,
-// tq2_q4.h and tq2_moe.h, and the call on the tensors' device and its current stream.
+// tq2_q4.h, tq2_moe.h and tq2_sample.h, and the call on the tensors' device and its current stream.
 //
 // A decode step makes a handful of these calls on small tensors, whose kernels
 // take 3 to 10 us: reading the tensors' types, shapes and strides from Python
@@ -22,6 +22,7 @@
 #include "tq2_attn.h"
 #include "tq2_moe.h"
 #include "tq2_q4.h"
+#include "tq2_sample.h"
 
 namespace {
 
@@ -458,6 +459,50 @@ PyObject* moe_experts(PyObject* const* args) {
   return made.defined() ? THPVariable_Wrap(made) : new_ref(args[9]);
 }
 
+// A setting of a row: a number for all rows, or a tensor of one for each.
+template <class T>
+const T* setting(const Device& dev, PyObject* o, at::ScalarType type, int64_t rows, const char* what) {
+  return THPVariable_Check(o) ? dev.plain<const T>(&THPVariable_Unpack(o), type, rows, what) : nullptr;
+}
+
+PyObject* sample(PyObject* const* args) {
+  const at::Tensor &logits = tensor(args[0], "logits"), &u = tensor(args[1], "u");
+  if (logits.dim() != 2) refuse("logits must be [rows, vocab]");
+  const Device dev(logits, "logits");
+  tq2_sample_args a{};
+  a.rows = logits.size(0);
+  a.vocab = logits.size(1);
+  a.row_stride = a.rows > 1 ? logits.stride(0) : a.vocab;
+  if (a.vocab > 1 && logits.stride(1) != 1) refuse("logits must have contiguous rows");
+  a.logits_type = act_type_of(logits, "logits");
+  a.logits = logits.data_ptr();
+  a.u = dev.plain<const float>(&u, at::kFloat, a.rows, "u");
+  a.temperatures = setting<float>(dev, args[2], at::kFloat, a.rows, "temperature");
+  if (!a.temperatures) a.temperature = real(args[2], "temperature");
+  a.top_ks = setting<int32_t>(dev, args[3], at::kInt, a.rows, "top_k");
+  if (!a.top_ks) a.top_k = integer(args[3], "top_k");
+  a.top_ps = setting<float>(dev, args[4], at::kFloat, a.rows, "top_p");
+  if (!a.top_ps) a.top_p = real(args[4], "top_p");
+  a.min_ps = setting<float>(dev, args[5], at::kFloat, a.rows, "min_p");
+  if (!a.min_ps) a.min_p = real(args[5], "min_p");
+  const at::Tensor* out = maybe(args[6], "out");
+  at::Tensor made, workspace;
+  if (!out) {
+    made = at::empty({a.rows}, logits.options().dtype(at::kInt));
+    out = &made;
+  }
+  a.ids = dev.plain<int32_t>(out, at::kInt, a.rows, "out");
+  a.logprob = dev.plain<float>(maybe(args[7], "logprob"), at::kFloat, a.rows, "logprob");
+  a.workspace_bytes = int64_t(tq2_sample_workspace_bytes(&a));
+  if (a.workspace_bytes > 0) {
+    workspace = at::empty({a.workspace_bytes}, logits.options().dtype(at::kByte));
+    a.workspace = workspace.data_ptr();
+  }
+  const int status = dev.launch([&](void* stream) { return tq2_sample(&a, stream); });
+  if (status != TQ2_OK) return PyLong_FromLong(status);
+  return made.defined() ? THPVariable_Wrap(made) : new_ref(args[6]);
+}
+
 // An entry with `count` positional arguments; no C++ exception leaves it.
 template <PyObject* (*body)(PyObject* const*), int count>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -498,6 +543,8 @@ PyMethodDef methods[] = {
      "x, weight, top_k, bias, scoring, renormalize, scale, weights, ids -> (weights, ids), or a status"},
     {"moe_experts", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<moe_experts, 10>)), METH_FASTCALL,
      "x, gate_up, its scales, down, its scales, ids, weights, experts, residual, out -> out, or a status"},
+    {"sample", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<sample, 8>)), METH_FASTCALL,
+     "logits, u, temperature, top_k, top_p, min_p, out, logprob -> out, or a status"},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
