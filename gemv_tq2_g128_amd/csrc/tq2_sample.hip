@@ -2,17 +2,18 @@
 //
 // Order.  All truncations keep a run from the top of the order (logit falling, index rising), and so does the draw: the
 // token is where the running sum of e = exp((l - max) / T), from the top, passes u times the kept sum.  So nothing is
-// sorted: a histogram over the logits' range, of counts and of sums, says in which bin the k-th token, the end of top-p's
-// run or the drawn one lies, and only that bin's few tokens are put in order.
+// sorted: a histogram over the logits, of counts and of sums, says in which bin the k-th token, the end of top-p's run
+// or the drawn one lies, and only that bin's tokens are put in order.
 //
-// Whole numbers.  e is computed in f64 and rounded to a multiple of 2^-43; sums are then u64, exact in any order, which
-// is what makes LDS atomics allowed here and the result one that repeats.  (32-bit exponentials would give another token
-// than the definition once in a few dozen draws over 10^5 tokens: that many borders lie within 1e-7 of u.)
+// Whole numbers.  e is computed in f64 and rounded to a multiple of 2^-43 of the largest of its chunk; sums are then
+// u64, exact in any order, which is what makes LDS atomics allowed here and the result one that repeats.  (32-bit
+// exponentials would give another token than the definition once in a few dozen draws over 10^5 tokens: that many
+// borders lie within 1e-7 of u.)
 //
-// Three launches.  max_kernel and bins_kernel: blocks for chunks of each row, so that one row uses many CUs;
-// choice_kernel: a block for each row, which joins the chunks' bins and reads only those chunks again that have tokens in
-// a bin it needs.  Bound: logits are read from HBM once (the second time from the caches); the f64 exponential costs about
-// 17 instructions an element, which is as long as the read.
+// Two launches.  bins_kernel: blocks for chunks of each row, held in registers: their largest logit, then counts and sums
+// in bins of a fixed grid (11 to a factor of two in e, so that chunks agree on them).  choice_kernel: a block for each
+// row, which joins the chunks' bins at the row's largest logit and reads again only those chunks that have tokens in a bin
+// it needs.  Bound: logits are read from HBM once, and mostly a second time from the caches.
 #include "tq2_device.h"
 #include "tq2_sample_internal.h"
 #include "tq2_types.h"
@@ -22,12 +23,18 @@
 namespace tq2 {
 namespace {
 
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
 constexpr int kBins = 512;
-constexpr int kMaxChunks = 32;
-constexpr int kThreads = 256;              // of the chunk kernels
-constexpr int kRowThreads = kBins;         // of the choice: a thread for each bin
+constexpr float kGrid = 11.f;              // bins of a factor of two: 2^46.5 over all, more than a weight's 43 bits
+constexpr int kMaxChunks = 64;
+constexpr int kSmallThreads = 256, kSmallVecs = 4;     // of a block of bins_kernel, and 16-byte vectors of a thread
+constexpr int kLargeThreads = 1024, kLargeVecs = 8;
+constexpr int kRowThreads = 1024;          // of the choice
+constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kList = 4096;                // tokens of a bin that are held in LDS
 constexpr int kUnit = 43;                  // a token of the largest logit weighs 2^43
+constexpr double kCoolest = 1e-36;         // temperatures below act as this one
 
 struct Args {
   const void* logits;
@@ -39,19 +46,55 @@ struct Args {
   const float* top_ps;
   const float* min_ps;
   int32_t top_k, vocab, chunks;
+  int32_t chunk_shift;                     // log2 of a chunk's vectors
   int64_t row_stride;
   double temperature, top_p, min_p;
-  float2* ends;                            // [rows, chunks]: largest and least logit
   uint64_t* sums;                          // [rows, chunks, kBins]
   uint32_t* counts;
+  float* tops;                             // [rows, chunks]: largest logit
 };
 
-// A row's logits: `head` elements up to the first 16-byte boundary, vectors of 16 bytes, and the rest.
+// Element types by their bits, f32 by f32.
+template <class T>
+struct Bits;
+template <>
+struct Bits<F32> {
+  static constexpr int kVec = 4;
+  static constexpr uint32_t kNone = 0xFF800000u;                     // -infinity
+  static __device__ float get(u32x4_t v, int i) { return __builtin_bit_cast(float, uint32_t(v[i])); }
+  static __device__ float one(const void* p, int i) { return static_cast<const float*>(p)[i]; }
+};
+template <>
+struct Bits<F16> {
+  static constexpr int kVec = 8;
+  static constexpr uint32_t kNone = 0xFC00FC00u;
+  static __device__ float get(u32x4_t v, int i) {
+    const uint32_t w = v[i >> 1];
+    return float(__builtin_bit_cast(_Float16, uint16_t(i & 1 ? w >> 16 : w)));
+  }
+  static __device__ float one(const void* p, int i) { return float(static_cast<const _Float16*>(p)[i]); }
+};
+template <>
+struct Bits<BF16> {
+  static constexpr int kVec = 8;
+  static constexpr uint32_t kNone = 0xFF80FF80u;
+  static __device__ float get(u32x4_t v, int i) {
+    const uint32_t w = v[i >> 1];
+    return __builtin_bit_cast(float, i & 1 ? w & 0xFFFF0000u : w << 16);
+  }
+  static __device__ float one(const void* p, int i) {
+    return __builtin_bit_cast(float, uint32_t(static_cast<const uint16_t*>(p)[i]) << 16);
+  }
+};
+
+// A row's logits: `head` elements up to the first 16-byte boundary, `vecs` vectors of 16 bytes, and the rest.  Chunk 0
+// has the head too, the last chunk the rest.
 template <class T>
 struct Row {
-  static constexpr int kVec = 16 / sizeof(typename T::elem);
+  static constexpr int kVec = Bits<T>::kVec;
   const typename T::elem* p;
-  int vocab, head, vecs, per_chunk;        // per_chunk: vectors of a chunk
+  const u32x4_t* body;
+  int vocab, head, vecs;
 
   __device__ Row(const Args& a, int row) {
     p = static_cast<const typename T::elem*>(a.logits) + row * a.row_stride;
@@ -59,75 +102,44 @@ struct Row {
     const int past = int(reinterpret_cast<uintptr_t>(p) & 15) / int(sizeof(typename T::elem));
     head = min(vocab, past ? kVec - past : 0);
     vecs = (vocab - head) / kVec;
-    per_chunk = (vecs + a.chunks - 1) / a.chunks;
+    body = reinterpret_cast<const u32x4_t*>(p + head);
   }
-  __device__ static float value(const typename T::elem* p) {
-    const float v = float(*p);
-    return v == v ? v : -__builtin_inff();            // NaN counts as -infinity
-  }
-  // f(value, index) for the elements of a chunk, shared by `threads` threads.  Chunk 0 has the head, the last one the rest.
-  template <class F>
-  __device__ void each(int chunk, int chunks, int threads, F f) const {
-    const int from = min(vecs, chunk * per_chunk), to = min(vecs, from + per_chunk);
-    const typename T::elem* body = p + head;
-    constexpr int kAhead = 4;
-    for (int v0 = from + threadIdx.x; v0 < to; v0 += kAhead * threads) {
-      f32x4_t x[kAhead][kVec / 4];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int v = min(v0 + i * threads, to - 1);
-#pragma unroll
-        for (int j = 0; j < kVec / 4; ++j) x[i][j] = load4(T(), body + v * kVec + 4 * j);
-      }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int v = v0 + i * threads;
-        if (v >= to) break;
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          const float y = x[i][j / 4][j % 4];
-          f(y == y ? y : -__builtin_inff(), head + v * kVec + j);
-        }
-      }
-    }
-    const int t = threadIdx.x;
-    if (chunk == 0 && t < head) f(value(p + t), t);
-    const int rest = head + vecs * kVec;
-    if (chunk == chunks - 1 && t < vocab - rest) f(value(p + rest + t), rest + t);
+  // The index of the thread's element among the head and the rest of a chunk, or -1.
+  __device__ int loose(const Args& a, int chunk) const {
+    const int t = threadIdx.x, rest = head + vecs * kVec;
+    if (chunk == 0 && t < head) return t;
+    if (chunk == a.chunks - 1 && t >= 64 && t - 64 < vocab - rest) return rest + t - 64;
+    return -1;
   }
 };
 
-// A row's settings, and the two functions of a logit that all kernels share.
+// A row's settings, and what becomes of a logit; `top` is the largest logit that weights are counted from.
 struct Rule {
-  float top, slope;                        // bin = (top - l) * slope
-  double heat, rate;                       // temperature; log2(e) / T
-  double least;                            // min_p
+  double rate;                             // log2(e) / T
+  float grid;                              // bins of the logits' unit
+  float top, base;
   bool greedy;
 
-  __device__ Rule(const Args& a, int row, float top, float low) : top(top) {
-    heat = a.temperatures ? double(a.temperatures[row]) : a.temperature;
-    greedy = !(heat > 0.0);
-    rate = greedy ? 0.0 : 1.4426950408889634 / heat;
-    least = a.min_ps ? double(a.min_ps[row]) : a.min_p;
-    least = least > 0.0 ? fmin(least, 1.0) : 0.0;
-    // Bins over what lies within 32 temperatures of the top, or over less.
-    slope = greedy ? 0.f : float(kBins - 1) / fminf(float(32.0 * heat), top - low);
+  __device__ Rule(const Args& a, int row) {
+    const double heat = a.temperatures ? double(a.temperatures[row]) : a.temperature;
+    greedy = !(heat > 0.0);                // the first of the order, at any temperature
+    rate = 1.4426950408889634 / (greedy ? 1.0 : fmax(heat, kCoolest));
+    grid = kGrid * float(rate);
   }
+  __device__ void set_top(float l) {
+    top = l;
+    base = floorf(l * grid);
+  }
+  // Bins from the top's; NaN and what is too far give kBins.
   __device__ int bin(float l) const {
-    return l == top ? 0 : int(fminf((top - l) * slope, float(kBins - 1)));
+    const float b = floorf(l * grid), d = b == base ? 0.f : base - b;
+    return d < float(kBins) ? int(d) : kBins;
   }
-  // log2 of e.
-  __device__ double power(float l) const {
-    if (l == top) return 0.0;
-    return greedy ? -__builtin_inf() : (double(l) - double(top)) * rate;
-  }
-  // e in units of 2^-kUnit; 0 below min_p.
-  __device__ uint64_t weight(float l) const {
-    const double y = power(l);
-    if (!(y > -(kUnit + 2))) return 0;                  // NaN as well: -infinity at an infinite temperature
-    // 2^f, |f| <= 1/2, by its Taylor polynomial of degree 11, which leaves 6.3e-15 of it.
+  __device__ double power(float l) const { return l == top ? 0.0 : (double(l) - double(top)) * rate; }
+  // 2^y, y <= 0: f = y - n, |f| <= 1/2, by the Taylor polynomial of degree 11, which leaves 6.3e-15 of it.
+  static __device__ double exp2_of(double y) {
     const double n = __builtin_rint(y), f = y - n;
-    double s = 4.44553827187081e-10;                     // ln(2)^k / k!, k = 11 .. 0
+    double s = 4.44553827187081e-10;                    // ln(2)^k / k!, k = 11 .. 0
     s = __builtin_fma(s, f, 7.054911620801121e-09);
     s = __builtin_fma(s, f, 1.0178086009239696e-07);
     s = __builtin_fma(s, f, 1.3215486790144305e-06);
@@ -139,74 +151,92 @@ struct Rule {
     s = __builtin_fma(s, f, 0.2402265069591007);
     s = __builtin_fma(s, f, 0.6931471805599453);
     s = __builtin_fma(s, f, 1.0);
-    s = __builtin_ldexp(s, int(n));
-    if (s < least) return 0;
-    // Rounded to a whole number by adding 2^52.
-    const double whole = __builtin_fma(s, double(uint64_t(1) << kUnit), 4503599627370496.0);
+    return __builtin_ldexp(s, int(n));
+  }
+  __device__ double e(float l) const {
+    const double y = power(l);
+    return y > -1000.0 ? exp2_of(y) : 0.0;
+  }
+  // e in units of 2^-kUnit, rounded to a whole number by adding 2^52.
+  __device__ uint64_t weight(float l) const {
+    const double y = power(l);
+    if (!(y > -(kUnit + 4))) return 0;
+    const double whole = __builtin_fma(exp2_of(y), double(uint64_t(1) << kUnit), 4503599627370496.0);
     return __builtin_bit_cast(uint64_t, whole) & ((uint64_t(1) << 52) - 1);
   }
 };
 
-// Largest first: a logit's bits in its order, then the index, lowest first.
-__device__ __forceinline__ uint64_t key_of(float l, int index) {
+// Logits as unsigned numbers of the same order, -0 as 0.
+__device__ __forceinline__ uint32_t order_of(float l) {
   const uint32_t b = __builtin_bit_cast(uint32_t, l == 0.f ? 0.f : l);
-  const uint32_t o = b >> 31 ? ~b : b | 0x80000000u;
-  return uint64_t(o) << 32 | uint32_t(~index);
+  return b >> 31 ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float logit_of(uint32_t o) {
+  return __builtin_bit_cast(float, o >> 31 ? o & 0x7FFFFFFFu : ~o);
+}
+// Largest first: the logit, then the index, lowest first.
+__device__ __forceinline__ uint64_t key_of(float l, int index) {
+  return uint64_t(order_of(l)) << 32 | uint32_t(~index);
 }
 
-__device__ __forceinline__ float2 join(float2 a, float2 b) { return make_float2(fmaxf(a.x, b.x), fminf(a.y, b.y)); }
-
-__device__ __forceinline__ float2 wave_ends(float2 v) {
+template <int WAVES>
+__device__ __forceinline__ float block_max(float v, float* part) {
 #pragma unroll
-  for (int m = 32; m; m >>= 1) v = join(v, make_float2(__shfl_xor(v.x, m), __shfl_xor(v.y, m)));
+  for (int m = 32; m; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = part[0];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) v = fmaxf(v, part[w]);
   return v;
 }
 
-template <class T>
-__global__ __launch_bounds__(kThreads) void max_kernel(Args a) {
-  __shared__ float2 part[kThreads / 64];
-  const int chunk = blockIdx.x, row = blockIdx.y;
-  float2 v = make_float2(-__builtin_inff(), __builtin_inff());
-  // -infinity is no least logit: bins are spread over what can be taken.
-  Row<T>(a, row).each(chunk, a.chunks, kThreads, [&](float l, int) {
-    v.x = fmaxf(v.x, l);
-    v.y = fminf(v.y, l > -__builtin_inff() ? l : __builtin_inff());
-  });
-  v = wave_ends(v);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < kThreads / 64; ++i) v = join(v, part[i]);
-    a.ends[row * a.chunks + chunk] = v;
-  }
-}
-
-// The row's largest and least logit, in every thread of each wave.
-__device__ __forceinline__ float2 row_ends(const Args& a, int row) {
-  const int lane = threadIdx.x & 63;
-  return wave_ends(a.ends[row * a.chunks + min(lane, a.chunks - 1)]);
-}
-
-template <class T>
-__global__ __launch_bounds__(kThreads) void bins_kernel(Args a) {
+template <class T, int THREADS, int VECS>
+__global__ __launch_bounds__(THREADS) void bins_kernel(Args a) {
   __shared__ uint64_t sums[kBins];
   __shared__ uint32_t counts[kBins];
+  __shared__ float part[THREADS / 64];
+  constexpr int kVec = Bits<T>::kVec;
   const int chunk = blockIdx.x, row = blockIdx.y;
-  for (int i = threadIdx.x; i < kBins; i += kThreads) sums[i] = 0, counts[i] = 0;
-  const float2 ends = row_ends(a, row);
-  const Rule rule(a, row, ends.x, ends.y);
-  __syncthreads();
-  Row<T>(a, row).each(chunk, a.chunks, kThreads, [&](float l, int) {
-    if (l == -__builtin_inff()) return;
-    const uint64_t w = rule.weight(l);
-    if (w == 0) return;
+  const Row<T> r(a, row);
+  u32x4_t x[VECS];
+#pragma unroll
+  for (int i = 0; i < VECS; ++i) {
+    const int v = chunk * (THREADS * VECS) + i * THREADS + threadIdx.x;
+    x[i] = u32x4_t{Bits<T>::kNone, Bits<T>::kNone, Bits<T>::kNone, Bits<T>::kNone};
+    if (v < r.vecs) x[i] = r.body[v];
+  }
+  const int loose = r.loose(a, chunk);
+  const float single = loose >= 0 ? Bits<T>::one(r.p, loose) : -__builtin_inff();
+  for (int i = threadIdx.x; i < kBins; i += THREADS) sums[i] = 0, counts[i] = 0;
+  Rule rule(a, row);
+  float top = fmaxf(single, -__builtin_inff());         // fmaxf passes NaN by
+#pragma unroll
+  for (int i = 0; i < VECS; ++i)
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) top = fmaxf(top, Bits<T>::get(x[i], j));
+  top = block_max<THREADS / 64>(top, part);
+  const size_t at = size_t(row) * a.chunks + chunk;
+  if (threadIdx.x == 0) a.tops[at] = top;
+  if (top == -__builtin_inff()) return;                 // its bins are not read
+  rule.set_top(top);
+  const auto put = [&](float l) {
     const int b = rule.bin(l);
-    atomicAdd(reinterpret_cast<unsigned long long*>(&sums[b]), static_cast<unsigned long long>(w));
+    if (b >= kBins) return;
+    atomicAdd(reinterpret_cast<unsigned long long*>(&sums[b]), static_cast<unsigned long long>(rule.weight(l)));
     atomicAdd(&counts[b], 1u);
-  });
+  };
+#pragma unroll 1
+  for (int i = 0; i < VECS; ++i) {
+    u32x4_t v = x[0];
+#pragma unroll
+    for (int j = 1; j < VECS; ++j) v = i == j ? x[j] : v;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) put(Bits<T>::get(v, j));
+  }
+  if (loose >= 0) put(single);
   __syncthreads();
-  const size_t at = (size_t(row) * a.chunks + chunk) * kBins;
-  for (int i = threadIdx.x; i < kBins; i += kThreads) a.sums[at + i] = sums[i], a.counts[at + i] = counts[i];
+  for (int i = threadIdx.x; i < kBins; i += THREADS) a.sums[at * kBins + i] = sums[i], a.counts[at * kBins + i] = counts[i];
 }
 
 // LDS of the choice.
@@ -215,29 +245,16 @@ struct Shared {
   uint64_t few_key[64], few_sum[64];
   uint64_t sums[kBins];
   uint32_t counts[kBins];
-  uint64_t wave_sum[kRowThreads / 64];
-  uint32_t wave_count[kRowThreads / 64];
-  uint64_t lo[kRowThreads / 64], hi[kRowThreads / 64];
-  uint32_t filled;
+  uint64_t wave_a[kRowWaves], wave_b[kRowWaves];
+  double factor[kMaxChunks];               // of a chunk's sums
+  int32_t shift[kMaxChunks];               // from the row's bins to the chunk's; kBins: no chunk to look at
+  int32_t visit[kMaxChunks];
+  uint32_t visits, filled;
   int bin;
-  uint64_t before, key;
+  uint64_t before, inside, key;
   uint32_t count_before, count;
+  float from, to;
 };
-
-// Inclusive sums over the block's threads, one bin each.
-__device__ __forceinline__ void scan(Shared& s, uint64_t& sum, uint32_t& count) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const uint64_t o = __shfl_up(static_cast<unsigned long long>(sum), d);
-    const uint32_t c = __shfl_up(count, d);
-    if (lane >= d) sum += o, count += c;
-  }
-  if (lane == 63) s.wave_sum[wave] = sum, s.wave_count[wave] = count;
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) sum += s.wave_sum[w], count += s.wave_count[w];
-  __syncthreads();
-}
 
 // What is looked for in the order: the `count`-th token (count > 0), or the first whose sum from the top reaches `sum`.
 struct Goal {
@@ -248,16 +265,43 @@ struct Goal {
   }
 };
 
-// The bin of the goal, with what lies above it: s.bin, s.before, s.count_before, s.count.  sum and count are the
-// thread's inclusive sums, own and n its bin's.
-__device__ __forceinline__ void find_bin(Shared& s, const Goal& g, uint64_t sum, uint64_t own, uint32_t count, uint32_t n) {
-  if (g.here(sum, own, count, n)) {
-    s.bin = threadIdx.x;
-    s.before = sum - own;
-    s.count_before = count - n;
-    s.count = n;
+// Inclusive sums over the bins, one for each of the first kBins threads.
+__device__ __forceinline__ void scan(Shared& s, uint64_t& sum, uint32_t& count) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint64_t o = __shfl_up(static_cast<unsigned long long>(sum), d);
+    const uint32_t c = __shfl_up(count, d);
+    if (lane >= d) sum += o, count += c;
   }
+  if (lane == 63) s.wave_a[wave] = sum, s.wave_b[wave] = count;
   __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kBins / 64; ++w)
+    if (w < wave) sum += s.wave_a[w], count += uint32_t(s.wave_b[w]);
+  __syncthreads();
+}
+
+// The smallest logit (as order_of gives it) that `holds`, which is false below it and true from it on up to `most`, by
+// one wave: first among the 64 around a guess, then by 64 tries at a time.
+template <class F>
+__device__ __forceinline__ uint32_t first_logit(float guess, uint32_t most, F holds) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t near = order_of(guess), from = near > 32 ? near - 32 : 0;
+  const uint32_t mine = from + lane < most ? from + lane : most;
+  uint64_t yes = __ballot(holds(logit_of(mine)));
+  if (yes && !(yes & 1)) return __builtin_amdgcn_readlane(int(mine), __builtin_ctzll(yes));
+  uint32_t lo = order_of(-__builtin_inff()), hi = most;           // the answer lies in (lo, hi]
+  while (hi - lo > 1) {
+    const uint32_t step = (hi - lo + 63) / 64;
+    const uint64_t at = uint64_t(lo) + uint64_t(step) * (lane + 1);
+    const uint32_t probe = at < hi ? uint32_t(at) : hi;
+    yes = __ballot(holds(logit_of(probe)));
+    const int n = yes ? __builtin_ctzll(yes) : 63;
+    hi = __builtin_amdgcn_readlane(int(probe), n);
+    if (n > 0) lo = __builtin_amdgcn_readlane(int(probe), n - 1);
+  }
+  return hi;
 }
 
 template <class T>
@@ -267,54 +311,121 @@ struct Choice {
   const Rule& rule;
   const Row<T>& row;
   int index;                               // of the row
-  int listed = -1;                         // the bin that the list holds
+  int listed = -1;                         // the bin that the list holds, whole
 
-  // f(key, weight) for the tokens of a bin, from the chunks that have any.
+  // Before the tokens of a bin are gone through: the chunks that have any, and the logits [from, to] of the bin.
+  __device__ void aim(int bin) {
+    const int t = threadIdx.x;
+    __syncthreads();
+    if (t < 64) {
+      const int at = t < a.chunks ? bin - s.shift[t] : -1;
+      const bool has = at >= 0 && a.counts[(size_t(index) * a.chunks + t) * kBins + at] > 0;
+      const uint64_t all = __ballot(has);
+      if (has) s.visit[__popcll(all & ((uint64_t(1) << t) - 1))] = t;
+      if (t == 0) s.visits = __popcll(all);
+    } else if (t < 128) {
+      const float guess = fminf(fmaxf((rule.base - float(bin)) / rule.grid, -3.4e38f), rule.top);
+      const uint32_t first = first_logit(guess, order_of(rule.top), [&](float l) { return rule.bin(l) <= bin; });
+      if (t == 64) s.from = logit_of(first);
+    } else if (t < 192) {
+      const float guess = fminf(fmaxf((rule.base - float(bin - 1)) / rule.grid, -3.4e38f), rule.top);
+      const uint32_t first =
+          bin > 0 ? first_logit(guess, order_of(rule.top), [&](float l) { return rule.bin(l) < bin; }) : 0;
+      if (t == 128) s.to = bin > 0 ? logit_of(first - 1) : rule.top;
+    }
+    __syncthreads();
+  }
+  // f(key, weight) for the tokens of the bin that was aimed at.
   template <class F>
-  __device__ void tokens(int bin, F f) {
-    for (int c = 0; c < a.chunks; ++c) {
-      if (a.counts[(size_t(index) * a.chunks + c) * kBins + bin] == 0) continue;
-      row.each(c, a.chunks, kRowThreads, [&](float l, int i) {
-        if (l == -__builtin_inff() || rule.bin(l) != bin) return;
-        const uint64_t w = rule.weight(l);
-        if (w) f(key_of(l, i), w);
-      });
+  __device__ void tokens(F f) {
+    const float from = s.from, to = s.to;
+    const auto look = [&](float l, int i) {
+      if (l >= from && l <= to) f(key_of(l, i), rule.weight(l));
+    };
+    constexpr int kVec = Bits<T>::kVec, kAhead = 16 / kVec;
+    const int all = int(s.visits) << a.chunk_shift;
+    for (int v0 = threadIdx.x; v0 < all; v0 += kAhead * kRowThreads) {
+      u32x4_t x[kAhead];
+      int at[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int v = v0 + i * kRowThreads;
+        at[i] = v < all ? (s.visit[v >> a.chunk_shift] << a.chunk_shift) + (v & ((1 << a.chunk_shift) - 1)) : row.vecs;
+        x[i] = u32x4_t{Bits<T>::kNone, Bits<T>::kNone, Bits<T>::kNone, Bits<T>::kNone};
+        if (at[i] < row.vecs) x[i] = row.body[at[i]];
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (at[i] >= row.vecs) continue;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) look(Bits<T>::get(x[i], j), row.head + at[i] * kVec + j);
+      }
+    }
+    for (uint32_t i = 0; i < s.visits; ++i) {
+      const int loose = row.loose(a, s.visit[i]);
+      if (loose >= 0) look(Bits<T>::one(row.p, loose), loose);
     }
   }
-
-  // The key of the goal's token among the n of a bin (the goal counted from the bin's start); *upto becomes the sum from
-  // the bin's start through it.  Called by all threads alike.
-  __device__ uint64_t resolve(int bin, uint32_t n, Goal g, uint64_t* upto) {
-    uint64_t lo = 0, hi = ~uint64_t(0), above = 0;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    bool in_list = listed == bin;
-    const auto each = [&](auto f) {
-      if (in_list) {
-        for (uint32_t i = threadIdx.x; i < s.filled; i += kRowThreads)
-          if (s.list_key[i] >= lo && s.list_key[i] <= hi) f(s.list_key[i], s.list_sum[i]);
-      } else {
-        tokens(bin, [&](uint64_t k, uint64_t w) {
-          if (k >= lo && k <= hi) f(k, w);
-        });
-      }
-    };
-    if (!in_list && n <= kList) {
-      __syncthreads();
-      if (threadIdx.x == 0) s.filled = 0;
-      __syncthreads();
-      tokens(bin, [&](uint64_t k, uint64_t w) {
-        const uint32_t at = atomicAdd(&s.filled, 1u);
-        s.list_key[at] = k;
-        s.list_sum[at] = w;
-      });
-      __syncthreads();
-      listed = bin;
-      in_list = true;
+  // Aim at a bin of n tokens, and keep them if they fit.
+  __device__ void open(int bin, uint32_t n) {
+    if (listed == bin) return;
+    aim(bin);
+    listed = -1;
+    if (n > kList) return;
+    if (threadIdx.x == 0) s.filled = 0;
+    __syncthreads();
+    tokens([&](uint64_t k, uint64_t w) {
+      const uint32_t at = atomicAdd(&s.filled, 1u);
+      if (at < kList) s.list_key[at] = k, s.list_sum[at] = w;
+    });
+    __syncthreads();
+    listed = bin;
+  }
+  template <class F>
+  __device__ void each(F f) {
+    if (listed >= 0) {
+      const uint32_t n = min(s.filled, uint32_t(kList));
+      for (uint32_t i = threadIdx.x; i < n; i += kRowThreads) f(s.list_key[i], s.list_sum[i]);
+    } else {
+      tokens(f);
     }
+  }
+  // Sums over the block.
+  __device__ void total(uint64_t& sum, uint32_t& count) {
+#pragma unroll
+    for (int m = 32; m; m >>= 1) {
+      sum += __shfl_xor(static_cast<unsigned long long>(sum), m);
+      count += __shfl_xor(count, m);
+    }
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) s.wave_a[threadIdx.x >> 6] = sum, s.wave_b[threadIdx.x >> 6] = count;
+    __syncthreads();
+    sum = 0, count = 0;
+#pragma unroll
+    for (int w = 0; w < kRowWaves; ++w) sum += s.wave_a[w], count += uint32_t(s.wave_b[w]);
+  }
+  // The key of the goal's token among the opened bin's (the goal counted from the bin's start); *upto becomes the sum
+  // from the bin's start through it.  Called by all threads alike.
+  __device__ uint64_t resolve(Goal g, uint64_t* upto) {
+    uint64_t lo = 0, hi = ~uint64_t(0), above = 0;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const auto inside = [&](auto f) {
+      each([&](uint64_t k, uint64_t w) {
+        if (k >= lo && k <= hi) f(k, w);
+      });
+    };
+    // Sums of tokens weighed at the row's top may miss those of the chunks by their last units.
+    uint64_t sum = 0;
+    uint32_t n = 0;
+    each([&](uint64_t, uint64_t w) { sum += w, ++n; });
+    total(sum, n);
+    if (g.count) g.count = min(g.count, n);
+    else if (sum == 0) g.count = 1;
+    else g.sum = g.sum < sum ? g.sum : sum;
     while (n > 64) {
       // The keys' range, then bins over it.
       uint64_t least = ~uint64_t(0), most = 0;
-      each([&](uint64_t k, uint64_t) {
+      inside([&](uint64_t k, uint64_t) {
         least = k < least ? k : least;
         most = k > most ? k : most;
       });
@@ -325,52 +436,46 @@ struct Choice {
         least = x < least ? x : least;
         most = y > most ? y : most;
       }
-      if (lane == 0) s.lo[wave] = least, s.hi[wave] = most;
-      s.sums[threadIdx.x] = 0;
-      s.counts[threadIdx.x] = 0;
       __syncthreads();
-      for (int w = 0; w < kRowThreads / 64; ++w) {
-        least = s.lo[w] < least ? s.lo[w] : least;
-        most = s.hi[w] > most ? s.hi[w] : most;
+      if (lane == 0) s.wave_a[wave] = least, s.wave_b[wave] = most;
+      if (t < kBins) s.sums[t] = 0, s.counts[t] = 0;
+      __syncthreads();
+      for (int w = 0; w < kRowWaves; ++w) {
+        least = s.wave_a[w] < least ? s.wave_a[w] : least;
+        most = s.wave_b[w] > most ? s.wave_b[w] : most;
       }
-      const int width = 64 - __builtin_clzll(most - least | 1), shift = width > 9 ? width - 9 : 0;
-      each([&](uint64_t k, uint64_t w) {
+      const int width = 64 - __builtin_clzll((most - least) | 1), shift = width > 9 ? width - 9 : 0;
+      inside([&](uint64_t k, uint64_t w) {
         const int b = int((most - k) >> shift);
         atomicAdd(reinterpret_cast<unsigned long long*>(&s.sums[b]), static_cast<unsigned long long>(w));
         atomicAdd(&s.counts[b], 1u);
       });
       __syncthreads();
-      const uint64_t own = s.sums[threadIdx.x];
-      const uint32_t mine = s.counts[threadIdx.x];
-      uint64_t sum = own;
-      uint32_t count = mine;
-      scan(s, sum, count);
-      find_bin(s, g, sum, own, count, mine);
+      find(g, t < kBins ? s.sums[t] : 0, t < kBins ? s.counts[t] : 0);
       hi = most - (uint64_t(s.bin) << shift);
       lo = hi - ((uint64_t(1) << shift) - 1);
       if (lo > hi) lo = 0;                               // below zero: the last bin may reach past the least key
       n = s.count;
       above += s.before;
-      if (g.count) g.count -= s.count_before; else g.sum -= s.before;
+      if (g.count) g.count -= s.count_before;
+      else g.sum -= s.before;
       __syncthreads();
     }
     // Few: one wave puts them in order by counting.
+    if (t == 0) s.count = 0;
     __syncthreads();
-    if (threadIdx.x == 0) s.count = 0;
-    __syncthreads();
-    each([&](uint64_t k, uint64_t w) {
+    inside([&](uint64_t k, uint64_t w) {
       const uint32_t at = atomicAdd(&s.count, 1u);
-      s.few_key[at] = k;
-      s.few_sum[at] = w;
+      if (at < 64) s.few_key[at] = k, s.few_sum[at] = w;
     });
     __syncthreads();
     if (wave == 0) {
       const uint64_t k = lane < int(n) ? s.few_key[lane] : 0, w = lane < int(n) ? s.few_sum[lane] : 0;
-      uint64_t sum = 0;
+      uint64_t upto_k = 0;
       uint32_t count = 0;
       for (uint32_t j = 0; j < n; ++j)
-        if (s.few_key[j] >= k) sum += s.few_sum[j], ++count;
-      if (lane < int(n) && g.here(sum, w, count, 1)) s.key = k, s.before = sum;
+        if (s.few_key[j] >= k) upto_k += s.few_sum[j], ++count;
+      if (lane < int(n) && g.here(upto_k, w, count, 1)) s.key = k, s.before = upto_k;
     }
     __syncthreads();
     *upto = above + s.before;
@@ -378,110 +483,156 @@ struct Choice {
     __syncthreads();
     return key;
   }
+  // The goal's bin by the sums and counts of each: s.bin, and what lies in it and above it: s.inside, s.count, s.before, s.count_before.
+  __device__ void find(const Goal& g, uint64_t own, uint32_t mine) {
+    uint64_t sum = own;
+    uint32_t count = mine;
+    scan(s, sum, count);
+    if (threadIdx.x < kBins && g.here(sum, own, count, mine)) {
+      s.bin = threadIdx.x;
+      s.before = sum - own;
+      s.inside = own;
+      s.count_before = count - mine;
+      s.count = mine;
+    }
+    __syncthreads();
+  }
 };
 
 template <class T>
 __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
-  const int index = blockIdx.x, t = threadIdx.x;
-  const float2 ends = row_ends(a, index);
-  if (ends.x == -__builtin_inff()) {
+  const int index = blockIdx.x, t = threadIdx.x, lane = t & 63;
+  Rule rule(a, index);
+  const size_t first_chunk = size_t(index) * a.chunks;
+  const float chunk_top = a.tops[first_chunk + min(lane, a.chunks - 1)];
+  float top = chunk_top;
+#pragma unroll
+  for (int m = 32; m; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
+  if (top == -__builtin_inff()) {
     if (t == 0) {
       a.ids[index] = -1;
       if (a.logprob) a.logprob[index] = -__builtin_inff();
     }
     return;
   }
-  const Rule rule(a, index, ends.x, ends.y);
-  const Row<T> row(a, index);
+  rule.set_top(top);
+  if (t < 64 && t < a.chunks) {
+    const bool any = chunk_top > -__builtin_inff();
+    s.shift[t] = any ? rule.bin(chunk_top) : kBins;
+    s.factor[t] = any ? rule.e(chunk_top) : 0.0;
+  }
+  __syncthreads();
+  // Thread t's bin of the row, joined.
   uint64_t own = 0;
   uint32_t mine = 0;
-  for (int c = 0; c < a.chunks; ++c) {
-    const size_t at = (size_t(index) * a.chunks + c) * kBins + t;
-    own += a.sums[at];
-    mine += a.counts[at];
-  }
-  uint64_t sum = own;
-  uint32_t count = mine;
-  scan(s, sum, count);
-  if (t == kBins - 1) s.before = sum, s.count = count;
-  __syncthreads();
-  uint64_t kept = s.before;                               // the sum of what is kept so far
-  const uint32_t all = s.count;
-  __syncthreads();
-  Choice<T> pick{s, a, rule, row, index};
-
-  const int top_k = a.top_ks ? a.top_ks[index] : a.top_k;
-  if (!rule.greedy && top_k > 0 && uint32_t(top_k) < all) {
-    Goal g{uint32_t(top_k), 0};
-    find_bin(s, g, sum, own, count, mine);
-    const int bin = s.bin;
-    const uint32_t n = s.count;
-    const uint64_t before = s.before;
-    g.count -= s.count_before;
-    __syncthreads();
-    if (g.count < n) {
-      uint64_t upto;
-      pick.resolve(bin, n, g, &upto);
-      kept = before + upto;
-    } else {
-      if (t == bin) s.before = sum;                      // the bin as a whole
-      __syncthreads();
-      kept = s.before;
-      __syncthreads();
+  if (t < kBins) {
+#pragma unroll 4
+    for (int c = 0; c < a.chunks; ++c) {
+      const int at = t - s.shift[c];
+      if (at < 0) continue;
+      const uint64_t sum = a.sums[(first_chunk + c) * kBins + at];
+      mine += a.counts[(first_chunk + c) * kBins + at];
+      const double f = s.factor[c];
+      own += f == 1.0 ? sum : uint64_t(double(sum) * f);
     }
   }
+  Choice<T> pick{s, a, rule, Row<T>(a, index), index};
+  uint64_t kept = 0;                                    // the sum and the count of what is kept so far
+  uint32_t left = 0;
+  {
+    uint64_t sum = own;
+    uint32_t count = mine;
+    pick.total(sum, count);
+    kept = sum, left = count;
+  }
+  const double min_p = a.min_ps ? double(a.min_ps[index]) : a.min_p;
+  if (!rule.greedy && min_p > 0.0) {
+    // The least logit with e >= min_p, its bin, and what lies above that.
+    const double least = fmin(min_p, 1.0);
+    const float guess = float(double(top) + log2(least) / rule.rate);
+    const uint32_t border = first_logit(guess < top ? guess : top, order_of(top), [&](float l) { return rule.e(l) >= least; });
+    const int bin = rule.bin(logit_of(border));
+    if (bin < kBins) {
+      uint64_t sum = t < bin ? own : 0, most = t <= bin ? own : 0;
+      uint32_t count = t < bin ? mine : 0, any = 0;
+      __syncthreads();
+      if (t == bin) s.count = mine;
+      __syncthreads();
+      pick.open(bin, s.count);
+      pick.each([&](uint64_t k, uint64_t w) {
+        if (uint32_t(k >> 32) >= border) sum += w, ++count;
+      });
+      pick.total(sum, count);
+      pick.total(most, any);
+      kept = sum < most ? sum : most, left = count;    // no more than the bins hold
+    }
+  }
+  const int top_k = a.top_ks ? a.top_ks[index] : a.top_k;
   const double top_p = a.top_ps ? double(a.top_ps[index]) : a.top_p;
-  if (!rule.greedy && top_p < 1.0) {
-    const uint64_t want = uint64_t(ceil(fmax(top_p, 0.0) * double(kept)));
-    Goal g{0, want < 1 ? 1 : want > kept ? kept : want};
-    find_bin(s, g, sum, own, count, mine);
+  const float u = a.u[index];
+  uint64_t key = 0;
+  for (int stage = 0; stage < 3; ++stage) {
+    Goal g{0, 1};
+    if (stage == 0) {
+      if (rule.greedy || top_k <= 0 || uint32_t(top_k) >= left) continue;
+      g = Goal{uint32_t(top_k), 0};
+    } else if (stage == 1) {
+      if (rule.greedy || !(top_p < 1.0)) continue;
+      const uint64_t want = uint64_t(ceil(fmax(top_p, 0.0) * double(kept)));
+      g.sum = want < 1 ? 1 : want > kept ? kept : want;
+    } else if (!rule.greedy && u > 0.f) {
+      const uint64_t past = uint64_t(fmin(double(u), 1.0) * double(kept));
+      g.sum = (past < kept ? past : kept - 1) + 1;
+    }
+    __syncthreads();
+    pick.find(g, own, mine);
     const int bin = s.bin;
     const uint32_t n = s.count;
-    const uint64_t before = s.before;
-    g.sum -= before;
+    const uint64_t before = s.before, inside = s.inside;
+    if (g.count) g.count -= s.count_before;
+    else g.sum -= before;
     __syncthreads();
+    pick.open(bin, n);
     uint64_t upto;
-    pick.resolve(bin, n, g, &upto);
-    kept = before + upto;
+    key = pick.resolve(g, &upto);
+    // No more than the bins hold, so that what is drawn lies in this run.
+    upto = upto < inside ? upto : inside;
+    if (stage < 2) kept = before + upto > 0 ? before + upto : 1;
   }
-  const float u = a.u[index];
-  uint64_t past = rule.greedy || !(u > 0.f) ? 0 : uint64_t(fmin(double(u), 1.0) * double(kept));
-  past = past < kept ? past : kept - 1;
-  Goal g{0, past + 1};
-  find_bin(s, g, sum, own, count, mine);
-  const int bin = s.bin;
-  const uint32_t n = s.count;
-  g.sum -= s.before;
-  __syncthreads();
-  uint64_t upto;
-  const uint64_t key = pick.resolve(bin, n, g, &upto);
   if (t == 0) {
-    const int id = int(~uint32_t(key));
-    a.ids[index] = id;
+    a.ids[index] = int(~uint32_t(key));
     if (a.logprob) {
-      const uint32_t o = uint32_t(key >> 32), b = o >> 31 ? o & 0x7FFFFFFFu : ~o;
-      const double y = rule.power(__builtin_bit_cast(float, b));
+      const double y = rule.power(logit_of(uint32_t(key >> 32)));
       a.logprob[index] = rule.greedy ? 0.f
                                      : float(y * 0.6931471805599453 - log(__builtin_ldexp(double(kept), -kUnit)));
     }
   }
 }
 
-// Chunks of a row: blocks for every CU, of at least 2048 logits each.
-int chunks_of(int64_t rows, int64_t vocab) {
-  int64_t chunks = 1024 / rows;
-  if (chunks > vocab / 2048) chunks = vocab / 2048;
-  if (chunks > kMaxChunks) chunks = kMaxChunks;
-  return chunks < 1 ? 1 : int(chunks);
+// Chunks: small ones while they are few, for the blocks' number; large ones otherwise, for the bins' traffic.
+struct Chunks {
+  bool large;
+  int vecs, count;
+};
+Chunks chunks_of(int64_t rows, int64_t vocab, int64_t type) {
+  const int64_t vec = type == TQ2_TYPE_F32 ? 4 : 8, vecs = vocab / vec;
+  const int64_t small = kSmallThreads * kSmallVecs, large = kLargeThreads * kLargeVecs;
+  const int64_t n = (vecs + small - 1) / small;
+  Chunks c;
+  c.large = n > kMaxChunks || rows * n > 2048;
+  c.vecs = int(c.large ? large : small);
+  c.count = int((vecs + c.vecs - 1) / c.vecs);
+  if (c.count < 1) c.count = 1;
+  return c;
 }
 
 template <class T>
-hipError_t launch(const Args& a, int64_t rows, hipStream_t stream) {
+hipError_t launch(const Args& a, bool large, int64_t rows, hipStream_t stream) {
   const dim3 grid(a.chunks, uint32_t(rows));
-  hipLaunchKernelGGL(max_kernel<T>, grid, dim3(kThreads), 0, stream, a);
-  hipLaunchKernelGGL(bins_kernel<T>, grid, dim3(kThreads), 0, stream, a);
+  if (large) hipLaunchKernelGGL((bins_kernel<T, kLargeThreads, kLargeVecs>), grid, dim3(kLargeThreads), 0, stream, a);
+  else hipLaunchKernelGGL((bins_kernel<T, kSmallThreads, kSmallVecs>), grid, dim3(kSmallThreads), 0, stream, a);
   const auto fn = choice_kernel<T>;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(Shared)));
@@ -492,11 +643,12 @@ hipError_t launch(const Args& a, int64_t rows, hipStream_t stream) {
 
 }  // namespace
 
-size_t sample_workspace(int64_t rows, int64_t vocab) {
-  return size_t(rows) * size_t(chunks_of(rows, vocab)) * (kBins * 12 + sizeof(float2));
+size_t sample_workspace(int64_t rows, int64_t vocab, int64_t type) {
+  return size_t(rows) * size_t(chunks_of(rows, vocab, type).count) * (kBins * 12 + 4);
 }
 
 hipError_t launch_sample(const tq2_sample_args& q, hipStream_t stream) {
+  const Chunks chunks = chunks_of(q.rows, q.vocab, q.logits_type);
   Args a;
   a.logits = q.logits;
   a.u = q.u;
@@ -508,18 +660,19 @@ hipError_t launch_sample(const tq2_sample_args& q, hipStream_t stream) {
   a.min_ps = q.min_ps;
   a.top_k = int32_t(q.top_k < 0 ? 0 : q.top_k < TQ2_SAMPLE_MAX_VOCAB ? q.top_k : TQ2_SAMPLE_MAX_VOCAB);
   a.vocab = int32_t(q.vocab);
-  a.chunks = chunks_of(q.rows, q.vocab);
+  a.chunks = chunks.count;
+  a.chunk_shift = __builtin_ctz(unsigned(chunks.vecs));
   a.row_stride = q.row_stride;
   a.temperature = q.temperature;
   a.top_p = q.top_p;
   a.min_p = q.min_p;
-  const size_t parts = size_t(q.rows) * size_t(a.chunks);
+  const size_t parts = size_t(q.rows) * size_t(chunks.count);
   a.sums = static_cast<uint64_t*>(q.workspace);
   a.counts = reinterpret_cast<uint32_t*>(a.sums + parts * kBins);
-  a.ends = reinterpret_cast<float2*>(a.counts + parts * kBins);
-  if (q.logits_type == TQ2_TYPE_F32) return launch<F32>(a, q.rows, stream);
-  if (q.logits_type == TQ2_TYPE_F16) return launch<F16>(a, q.rows, stream);
-  return launch<BF16>(a, q.rows, stream);
+  a.tops = reinterpret_cast<float*>(a.counts + parts * kBins);
+  if (q.logits_type == TQ2_TYPE_F32) return launch<F32>(a, chunks.large, q.rows, stream);
+  if (q.logits_type == TQ2_TYPE_F16) return launch<F16>(a, chunks.large, q.rows, stream);
+  return launch<BF16>(a, chunks.large, q.rows, stream);
 }
 
 }  // namespace tq2

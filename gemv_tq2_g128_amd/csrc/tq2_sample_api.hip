@@ -26,7 +26,7 @@ extern "C" {
 
 size_t tq2_sample_workspace_bytes(const tq2_sample_args* args) {
   if (!args || check_sizes(*args) != TQ2_OK || args->rows == 0) return 0;
-  return tq2::sample_workspace(args->rows, args->vocab);
+  return tq2::sample_workspace(args->rows, args->vocab, args->logits_type);
 }
 
 int tq2_sample(const tq2_sample_args* args, void* stream) {
@@ -38,7 +38,7 @@ int tq2_sample(const tq2_sample_args* args, void* stream) {
       (!a.min_ps && a.min_p != a.min_p))
     return TQ2_ERR_INVALID;
   if (a.rows == 0) return TQ2_OK;
-  const size_t need = tq2::sample_workspace(a.rows, a.vocab);
+  const size_t need = tq2::sample_workspace(a.rows, a.vocab, a.logits_type);
   if (!a.logits || !a.u || !a.ids || !a.workspace || a.workspace_bytes < 0 || size_t(a.workspace_bytes) < need)
     return TQ2_ERR_INVALID;
   const size_t element = a.logits_type == TQ2_TYPE_F32 ? 4 : 2, row = size_t(a.rows) * 4;

@@ -9,7 +9,7 @@
 
 namespace tq2 {
 
-size_t sample_workspace(int64_t rows, int64_t vocab);
+size_t sample_workspace(int64_t rows, int64_t vocab, int64_t type);
 hipError_t launch_sample(const tq2_sample_args& a, hipStream_t stream);
 
 }  // namespace tq2
