@@ -28,11 +28,12 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 constexpr int kBins = 512;
 constexpr float kGrid = 11.f;              // bins of a factor of two: 2^46.5 over all, more than a weight's 43 bits
 constexpr int kMaxChunks = 64;
-constexpr int kSmallThreads = 256, kSmallVecs = 4;     // of a block of bins_kernel, and 16-byte vectors of a thread
-constexpr int kLargeThreads = 1024, kLargeVecs = 8;
+constexpr int kThreads = 1024;             // of bins_kernel
+constexpr int kSmall = 1, kLarge = 8;      // 16-byte vectors of a thread: chunks of 4096 to 65536 logits
 constexpr int kRowThreads = 1024;          // of the choice
 constexpr int kRowWaves = kRowThreads / 64;
-constexpr int kList = 4096;                // tokens of a bin that are held in LDS
+constexpr int kWaveList = 256;             // tokens that each wave of the choice lists
+constexpr uint32_t kFew = 512;             // tokens from the top that are listed together
 constexpr int kUnit = 43;                  // a token of the largest logit weighs 2^43
 constexpr double kCoolest = 1e-36;         // temperatures below act as this one
 
@@ -157,10 +158,10 @@ struct Rule {
     const double y = power(l);
     return y > -1000.0 ? exp2_of(y) : 0.0;
   }
-  // e in units of 2^-kUnit, rounded to a whole number by adding 2^52.
-  __device__ uint64_t weight(float l) const {
-    const double y = power(l);
-    if (!(y > -(kUnit + 4))) return 0;
+  // e in units of 2^-kUnit, rounded to a whole number by adding 2^52.  Free of branches, and right for a logit whose bin
+  // is below kBins; any number for others.
+  __device__ uint64_t near_weight(float l) const {
+    const double y = fmax(power(l), -64.0);             // fmax passes NaN by
     const double whole = __builtin_fma(exp2_of(y), double(uint64_t(1) << kUnit), 4503599627370496.0);
     return __builtin_bit_cast(uint64_t, whole) & ((uint64_t(1) << 52) - 1);
   }
@@ -191,68 +192,132 @@ __device__ __forceinline__ float block_max(float v, float* part) {
   return v;
 }
 
-template <class T, int THREADS, int VECS>
-__global__ __launch_bounds__(THREADS) void bins_kernel(Args a) {
-  __shared__ uint64_t sums[kBins];
-  __shared__ uint32_t counts[kBins];
-  __shared__ float part[THREADS / 64];
+// Inclusive sums over the bins, one for each of the first kBins threads; part: two values for each of their waves.
+template <class A>
+__device__ __forceinline__ void scan(A& sum, uint32_t& count, A* part_sum, uint32_t* part_count) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (wave < kBins / 64) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const A o = __shfl_up(sum, d);
+      const uint32_t c = __shfl_up(count, d);
+      if (lane >= d) sum += o, count += c;
+    }
+    if (lane == 63) part_sum[wave] = sum, part_count[wave] = count;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kBins / 64; ++w)
+    if (w < wave) sum += part_sum[w], count += part_count[w];
+}
+
+// The last bin that min_p leaves anything of, for a largest logit that is the row's or below it, with one to spare.
+__device__ __forceinline__ int last_bin(double min_p) {
+  return min_p > 0.0 ? min(kBins - 1, 2 - int(floor(log2(fmin(min_p, 1.0)) * double(kGrid)))) : kBins - 1;
+}
+
+template <class T, int VECS>
+__global__ __launch_bounds__(kThreads) void bins_kernel(Args a) {
+  __shared__ unsigned long long sums[kBins];
+  __shared__ uint32_t counts[kBins], part_a[kBins / 64], part_b[kBins / 64];
+  __shared__ float part[kThreads / 64];
+  __shared__ int last;
   constexpr int kVec = Bits<T>::kVec;
   const int chunk = blockIdx.x, row = blockIdx.y;
   const Row<T> r(a, row);
   u32x4_t x[VECS];
 #pragma unroll
   for (int i = 0; i < VECS; ++i) {
-    const int v = chunk * (THREADS * VECS) + i * THREADS + threadIdx.x;
+    const int v = chunk * (kThreads * VECS) + i * kThreads + threadIdx.x;
     x[i] = u32x4_t{Bits<T>::kNone, Bits<T>::kNone, Bits<T>::kNone, Bits<T>::kNone};
     if (v < r.vecs) x[i] = r.body[v];
   }
   const int loose = r.loose(a, chunk);
   const float single = loose >= 0 ? Bits<T>::one(r.p, loose) : -__builtin_inff();
-  for (int i = threadIdx.x; i < kBins; i += THREADS) sums[i] = 0, counts[i] = 0;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) sums[i] = 0, counts[i] = 0;
   Rule rule(a, row);
+  const double min_p = a.min_ps ? double(a.min_ps[row]) : a.min_p;
+  const int top_k = rule.greedy ? 1 : a.top_ks ? a.top_ks[row] : a.top_k;
   float top = fmaxf(single, -__builtin_inff());         // fmaxf passes NaN by
 #pragma unroll
   for (int i = 0; i < VECS; ++i)
 #pragma unroll
     for (int j = 0; j < kVec; ++j) top = fmaxf(top, Bits<T>::get(x[i], j));
-  top = block_max<THREADS / 64>(top, part);
+  top = block_max<kThreads / 64>(top, part);
   const size_t at = size_t(row) * a.chunks + chunk;
   if (threadIdx.x == 0) a.tops[at] = top;
   if (top == -__builtin_inff()) return;                 // its bins are not read
   rule.set_top(top);
-  const auto put = [&](float l) {
-    const int b = rule.bin(l);
-    if (b >= kBins) return;
-    atomicAdd(reinterpret_cast<unsigned long long*>(&sums[b]), static_cast<unsigned long long>(rule.weight(l)));
-    atomicAdd(&counts[b], 1u);
-  };
-#pragma unroll 1
-  for (int i = 0; i < VECS; ++i) {
-    u32x4_t v = x[0];
+  // What min_p or top_k drop of a chunk by itself is no part of the row's either: no weights for it.
+  int cut = last_bin(min_p);
+  const bool first_k = top_k > 0 && top_k < a.vocab;
+  if (first_k) {
 #pragma unroll
-    for (int j = 1; j < VECS; ++j) v = i == j ? x[j] : v;
+    for (int i = 0; i < VECS; ++i) {
+      const u32x4_t v = x[i];
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) put(Bits<T>::get(v, j));
+      for (int j = 0; j < kVec; ++j) {
+        const int b = rule.bin(Bits<T>::get(v, j));
+        if (b <= cut) atomicAdd(&counts[b], 1u);
+      }
+    }
+    if (loose >= 0 && rule.bin(single) <= cut) atomicAdd(&counts[rule.bin(single)], 1u);
+    if (threadIdx.x == 0) last = cut;
+    __syncthreads();
+    const uint32_t own = threadIdx.x < kBins ? counts[threadIdx.x] : 0;
+    uint32_t upto = own, none = 0;
+    scan(upto, none, part_a, part_b);
+    if (threadIdx.x < kBins && upto >= uint32_t(top_k) && upto - own < uint32_t(top_k)) last = threadIdx.x;
+    __syncthreads();
+    cut = last;
+    if (int(threadIdx.x) < kBins && int(threadIdx.x) > cut) counts[threadIdx.x] = 0;
   }
-  if (loose >= 0) put(single);
+#pragma unroll
+  for (int i = 0; i < VECS; ++i) {
+    const u32x4_t v = x[i];
+    int b[kVec];
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      b[j] = rule.bin(Bits<T>::get(v, j));
+      any |= b[j] <= cut;
+    }
+    if (!__any(any)) continue;
+    // The exponentials side by side: each is one long chain.
+    uint64_t w[kVec];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) w[j] = rule.near_weight(Bits<T>::get(v, j));
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      if (b[j] > cut) continue;
+      atomicAdd(&sums[b[j]], static_cast<unsigned long long>(w[j]));
+      if (!first_k) atomicAdd(&counts[b[j]], 1u);
+    }
+  }
+  if (loose >= 0 && rule.bin(single) <= cut) {
+    atomicAdd(&sums[rule.bin(single)], static_cast<unsigned long long>(rule.near_weight(single)));
+    if (!first_k) atomicAdd(&counts[rule.bin(single)], 1u);
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < kBins; i += THREADS) a.sums[at * kBins + i] = sums[i], a.counts[at * kBins + i] = counts[i];
+  for (int i = threadIdx.x; i < kBins; i += kThreads) a.sums[at * kBins + i] = sums[i], a.counts[at * kBins + i] = counts[i];
 }
 
 // LDS of the choice.
 struct Shared {
-  uint64_t list_key[kList], list_sum[kList];
+  uint64_t list[kRowWaves][kWaveList];     // keys, each wave's own
   uint64_t few_key[64], few_sum[64];
   uint64_t sums[kBins];
+  uint64_t part_a[kRowWaves], part_b[kRowWaves];
   uint32_t counts[kBins];
-  uint64_t wave_a[kRowWaves], wave_b[kRowWaves];
+  uint32_t part_c[kRowWaves];
+  uint32_t listed[kRowWaves];              // keys of each wave's list
   double factor[kMaxChunks];               // of a chunk's sums
   int32_t shift[kMaxChunks];               // from the row's bins to the chunk's; kBins: no chunk to look at
   int32_t visit[kMaxChunks];
-  uint32_t visits, filled;
+  uint32_t visits, few, count, upto_count, over;
   int bin;
   uint64_t before, inside, key;
-  uint32_t count_before, count;
+  uint32_t count_before;
   float from, to;
 };
 
@@ -264,23 +329,6 @@ struct Goal {
     return count ? upto_n >= count && upto_n - n < count : upto >= sum && upto - own < sum;
   }
 };
-
-// Inclusive sums over the bins, one for each of the first kBins threads.
-__device__ __forceinline__ void scan(Shared& s, uint64_t& sum, uint32_t& count) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const uint64_t o = __shfl_up(static_cast<unsigned long long>(sum), d);
-    const uint32_t c = __shfl_up(count, d);
-    if (lane >= d) sum += o, count += c;
-  }
-  if (lane == 63) s.wave_a[wave] = sum, s.wave_b[wave] = count;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kBins / 64; ++w)
-    if (w < wave) sum += s.wave_a[w], count += uint32_t(s.wave_b[w]);
-  __syncthreads();
-}
 
 // The smallest logit (as order_of gives it) that `holds`, which is false below it and true from it on up to `most`, by
 // one wave: first among the 64 around a guess, then by 64 tries at a time.
@@ -304,6 +352,12 @@ __device__ __forceinline__ uint32_t first_logit(float guess, uint32_t most, F ho
   return hi;
 }
 
+__device__ __forceinline__ uint64_t wave_sum(uint64_t v) {
+#pragma unroll
+  for (int m = 32; m; m >>= 1) v += __shfl_xor(static_cast<unsigned long long>(v), m);
+  return v;
+}
+
 template <class T>
 struct Choice {
   Shared& s;
@@ -311,38 +365,44 @@ struct Choice {
   const Rule& rule;
   const Row<T>& row;
   int index;                               // of the row
-  int listed = -1;                         // the bin that the list holds, whole
+  // Thread t's bin (t < kBins): sum and count, by itself and through it from the top.
+  uint64_t own, sum;
+  uint32_t mine, count;
+  int low = 0, high = -1;                  // bins that the list holds whole
 
-  // Before the tokens of a bin are gone through: the chunks that have any, and the logits [from, to] of the bin.
-  __device__ void aim(int bin) {
-    const int t = threadIdx.x;
+  // Before the tokens of bins lo .. hi are gone through: the chunks that have any, and the bins' logits [from, to].
+  __device__ void aim(int lo, int hi) {
+    const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
+    if (t == 0) s.visits = 0, s.over = 0;
     __syncthreads();
-    if (t < 64) {
-      const int at = t < a.chunks ? bin - s.shift[t] : -1;
-      const bool has = at >= 0 && a.counts[(size_t(index) * a.chunks + t) * kBins + at] > 0;
-      const uint64_t all = __ballot(has);
-      if (has) s.visit[__popcll(all & ((uint64_t(1) << t) - 1))] = t;
-      if (t == 0) s.visits = __popcll(all);
-    } else if (t < 128) {
-      const float guess = fminf(fmaxf((rule.base - float(bin)) / rule.grid, -3.4e38f), rule.top);
-      const uint32_t first = first_logit(guess, order_of(rule.top), [&](float l) { return rule.bin(l) <= bin; });
-      if (t == 64) s.from = logit_of(first);
-    } else if (t < 192) {
-      const float guess = fminf(fmaxf((rule.base - float(bin - 1)) / rule.grid, -3.4e38f), rule.top);
-      const uint32_t first =
-          bin > 0 ? first_logit(guess, order_of(rule.top), [&](float l) { return rule.bin(l) < bin; }) : 0;
-      if (t == 128) s.to = bin > 0 ? logit_of(first - 1) : rule.top;
+    if (wave == kRowWaves - 1) {
+      const float guess = fminf(fmaxf((rule.base - float(hi)) / rule.grid, -3.4e38f), rule.top);
+      const uint32_t first = first_logit(guess, order_of(rule.top), [&](float l) { return rule.bin(l) <= hi; });
+      if (lane == 0) s.from = logit_of(first);
+    } else if (wave == kRowWaves - 2) {
+      uint32_t first = order_of(rule.top) + 1;
+      if (lo > 0) {
+        const float guess = fminf(fmaxf((rule.base - float(lo - 1)) / rule.grid, -3.4e38f), rule.top);
+        first = first_logit(guess, order_of(rule.top), [&](float l) { return rule.bin(l) < lo; });
+      }
+      if (lane == 0) s.to = lo > 0 ? logit_of(first - 1) : rule.top;
+    } else {
+      // A wave for a chunk at a time, a lane for a bin.
+      for (int c = wave; c < a.chunks; c += kRowWaves - 2) {
+        const int shift = s.shift[c], from = max(lo - shift, 0), to = hi - shift;
+        const uint32_t* n = a.counts + (size_t(index) * a.chunks + c) * kBins;
+        uint32_t any = 0;
+        for (int b = from + lane; b <= to; b += 64) any |= n[b];
+        if (__any(any != 0) && lane == 0) s.visit[atomicAdd(&s.visits, 1u)] = c;
+      }
     }
     __syncthreads();
   }
-  // f(key, weight) for the tokens of the bin that was aimed at.
+  // f(logit, index) for the tokens that were aimed at.
   template <class F>
   __device__ void tokens(F f) {
     const float from = s.from, to = s.to;
-    const auto look = [&](float l, int i) {
-      if (l >= from && l <= to) f(key_of(l, i), rule.weight(l));
-    };
-    constexpr int kVec = Bits<T>::kVec, kAhead = 16 / kVec;
+    constexpr int kVec = Bits<T>::kVec, kAhead = 8 / kVec;
     const int all = int(s.visits) << a.chunk_shift;
     for (int v0 = threadIdx.x; v0 < all; v0 += kAhead * kRowThreads) {
       u32x4_t x[kAhead];
@@ -356,79 +416,132 @@ struct Choice {
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        if (at[i] >= row.vecs) continue;
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) look(Bits<T>::get(x[i], j), row.head + at[i] * kVec + j);
+        for (int j = 0; j < kVec; ++j) {
+          const float l = Bits<T>::get(x[i], j);
+          if (l >= from && l <= to && at[i] < row.vecs) f(l, row.head + at[i] * kVec + j);
+        }
       }
     }
     for (uint32_t i = 0; i < s.visits; ++i) {
       const int loose = row.loose(a, s.visit[i]);
-      if (loose >= 0) look(Bits<T>::one(row.p, loose), loose);
+      if (loose < 0) continue;
+      const float l = Bits<T>::one(row.p, loose);
+      if (l >= from && l <= to) f(l, loose);
     }
   }
-  // Aim at a bin of n tokens, and keep them if they fit.
-  __device__ void open(int bin, uint32_t n) {
-    if (listed == bin) return;
-    aim(bin);
-    listed = -1;
-    if (n > kList) return;
-    if (threadIdx.x == 0) s.filled = 0;
+  // Have the tokens of a bin at hand: listed, with all above them if these are few, or aimed at.
+  __device__ void open(int bin) {
+    if (bin >= low && bin <= high) return;
+    const int t = threadIdx.x, wave = t >> 6;
     __syncthreads();
-    tokens([&](uint64_t k, uint64_t w) {
-      const uint32_t at = atomicAdd(&s.filled, 1u);
-      if (at < kList) s.list_key[at] = k, s.list_sum[at] = w;
+    if (t == bin) s.count = mine, s.upto_count = count;
+    __syncthreads();
+    const uint32_t upto = s.upto_count;
+    const int lo = upto <= kFew ? 0 : bin;
+    low = 0, high = -1;
+    aim(lo, bin);
+    if (s.count > kRowWaves * kWaveList) return;
+    if ((t & 63) == 0) s.listed[wave] = 0;
+    tokens([&](float l, int i) {
+      const uint32_t at = atomicAdd(&s.listed[wave], 1u);
+      if (at < kWaveList) s.list[wave][at] = key_of(l, i);
+      else s.over = 1;
     });
     __syncthreads();
-    listed = bin;
+    if (s.over) return;                                 // a wave had more than its list holds: gone through again
+    low = lo, high = bin;
   }
+  // f(key) for the opened bin's tokens.
   template <class F>
-  __device__ void each(F f) {
-    if (listed >= 0) {
-      const uint32_t n = min(s.filled, uint32_t(kList));
-      for (uint32_t i = threadIdx.x; i < n; i += kRowThreads) f(s.list_key[i], s.list_sum[i]);
+  __device__ void each(int bin, F f) {
+    if (bin >= low && bin <= high) {
+      const int wave = threadIdx.x >> 6;
+      const uint32_t n = s.listed[wave];
+      for (uint32_t i = threadIdx.x & 63; i < n; i += 64) {
+        const uint64_t key = s.list[wave][i];
+        if (rule.bin(logit_of(uint32_t(key >> 32))) == bin) f(key);
+      }
     } else {
-      tokens(f);
+      tokens([&](float l, int i) {
+        if (rule.bin(l) == bin) f(key_of(l, i));
+      });
     }
   }
+  __device__ uint64_t weight(uint64_t key) const { return rule.near_weight(logit_of(uint32_t(key >> 32))); }
   // Sums over the block.
-  __device__ void total(uint64_t& sum, uint32_t& count) {
+  __device__ void total(uint64_t& sum, uint32_t& n) {
+    sum = wave_sum(sum);
+    n = uint32_t(wave_sum(n));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) s.part_a[threadIdx.x >> 6] = sum, s.part_c[threadIdx.x >> 6] = n;
+    __syncthreads();
+    sum = 0, n = 0;
 #pragma unroll
-    for (int m = 32; m; m >>= 1) {
-      sum += __shfl_xor(static_cast<unsigned long long>(sum), m);
-      count += __shfl_xor(count, m);
+    for (int w = 0; w < kRowWaves; ++w) sum += s.part_a[w], n += s.part_c[w];
+  }
+  // The goal's bin: s.bin, what lies in it, s.inside, and what above it, s.before and s.count_before.
+  __device__ void find(const Goal& g) {
+    __syncthreads();
+    if (threadIdx.x < kBins && g.here(sum, own, count, mine)) {
+      s.bin = threadIdx.x;
+      s.before = sum - own;
+      s.inside = own;
+      s.count_before = count - mine;
     }
     __syncthreads();
-    if ((threadIdx.x & 63) == 0) s.wave_a[threadIdx.x >> 6] = sum, s.wave_b[threadIdx.x >> 6] = count;
-    __syncthreads();
-    sum = 0, count = 0;
-#pragma unroll
-    for (int w = 0; w < kRowWaves; ++w) sum += s.wave_a[w], count += uint32_t(s.wave_b[w]);
   }
   // The key of the goal's token among the opened bin's (the goal counted from the bin's start); *upto becomes the sum
   // from the bin's start through it.  Called by all threads alike.
-  __device__ uint64_t resolve(Goal g, uint64_t* upto) {
+  __device__ uint64_t resolve(int bin, Goal g, uint64_t* upto) {
     uint64_t lo = 0, hi = ~uint64_t(0), above = 0;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    const auto inside = [&](auto f) {
-      each([&](uint64_t k, uint64_t w) {
-        if (k >= lo && k <= hi) f(k, w);
+    bool clamped = false;
+    for (;;) {
+      // Few enough for one wave to put them in order by counting?
+      if (t == 0) s.few = 0;
+      __syncthreads();
+      each(bin, [&](uint64_t k) {
+        if (k < lo || k > hi) return;
+        const uint32_t at = atomicAdd(&s.few, 1u);
+        if (at < 64) s.few_key[at] = k, s.few_sum[at] = weight(k);
       });
-    };
-    // Sums of tokens weighed at the row's top may miss those of the chunks by their last units.
-    uint64_t sum = 0;
-    uint32_t n = 0;
-    each([&](uint64_t, uint64_t w) { sum += w, ++n; });
-    total(sum, n);
-    if (g.count) g.count = min(g.count, n);
-    else if (sum == 0) g.count = 1;
-    else g.sum = g.sum < sum ? g.sum : sum;
-    while (n > 64) {
+      __syncthreads();
+      const uint32_t n = s.few;
+      if (n <= 64) {
+        if (wave == 0) {
+          const uint64_t k = lane < int(n) ? s.few_key[lane] : 0, w = lane < int(n) ? s.few_sum[lane] : 0;
+          // Sums of tokens weighed at the row's top may miss those of the chunks by their last units.
+          const uint64_t all = wave_sum(w);
+          if (g.count) g.count = min(g.count, n);
+          else if (all == 0) g.count = 1;
+          else g.sum = g.sum < all ? g.sum : all;
+          uint64_t sum_k = 0;
+          uint32_t n_k = 0;
+          for (uint32_t j = 0; j < n; ++j)
+            if (s.few_key[j] >= k) sum_k += s.few_sum[j], ++n_k;
+          if (lane < int(n) && g.here(sum_k, w, n_k, 1)) s.key = k, s.before = sum_k;
+        }
+        __syncthreads();
+        *upto = above + s.before;
+        return s.key;
+      }
       // The keys' range, then bins over it.
-      uint64_t least = ~uint64_t(0), most = 0;
-      inside([&](uint64_t k, uint64_t) {
+      uint64_t least = ~uint64_t(0), most = 0, all = 0;
+      uint32_t any = 0;
+      each(bin, [&](uint64_t k) {
+        if (k < lo || k > hi) return;
         least = k < least ? k : least;
         most = k > most ? k : most;
+        if (!clamped) all += weight(k), ++any;
       });
+      if (!clamped) {
+        total(all, any);
+        if (g.count) g.count = min(g.count, any);
+        else if (all == 0) g.count = 1;
+        else g.sum = g.sum < all ? g.sum : all;
+        clamped = true;
+      }
 #pragma unroll
       for (int m = 32; m; m >>= 1) {
         const uint64_t x = __shfl_xor(static_cast<unsigned long long>(least), m);
@@ -437,65 +550,39 @@ struct Choice {
         most = y > most ? y : most;
       }
       __syncthreads();
-      if (lane == 0) s.wave_a[wave] = least, s.wave_b[wave] = most;
+      if (lane == 0) s.part_a[wave] = least, s.part_b[wave] = most;
       if (t < kBins) s.sums[t] = 0, s.counts[t] = 0;
       __syncthreads();
       for (int w = 0; w < kRowWaves; ++w) {
-        least = s.wave_a[w] < least ? s.wave_a[w] : least;
-        most = s.wave_b[w] > most ? s.wave_b[w] : most;
+        least = s.part_a[w] < least ? s.part_a[w] : least;
+        most = s.part_b[w] > most ? s.part_b[w] : most;
       }
       const int width = 64 - __builtin_clzll((most - least) | 1), shift = width > 9 ? width - 9 : 0;
-      inside([&](uint64_t k, uint64_t w) {
+      each(bin, [&](uint64_t k) {
+        if (k < lo || k > hi) return;
         const int b = int((most - k) >> shift);
-        atomicAdd(reinterpret_cast<unsigned long long*>(&s.sums[b]), static_cast<unsigned long long>(w));
+        atomicAdd(reinterpret_cast<unsigned long long*>(&s.sums[b]), static_cast<unsigned long long>(weight(k)));
         atomicAdd(&s.counts[b], 1u);
       });
       __syncthreads();
-      find(g, t < kBins ? s.sums[t] : 0, t < kBins ? s.counts[t] : 0);
+      const uint64_t part = t < kBins ? s.sums[t] : 0;
+      const uint32_t part_n = t < kBins ? s.counts[t] : 0;
+      uint64_t upto_b = part;
+      uint32_t upto_n = part_n;
+      scan(upto_b, upto_n, s.part_a, s.part_c);
+      if (t < kBins && g.here(upto_b, part, upto_n, part_n)) {
+        s.bin = t;
+        s.before = upto_b - part;
+        s.count_before = upto_n - part_n;
+      }
+      __syncthreads();
       hi = most - (uint64_t(s.bin) << shift);
       lo = hi - ((uint64_t(1) << shift) - 1);
       if (lo > hi) lo = 0;                               // below zero: the last bin may reach past the least key
-      n = s.count;
       above += s.before;
       if (g.count) g.count -= s.count_before;
       else g.sum -= s.before;
-      __syncthreads();
     }
-    // Few: one wave puts them in order by counting.
-    if (t == 0) s.count = 0;
-    __syncthreads();
-    inside([&](uint64_t k, uint64_t w) {
-      const uint32_t at = atomicAdd(&s.count, 1u);
-      if (at < 64) s.few_key[at] = k, s.few_sum[at] = w;
-    });
-    __syncthreads();
-    if (wave == 0) {
-      const uint64_t k = lane < int(n) ? s.few_key[lane] : 0, w = lane < int(n) ? s.few_sum[lane] : 0;
-      uint64_t upto_k = 0;
-      uint32_t count = 0;
-      for (uint32_t j = 0; j < n; ++j)
-        if (s.few_key[j] >= k) upto_k += s.few_sum[j], ++count;
-      if (lane < int(n) && g.here(upto_k, w, count, 1)) s.key = k, s.before = upto_k;
-    }
-    __syncthreads();
-    *upto = above + s.before;
-    const uint64_t key = s.key;
-    __syncthreads();
-    return key;
-  }
-  // The goal's bin by the sums and counts of each: s.bin, and what lies in it and above it: s.inside, s.count, s.before, s.count_before.
-  __device__ void find(const Goal& g, uint64_t own, uint32_t mine) {
-    uint64_t sum = own;
-    uint32_t count = mine;
-    scan(s, sum, count);
-    if (threadIdx.x < kBins && g.here(sum, own, count, mine)) {
-      s.bin = threadIdx.x;
-      s.before = sum - own;
-      s.inside = own;
-      s.count_before = count - mine;
-      s.count = mine;
-    }
-    __syncthreads();
   }
 };
 
@@ -505,6 +592,10 @@ __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
   Shared& s = *reinterpret_cast<Shared*>(smem);
   const int index = blockIdx.x, t = threadIdx.x, lane = t & 63;
   Rule rule(a, index);
+  const double min_p = a.min_ps ? double(a.min_ps[index]) : a.min_p;
+  const int top_k = a.top_ks ? a.top_ks[index] : a.top_k;
+  const double top_p = a.top_ps ? double(a.top_ps[index]) : a.top_p;
+  const float u = a.u[index];
   const size_t first_chunk = size_t(index) * a.chunks;
   const float chunk_top = a.tops[first_chunk + min(lane, a.chunks - 1)];
   float top = chunk_top;
@@ -518,36 +609,39 @@ __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
     return;
   }
   rule.set_top(top);
-  if (t < 64 && t < a.chunks) {
+  if (t < a.chunks) {                                   // at most kMaxChunks: the first wave
     const bool any = chunk_top > -__builtin_inff();
     s.shift[t] = any ? rule.bin(chunk_top) : kBins;
     s.factor[t] = any ? rule.e(chunk_top) : 0.0;
   }
   __syncthreads();
-  // Thread t's bin of the row, joined.
+  // The row's bins: half of the threads join the even chunks, the others the odd ones.
   uint64_t own = 0;
   uint32_t mine = 0;
-  if (t < kBins) {
-#pragma unroll 4
-    for (int c = 0; c < a.chunks; ++c) {
-      const int at = t - s.shift[c];
-      if (at < 0) continue;
-      const uint64_t sum = a.sums[(first_chunk + c) * kBins + at];
-      mine += a.counts[(first_chunk + c) * kBins + at];
-      const double f = s.factor[c];
-      own += f == 1.0 ? sum : uint64_t(double(sum) * f);
-    }
+  const int bin_of_thread = t & (kBins - 1);
+#pragma unroll 8
+  for (int c = t / kBins; c < a.chunks; c += kRowThreads / kBins) {
+    const int at = bin_of_thread - s.shift[c];
+    const size_t from = (first_chunk + c) * kBins + max(at, 0);
+    const bool here = at >= 0;
+    const uint64_t sum = here ? a.sums[from] : 0;
+    mine += here ? a.counts[from] : 0;
+    const double f = s.factor[c];
+    own += f == 1.0 ? sum : uint64_t(double(sum) * f);
   }
-  Choice<T> pick{s, a, rule, Row<T>(a, index), index};
-  uint64_t kept = 0;                                    // the sum and the count of what is kept so far
-  uint32_t left = 0;
-  {
-    uint64_t sum = own;
-    uint32_t count = mine;
-    pick.total(sum, count);
-    kept = sum, left = count;
-  }
-  const double min_p = a.min_ps ? double(a.min_ps[index]) : a.min_p;
+  if (t >= kBins) s.sums[bin_of_thread] = own, s.counts[bin_of_thread] = mine;
+  __syncthreads();
+  own = t < kBins ? own + s.sums[t] : 0;
+  mine = t < kBins ? mine + s.counts[t] : 0;
+  uint64_t sum = own;
+  uint32_t count = mine;
+  scan(sum, count, s.part_a, s.part_c);
+  if (t == kBins - 1) s.before = sum, s.count = count;
+  __syncthreads();
+  uint64_t kept = s.before;                             // the sum and the count of what is kept so far
+  uint32_t left = s.count;
+  const Row<T> row(a, index);
+  Choice<T> pick{s, a, rule, row, index, own, sum, mine, count};
   if (!rule.greedy && min_p > 0.0) {
     // The least logit with e >= min_p, its bin, and what lies above that.
     const double least = fmin(min_p, 1.0);
@@ -555,23 +649,21 @@ __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
     const uint32_t border = first_logit(guess < top ? guess : top, order_of(top), [&](float l) { return rule.e(l) >= least; });
     const int bin = rule.bin(logit_of(border));
     if (bin < kBins) {
-      uint64_t sum = t < bin ? own : 0, most = t <= bin ? own : 0;
-      uint32_t count = t < bin ? mine : 0, any = 0;
-      __syncthreads();
-      if (t == bin) s.count = mine;
-      __syncthreads();
-      pick.open(bin, s.count);
-      pick.each([&](uint64_t k, uint64_t w) {
-        if (uint32_t(k >> 32) >= border) sum += w, ++count;
+      pick.open(bin);
+      uint64_t part = 0;
+      uint32_t n = 0;
+      pick.each(bin, [&](uint64_t k) {
+        if (uint32_t(k >> 32) >= border) part += pick.weight(k), ++n;
       });
-      pick.total(sum, count);
-      pick.total(most, any);
-      kept = sum < most ? sum : most, left = count;    // no more than the bins hold
+      pick.total(part, n);
+      if (t == bin) {
+        s.before = sum - own + (part < own ? part : own);     // no more than the bins hold
+        s.count = count - mine + n;
+      }
+      __syncthreads();
+      kept = s.before, left = s.count;
     }
   }
-  const int top_k = a.top_ks ? a.top_ks[index] : a.top_k;
-  const double top_p = a.top_ps ? double(a.top_ps[index]) : a.top_p;
-  const float u = a.u[index];
   uint64_t key = 0;
   for (int stage = 0; stage < 3; ++stage) {
     Goal g{0, 1};
@@ -586,17 +678,14 @@ __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
       const uint64_t past = uint64_t(fmin(double(u), 1.0) * double(kept));
       g.sum = (past < kept ? past : kept - 1) + 1;
     }
-    __syncthreads();
-    pick.find(g, own, mine);
+    pick.find(g);
     const int bin = s.bin;
-    const uint32_t n = s.count;
     const uint64_t before = s.before, inside = s.inside;
     if (g.count) g.count -= s.count_before;
     else g.sum -= before;
-    __syncthreads();
-    pick.open(bin, n);
+    pick.open(bin);
     uint64_t upto;
-    key = pick.resolve(g, &upto);
+    key = pick.resolve(bin, g, &upto);
     // No more than the bins hold, so that what is drawn lies in this run.
     upto = upto < inside ? upto : inside;
     if (stage < 2) kept = before + upto > 0 ? before + upto : 1;
@@ -618,7 +707,7 @@ struct Chunks {
 };
 Chunks chunks_of(int64_t rows, int64_t vocab, int64_t type) {
   const int64_t vec = type == TQ2_TYPE_F32 ? 4 : 8, vecs = vocab / vec;
-  const int64_t small = kSmallThreads * kSmallVecs, large = kLargeThreads * kLargeVecs;
+  const int64_t small = kThreads * kSmall, large = kThreads * kLarge;
   const int64_t n = (vecs + small - 1) / small;
   Chunks c;
   c.large = n > kMaxChunks || rows * n > 2048;
@@ -631,8 +720,8 @@ Chunks chunks_of(int64_t rows, int64_t vocab, int64_t type) {
 template <class T>
 hipError_t launch(const Args& a, bool large, int64_t rows, hipStream_t stream) {
   const dim3 grid(a.chunks, uint32_t(rows));
-  if (large) hipLaunchKernelGGL((bins_kernel<T, kLargeThreads, kLargeVecs>), grid, dim3(kLargeThreads), 0, stream, a);
-  else hipLaunchKernelGGL((bins_kernel<T, kSmallThreads, kSmallVecs>), grid, dim3(kSmallThreads), 0, stream, a);
+  const auto bins = large ? bins_kernel<T, kLarge> : bins_kernel<T, kSmall>;
+  hipLaunchKernelGGL(bins, grid, dim3(kThreads), 0, stream, a);
   const auto fn = choice_kernel<T>;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(Shared)));
