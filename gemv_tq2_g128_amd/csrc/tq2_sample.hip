@@ -33,7 +33,8 @@ constexpr int kSmall = 1, kLarge = 8;      // 16-byte vectors of a thread: chunk
 constexpr int kRowThreads = 1024;          // of the choice
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr int kWaveList = 256;             // tokens that each wave of the choice lists
-constexpr uint32_t kFew = 512;             // tokens from the top that are listed together
+constexpr uint32_t kFew = kRowThreads / 4; // tokens that are put in order at once: four threads for each
+constexpr int kMaxStrips = 4 * kRowThreads;            // 2^20 f32 logits
 constexpr int kUnit = 43;                  // a token of the largest logit weighs 2^43
 constexpr double kCoolest = 1e-36;         // temperatures below act as this one
 
@@ -53,6 +54,7 @@ struct Args {
   uint64_t* sums;                          // [rows, chunks, kBins]
   uint32_t* counts;
   float* tops;                             // [rows, chunks]: largest logit
+  float* strips;                           // [rows, strips]: largest logit of each 64 vectors
 };
 
 // Element types by their bits, f32 by f32.
@@ -105,11 +107,11 @@ struct Row {
     vecs = (vocab - head) / kVec;
     body = reinterpret_cast<const u32x4_t*>(p + head);
   }
-  // The index of the thread's element among the head and the rest of a chunk, or -1.
-  __device__ int loose(const Args& a, int chunk) const {
+  // The index of the thread's element among the head (a first chunk's) and the rest (a last one's), or -1.
+  __device__ int loose(bool first, bool last) const {
     const int t = threadIdx.x, rest = head + vecs * kVec;
-    if (chunk == 0 && t < head) return t;
-    if (chunk == a.chunks - 1 && t >= 64 && t - 64 < vocab - rest) return rest + t - 64;
+    if (first && t < head) return t;
+    if (last && t >= 64 && t - 64 < vocab - rest) return rest + t - 64;
     return -1;
   }
 };
@@ -180,16 +182,20 @@ __device__ __forceinline__ uint64_t key_of(float l, int index) {
   return uint64_t(order_of(l)) << 32 | uint32_t(~index);
 }
 
-template <int WAVES>
-__device__ __forceinline__ float block_max(float v, float* part) {
-#pragma unroll
-  for (int m = 32; m; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = part[0];
-#pragma unroll
-  for (int w = 1; w < WAVES; ++w) v = fmaxf(v, part[w]);
-  return v;
+// One lane move of the maximum over a wave; lanes outside ROW_MASK keep theirs.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float max_move(float v) {
+  const int x = __builtin_bit_cast(int, v);
+  return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(x, x, CTRL, ROW_MASK, 0xF, false)));
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = max_move<0xB1, 0xF>(v);
+  v = max_move<0x4E, 0xF>(v);
+  v = max_move<0x141, 0xF>(v);
+  v = max_move<0x140, 0xF>(v);
+  v = max_move<0x142, 0xA>(v);
+  v = max_move<0x143, 0xC>(v);
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
 // Inclusive sums over the bins, one for each of the first kBins threads; part: two values for each of their waves.
@@ -232,19 +238,28 @@ __global__ __launch_bounds__(kThreads) void bins_kernel(Args a) {
     x[i] = u32x4_t{Bits<T>::kNone, Bits<T>::kNone, Bits<T>::kNone, Bits<T>::kNone};
     if (v < r.vecs) x[i] = r.body[v];
   }
-  const int loose = r.loose(a, chunk);
+  const int loose = r.loose(chunk == 0, chunk == a.chunks - 1);
   const float single = loose >= 0 ? Bits<T>::one(r.p, loose) : -__builtin_inff();
   for (int i = threadIdx.x; i < kBins; i += kThreads) sums[i] = 0, counts[i] = 0;
   Rule rule(a, row);
   const double min_p = a.min_ps ? double(a.min_ps[row]) : a.min_p;
   const int top_k = rule.greedy ? 1 : a.top_ks ? a.top_ks[row] : a.top_k;
-  float top = fmaxf(single, -__builtin_inff());         // fmaxf passes NaN by
-#pragma unroll
-  for (int i = 0; i < VECS; ++i)
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) top = fmaxf(top, Bits<T>::get(x[i], j));
-  top = block_max<kThreads / 64>(top, part);
   const size_t at = size_t(row) * a.chunks + chunk;
+  float* strips = a.strips + at * (kThreads / 64 * VECS) + (threadIdx.x >> 6);
+  float top = wave_max(fmaxf(single, -__builtin_inff()));            // fmaxf passes NaN by
+#pragma unroll
+  for (int i = 0; i < VECS; ++i) {
+    float v = -__builtin_inff();
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) v = fmaxf(v, Bits<T>::get(x[i], j));
+    v = wave_max(v);
+    if ((threadIdx.x & 63) == 0) strips[i * (kThreads / 64)] = v;
+    top = fmaxf(top, v);
+  }
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) top = fmaxf(top, part[w]);
   if (threadIdx.x == 0) a.tops[at] = top;
   if (top == -__builtin_inff()) return;                 // its bins are not read
   rule.set_top(top);
@@ -305,7 +320,7 @@ __global__ __launch_bounds__(kThreads) void bins_kernel(Args a) {
 // LDS of the choice.
 struct Shared {
   uint64_t list[kRowWaves][kWaveList];     // keys, each wave's own
-  uint64_t few_key[64], few_sum[64];
+  uint64_t few_key[kFew], few_sum[kFew];
   uint64_t sums[kBins];
   uint64_t part_a[kRowWaves], part_b[kRowWaves];
   uint32_t counts[kBins];
@@ -313,12 +328,11 @@ struct Shared {
   uint32_t listed[kRowWaves];              // keys of each wave's list
   double factor[kMaxChunks];               // of a chunk's sums
   int32_t shift[kMaxChunks];               // from the row's bins to the chunk's; kBins: no chunk to look at
-  int32_t visit[kMaxChunks];
-  uint32_t visits, few, count, upto_count, over;
+  uint16_t visit[kMaxStrips];
+  uint32_t visits, over, few, count, upto;
   int bin;
-  uint64_t before, inside, key;
+  uint64_t before, inside, key, all;
   uint32_t count_before;
-  float from, to;
 };
 
 // What is looked for in the order: the `count`-th token (count > 0), or the first whose sum from the top reaches `sum`.
@@ -364,184 +378,211 @@ struct Choice {
   const Args& a;
   const Rule& rule;
   const Row<T>& row;
-  int index;                               // of the row
+  const float (&strips)[kMaxStrips / kRowThreads];     // the thread's strips' largest logits
   // Thread t's bin (t < kBins): sum and count, by itself and through it from the top.
   uint64_t own, sum;
   uint32_t mine, count;
-  int low = 0, high = -1;                  // bins that the list holds whole
+  int low = 0, high = -1;                  // bins whose tokens are at hand: listed, and in order if there are few
+  bool ordered = false;
+  // Of those in order, a token for four threads: its key and weight, the sum and count from the first through it; what
+  // lies above the first.
+  uint64_t key = 0, weight = 0, upto = 0, above = 0;
+  uint32_t rank = 0, above_n = 0, tokens = 0;
 
-  // Before the tokens of bins lo .. hi are gone through: the chunks that have any, and the bins' logits [from, to].
-  __device__ void aim(int lo, int hi) {
-    const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
-    if (t == 0) s.visits = 0, s.over = 0;
-    __syncthreads();
-    if (wave == kRowWaves - 1) {
-      const float guess = fminf(fmaxf((rule.base - float(hi)) / rule.grid, -3.4e38f), rule.top);
-      const uint32_t first = first_logit(guess, order_of(rule.top), [&](float l) { return rule.bin(l) <= hi; });
-      if (lane == 0) s.from = logit_of(first);
-    } else if (wave == kRowWaves - 2) {
-      uint32_t first = order_of(rule.top) + 1;
-      if (lo > 0) {
-        const float guess = fminf(fmaxf((rule.base - float(lo - 1)) / rule.grid, -3.4e38f), rule.top);
-        first = first_logit(guess, order_of(rule.top), [&](float l) { return rule.bin(l) < lo; });
-      }
-      if (lane == 0) s.to = lo > 0 ? logit_of(first - 1) : rule.top;
-    } else {
-      // A wave for a chunk at a time, a lane for a bin.
-      for (int c = wave; c < a.chunks; c += kRowWaves - 2) {
-        const int shift = s.shift[c], from = max(lo - shift, 0), to = hi - shift;
-        const uint32_t* n = a.counts + (size_t(index) * a.chunks + c) * kBins;
-        uint32_t any = 0;
-        for (int b = from + lane; b <= to; b += 64) any |= n[b];
-        if (__any(any != 0) && lane == 0) s.visit[atomicAdd(&s.visits, 1u)] = c;
-      }
-    }
-    __syncthreads();
-  }
-  // f(logit, index) for the tokens that were aimed at.
-  template <class F>
-  __device__ void tokens(F f) {
-    const float from = s.from, to = s.to;
-    constexpr int kVec = Bits<T>::kVec, kAhead = 8 / kVec;
-    const int all = int(s.visits) << a.chunk_shift;
-    for (int v0 = threadIdx.x; v0 < all; v0 += kAhead * kRowThreads) {
-      u32x4_t x[kAhead];
-      int at[kAhead];
+  __device__ uint64_t weight_of(uint64_t k) const { return rule.near_weight(logit_of(uint32_t(k >> 32))); }
+
+  // f(whether it is one, logit, index) for the tokens of bins lo .. hi among the others, by whole waves.
+  template <int AHEAD, class F>
+  __device__ void walk(int lo, int hi, F f) {
+    constexpr int kVec = Bits<T>::kVec;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, visits = int(s.visits);
+    const auto look = [&](float l, int i, bool there) {
+      const int b = rule.bin(l);
+      f(there && b >= lo && b <= hi, l, i);
+    };
+    for (int v = wave; v < visits; v += AHEAD * kRowWaves) {
+      u32x4_t x[AHEAD];
+      int at[AHEAD];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int v = v0 + i * kRowThreads;
-        at[i] = v < all ? (s.visit[v >> a.chunk_shift] << a.chunk_shift) + (v & ((1 << a.chunk_shift) - 1)) : row.vecs;
+      for (int i = 0; i < AHEAD; ++i) {
+        const int n = v + i * kRowWaves;
+        at[i] = n < visits ? s.visit[n] * 64 + lane : row.vecs;
         x[i] = u32x4_t{Bits<T>::kNone, Bits<T>::kNone, Bits<T>::kNone, Bits<T>::kNone};
         if (at[i] < row.vecs) x[i] = row.body[at[i]];
       }
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
+      for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          const float l = Bits<T>::get(x[i], j);
-          if (l >= from && l <= to && at[i] < row.vecs) f(l, row.head + at[i] * kVec + j);
-        }
-      }
+        for (int j = 0; j < kVec; ++j) look(Bits<T>::get(x[i], j), row.head + at[i] * kVec + j, at[i] < row.vecs);
     }
-    for (uint32_t i = 0; i < s.visits; ++i) {
-      const int loose = row.loose(a, s.visit[i]);
-      if (loose < 0) continue;
-      const float l = Bits<T>::one(row.p, loose);
-      if (l >= from && l <= to) f(l, loose);
+    if (wave < 2) {
+      const int loose = row.loose(true, true);
+      look(loose >= 0 ? Bits<T>::one(row.p, loose) : 0.f, loose, loose >= 0);
     }
   }
-  // Have the tokens of a bin at hand: listed, with all above them if these are few, or aimed at.
+  // Have the tokens of a bin at hand, and all above them if these are few.
   __device__ void open(int bin) {
     if (bin >= low && bin <= high) return;
-    const int t = threadIdx.x, wave = t >> 6;
+    const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
     __syncthreads();
-    if (t == bin) s.count = mine, s.upto_count = count;
+    if (t == bin) s.upto = count, s.count = mine, s.before = sum - own;
+    if (t == 0) s.visits = 0, s.over = 0;
     __syncthreads();
-    const uint32_t upto = s.upto_count;
-    const int lo = upto <= kFew ? 0 : bin;
-    low = 0, high = -1;
-    aim(lo, bin);
-    if (s.count > kRowWaves * kWaveList) return;
-    if ((t & 63) == 0) s.listed[wave] = 0;
-    tokens([&](float l, int i) {
-      const uint32_t at = atomicAdd(&s.listed[wave], 1u);
-      if (at < kWaveList) s.list[wave][at] = key_of(l, i);
-      else s.over = 1;
+    const bool all = s.upto <= kFew;
+    const int lo = all ? 0 : bin;
+    above = all ? 0 : s.before;
+    above_n = all ? 0 : s.upto - s.count;
+    const uint32_t n = all ? s.upto : s.count;
+    const int strips_n = a.chunks << (a.chunk_shift - 6);
+#pragma unroll
+    for (int i = 0; i < kMaxStrips / kRowThreads; ++i) {
+      if (i * kRowThreads >= strips_n) break;
+      const bool any = t + i * kRowThreads < strips_n && rule.bin(strips[i]) <= bin;
+      const uint64_t those = __ballot(any);
+      uint32_t at = 0;
+      if (lane == 0 && those) at = atomicAdd(&s.visits, uint32_t(__popcll(those)));
+      at = __builtin_amdgcn_readfirstlane(at);
+      if (any) s.visit[at + __popcll(those & ((uint64_t(1) << lane) - 1))] = uint16_t(t + i * kRowThreads);
+    }
+    __syncthreads();
+    low = 0, high = -1, ordered = false;
+    if (n > kRowWaves * kWaveList) return;
+    uint32_t filled = 0;
+    walk<16 / Bits<T>::kVec>(lo, bin, [&](bool is, float l, int i) {
+      const uint64_t those = __ballot(is);
+      if (!those) return;
+      const uint32_t at = filled + __popcll(those & ((uint64_t(1) << lane) - 1));
+      if (is && at < kWaveList) s.list[wave][at] = key_of(l, i);
+      filled += __popcll(those);
     });
+    if (lane == 0) {
+      s.listed[wave] = filled;
+      if (filled > kWaveList) s.over = 1;               // gone through again each time
+    }
     __syncthreads();
-    if (s.over) return;                                 // a wave had more than its list holds: gone through again
+    if (s.over) return;
     low = lo, high = bin;
+    order();
+  }
+  // Put what is listed in order by counting, if it is few: the list also has tokens that top_k dropped from a chunk.
+  __device__ void order() {
+    const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
+    uint32_t from = 0, n = 0;
+#pragma unroll
+    for (int w = 0; w < kRowWaves; ++w) {
+      from += w < wave ? s.listed[w] : 0;
+      n += s.listed[w];
+    }
+    if (n > kFew) return;
+    for (uint32_t i = lane; i < s.listed[wave]; i += 64) {
+      const uint64_t k = s.list[wave][i];
+      s.few_key[from + i] = k;
+      s.few_sum[from + i] = weight_of(k);
+    }
+    __syncthreads();
+    tokens = n;
+    const uint32_t i = t >> 2;
+    key = i < n ? s.few_key[i] : 0;
+    weight = i < n ? s.few_sum[i] : 0;
+    upto = 0, rank = 0;
+    if (i < ((n + 15) & ~15u)) {
+      for (uint32_t j = t & 3; j < n; j += 4)
+        if (s.few_key[j] >= key) upto += s.few_sum[j], ++rank;
+#pragma unroll
+      for (int m = 1; m < 4; m *= 2) upto += __shfl_xor(static_cast<unsigned long long>(upto), m), rank += __shfl_xor(rank, m);
+    }
+    if (i < n && rank == n) s.all = upto;
+    __syncthreads();
+    ordered = true;
   }
   // f(key) for the opened bin's tokens.
   template <class F>
   __device__ void each(int bin, F f) {
     if (bin >= low && bin <= high) {
       const int wave = threadIdx.x >> 6;
-      const uint32_t n = s.listed[wave];
-      for (uint32_t i = threadIdx.x & 63; i < n; i += 64) {
-        const uint64_t key = s.list[wave][i];
-        if (rule.bin(logit_of(uint32_t(key >> 32))) == bin) f(key);
+      for (uint32_t i = threadIdx.x & 63; i < s.listed[wave]; i += 64) {
+        const uint64_t k = s.list[wave][i];
+        if (rule.bin(logit_of(uint32_t(k >> 32))) == bin) f(k);
       }
     } else {
-      tokens([&](float l, int i) {
-        if (rule.bin(l) == bin) f(key_of(l, i));
+      walk<1>(bin, bin, [&](bool is, float l, int i) {
+        if (is) f(key_of(l, i));
       });
     }
   }
-  __device__ uint64_t weight(uint64_t key) const { return rule.near_weight(logit_of(uint32_t(key >> 32))); }
   // Sums over the block.
-  __device__ void total(uint64_t& sum, uint32_t& n) {
-    sum = wave_sum(sum);
-    n = uint32_t(wave_sum(n));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) s.part_a[threadIdx.x >> 6] = sum, s.part_c[threadIdx.x >> 6] = n;
-    __syncthreads();
-    sum = 0, n = 0;
+  __device__ void total(uint64_t& v, uint32_t& n) {
 #pragma unroll
-    for (int w = 0; w < kRowWaves; ++w) sum += s.part_a[w], n += s.part_c[w];
-  }
-  // The goal's bin: s.bin, what lies in it, s.inside, and what above it, s.before and s.count_before.
-  __device__ void find(const Goal& g) {
+    for (int m = 32; m; m >>= 1) v += __shfl_xor(static_cast<unsigned long long>(v), m), n += __shfl_xor(n, m);
     __syncthreads();
-    if (threadIdx.x < kBins && g.here(sum, own, count, mine)) {
-      s.bin = threadIdx.x;
+    if ((threadIdx.x & 63) == 0) s.part_a[threadIdx.x >> 6] = v, s.part_c[threadIdx.x >> 6] = n;
+    __syncthreads();
+    v = 0, n = 0;
+#pragma unroll
+    for (int w = 0; w < kRowWaves; ++w) v += s.part_a[w], n += s.part_c[w];
+  }
+  // What is kept by min_p: the tokens whose logit's order is `border` or above, of which `bin` has the last.
+  __device__ void cut(uint32_t border, int bin, uint64_t* kept, uint32_t* left) {
+    const int t = threadIdx.x;
+    open(bin);
+    uint64_t part = 0;
+    uint32_t n = 0;
+    each(bin, [&](uint64_t k) {
+      if (uint32_t(k >> 32) >= border) part += weight_of(k), ++n;
+    });
+    total(part, n);
+    if (t == bin) {
+      s.before = sum - own + (part < own ? part : own);      // no more than the bins hold
+      s.count = count - mine + n;
+    }
+    __syncthreads();
+    *kept = s.before, *left = s.count;
+  }
+  // The goal's token; *through becomes the sum from the top through it.  Called by all threads alike.
+  __device__ uint64_t find(Goal g, uint64_t* through) {
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    __syncthreads();
+    if (t < kBins && g.here(sum, own, count, mine)) {
+      s.bin = t;
       s.before = sum - own;
       s.inside = own;
       s.count_before = count - mine;
     }
     __syncthreads();
-  }
-  // The key of the goal's token among the opened bin's (the goal counted from the bin's start); *upto becomes the sum
-  // from the bin's start through it.  Called by all threads alike.
-  __device__ uint64_t resolve(int bin, Goal g, uint64_t* upto) {
-    uint64_t lo = 0, hi = ~uint64_t(0), above = 0;
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    bool clamped = false;
-    for (;;) {
-      // Few enough for one wave to put them in order by counting?
-      if (t == 0) s.few = 0;
+    const int bin = s.bin;
+    const uint64_t before = s.before, end = before + s.inside;
+    const uint32_t before_n = s.count_before;
+    open(bin);
+    // Sums of tokens weighed at the row's top may miss those of the chunks by their last units: goals are cut to what
+    // is there, and no more is kept than the bins hold, so that what is drawn lies in the kept run.
+    if (ordered) {
+      if (g.count) g.count = min(g.count - above_n, tokens);
+      else g.sum = g.sum - above < s.all ? g.sum - above : s.all;
+      if (g.sum == 0 && g.count == 0) g.count = 1;
       __syncthreads();
-      each(bin, [&](uint64_t k) {
-        if (k < lo || k > hi) return;
-        const uint32_t at = atomicAdd(&s.few, 1u);
-        if (at < 64) s.few_key[at] = k, s.few_sum[at] = weight(k);
-      });
+      if (uint32_t(t >> 2) < tokens && g.here(upto, weight, rank, 1)) s.key = key, s.before = upto;
       __syncthreads();
-      const uint32_t n = s.few;
-      if (n <= 64) {
-        if (wave == 0) {
-          const uint64_t k = lane < int(n) ? s.few_key[lane] : 0, w = lane < int(n) ? s.few_sum[lane] : 0;
-          // Sums of tokens weighed at the row's top may miss those of the chunks by their last units.
-          const uint64_t all = wave_sum(w);
-          if (g.count) g.count = min(g.count, n);
-          else if (all == 0) g.count = 1;
-          else g.sum = g.sum < all ? g.sum : all;
-          uint64_t sum_k = 0;
-          uint32_t n_k = 0;
-          for (uint32_t j = 0; j < n; ++j)
-            if (s.few_key[j] >= k) sum_k += s.few_sum[j], ++n_k;
-          if (lane < int(n) && g.here(sum_k, w, n_k, 1)) s.key = k, s.before = sum_k;
-        }
-        __syncthreads();
-        *upto = above + s.before;
-        return s.key;
-      }
+      const uint64_t got = above + s.before;
+      *through = got < end ? got : end;
+      return s.key;
+    }
+    if (g.count) g.count -= before_n;
+    else g.sum -= before;
+    uint64_t lo = 0, hi = ~uint64_t(0), passed = 0, all = 0;
+    uint32_t n = 0;
+    each(bin, [&](uint64_t k) { all += weight_of(k), ++n; });
+    total(all, n);
+    if (g.count) g.count = min(g.count, n);
+    else if (all == 0) g.count = 1;
+    else g.sum = g.sum < all ? g.sum : all;
+    while (n > 64) {
       // The keys' range, then bins over it.
-      uint64_t least = ~uint64_t(0), most = 0, all = 0;
-      uint32_t any = 0;
+      uint64_t least = ~uint64_t(0), most = 0;
       each(bin, [&](uint64_t k) {
         if (k < lo || k > hi) return;
         least = k < least ? k : least;
         most = k > most ? k : most;
-        if (!clamped) all += weight(k), ++any;
       });
-      if (!clamped) {
-        total(all, any);
-        if (g.count) g.count = min(g.count, any);
-        else if (all == 0) g.count = 1;
-        else g.sum = g.sum < all ? g.sum : all;
-        clamped = true;
-      }
 #pragma unroll
       for (int m = 32; m; m >>= 1) {
         const uint64_t x = __shfl_xor(static_cast<unsigned long long>(least), m);
@@ -561,7 +602,7 @@ struct Choice {
       each(bin, [&](uint64_t k) {
         if (k < lo || k > hi) return;
         const int b = int((most - k) >> shift);
-        atomicAdd(reinterpret_cast<unsigned long long*>(&s.sums[b]), static_cast<unsigned long long>(weight(k)));
+        atomicAdd(reinterpret_cast<unsigned long long*>(&s.sums[b]), static_cast<unsigned long long>(weight_of(k)));
         atomicAdd(&s.counts[b], 1u);
       });
       __syncthreads();
@@ -574,15 +615,39 @@ struct Choice {
         s.bin = t;
         s.before = upto_b - part;
         s.count_before = upto_n - part_n;
+        s.count = part_n;
       }
       __syncthreads();
       hi = most - (uint64_t(s.bin) << shift);
       lo = hi - ((uint64_t(1) << shift) - 1);
       if (lo > hi) lo = 0;                               // below zero: the last bin may reach past the least key
-      above += s.before;
+      n = s.count;
+      passed += s.before;
       if (g.count) g.count -= s.count_before;
       else g.sum -= s.before;
     }
+    // At most 64: one wave puts them in order by counting.
+    __syncthreads();
+    if (t == 0) s.few = 0;
+    __syncthreads();
+    each(bin, [&](uint64_t k) {
+      if (k < lo || k > hi) return;
+      const uint32_t at = atomicAdd(&s.few, 1u);
+      if (at < 64) s.few_key[at] = k, s.few_sum[at] = weight_of(k);
+    });
+    __syncthreads();
+    if (wave == 0) {
+      const uint64_t k = lane < int(n) ? s.few_key[lane] : 0, w = lane < int(n) ? s.few_sum[lane] : 0;
+      uint64_t sum_k = 0;
+      uint32_t n_k = 0;
+      for (uint32_t j = 0; j < n; ++j)
+        if (s.few_key[j] >= k) sum_k += s.few_sum[j], ++n_k;
+      if (lane < int(n) && g.here(sum_k, w, n_k, 1)) s.key = k, s.before = sum_k;
+    }
+    __syncthreads();
+    const uint64_t got = before + passed + s.before;
+    *through = got < end ? got : end;
+    return s.key;
   }
 };
 
@@ -598,9 +663,14 @@ __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
   const float u = a.u[index];
   const size_t first_chunk = size_t(index) * a.chunks;
   const float chunk_top = a.tops[first_chunk + min(lane, a.chunks - 1)];
-  float top = chunk_top;
+  const int strips_n = a.chunks << (a.chunk_shift - 6);
+  float strips[kMaxStrips / kRowThreads];
 #pragma unroll
-  for (int m = 32; m; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
+  for (int i = 0; i < kMaxStrips / kRowThreads; ++i) {
+    const int at = t + i * kRowThreads;
+    strips[i] = at < strips_n ? a.strips[size_t(index) * strips_n + at] : 0.f;
+  }
+  const float top = wave_max(chunk_top);
   if (top == -__builtin_inff()) {
     if (t == 0) {
       a.ids[index] = -1;
@@ -641,28 +711,14 @@ __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
   uint64_t kept = s.before;                             // the sum and the count of what is kept so far
   uint32_t left = s.count;
   const Row<T> row(a, index);
-  Choice<T> pick{s, a, rule, row, index, own, sum, mine, count};
+  Choice<T> pick{s, a, rule, row, strips, own, sum, mine, count};
   if (!rule.greedy && min_p > 0.0) {
-    // The least logit with e >= min_p, its bin, and what lies above that.
+    // The least logit with e >= min_p.
     const double least = fmin(min_p, 1.0);
     const float guess = float(double(top) + log2(least) / rule.rate);
     const uint32_t border = first_logit(guess < top ? guess : top, order_of(top), [&](float l) { return rule.e(l) >= least; });
     const int bin = rule.bin(logit_of(border));
-    if (bin < kBins) {
-      pick.open(bin);
-      uint64_t part = 0;
-      uint32_t n = 0;
-      pick.each(bin, [&](uint64_t k) {
-        if (uint32_t(k >> 32) >= border) part += pick.weight(k), ++n;
-      });
-      pick.total(part, n);
-      if (t == bin) {
-        s.before = sum - own + (part < own ? part : own);     // no more than the bins hold
-        s.count = count - mine + n;
-      }
-      __syncthreads();
-      kept = s.before, left = s.count;
-    }
+    if (bin < kBins) pick.cut(border, bin, &kept, &left);
   }
   uint64_t key = 0;
   for (int stage = 0; stage < 3; ++stage) {
@@ -678,17 +734,9 @@ __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
       const uint64_t past = uint64_t(fmin(double(u), 1.0) * double(kept));
       g.sum = (past < kept ? past : kept - 1) + 1;
     }
-    pick.find(g);
-    const int bin = s.bin;
-    const uint64_t before = s.before, inside = s.inside;
-    if (g.count) g.count -= s.count_before;
-    else g.sum -= before;
-    pick.open(bin);
-    uint64_t upto;
-    key = pick.resolve(bin, g, &upto);
-    // No more than the bins hold, so that what is drawn lies in this run.
-    upto = upto < inside ? upto : inside;
-    if (stage < 2) kept = before + upto > 0 ? before + upto : 1;
+    uint64_t through;
+    key = pick.find(g, &through);
+    if (stage < 2) kept = through > 0 ? through : 1;
   }
   if (t == 0) {
     a.ids[index] = int(~uint32_t(key));
@@ -733,7 +781,8 @@ hipError_t launch(const Args& a, bool large, int64_t rows, hipStream_t stream) {
 }  // namespace
 
 size_t sample_workspace(int64_t rows, int64_t vocab, int64_t type) {
-  return size_t(rows) * size_t(chunks_of(rows, vocab, type).count) * (kBins * 12 + 4);
+  const Chunks c = chunks_of(rows, vocab, type);
+  return size_t(rows) * size_t(c.count) * (kBins * 12 + 4 + size_t(c.vecs / 64) * 4);
 }
 
 hipError_t launch_sample(const tq2_sample_args& q, hipStream_t stream) {
@@ -759,6 +808,7 @@ hipError_t launch_sample(const tq2_sample_args& q, hipStream_t stream) {
   a.sums = static_cast<uint64_t*>(q.workspace);
   a.counts = reinterpret_cast<uint32_t*>(a.sums + parts * kBins);
   a.tops = reinterpret_cast<float*>(a.counts + parts * kBins);
+  a.strips = a.tops + parts;
   if (q.logits_type == TQ2_TYPE_F32) return launch<F32>(a, chunks.large, q.rows, stream);
   if (q.logits_type == TQ2_TYPE_F16) return launch<F16>(a, chunks.large, q.rows, stream);
   return launch<BF16>(a, chunks.large, q.rows, stream);
