@@ -11,9 +11,10 @@
 // borders lie within 1e-7 of u.)
 //
 // Two launches.  bins_kernel: blocks for chunks of each row, held in registers: their largest logit, then counts and sums
-// in bins of a fixed grid (11 to a factor of two in e, so that chunks agree on them).  choice_kernel: a block for each
-// row, which joins the chunks' bins at the row's largest logit and reads again only those chunks that have tokens in a bin
-// it needs.  Bound: logits are read from HBM once, and mostly a second time from the caches.
+// in bins of a fixed grid (11 to a factor of two in e, so that chunks agree on them), and the tokens' places ordered by
+// bin.  What min_p or top_k drop of a chunk alone is dropped at once.  choice_kernel: a block for each row, which joins the
+// chunks' bins at the row's largest logit and reads the tokens of the bins it needs.  Bound: logits are read from HBM
+// once, two bytes are written for each that is not dropped.
 #include "tq2_device.h"
 #include "tq2_sample_internal.h"
 #include "tq2_types.h"
@@ -29,12 +30,11 @@ constexpr int kBins = 512;
 constexpr float kGrid = 11.f;              // bins of a factor of two: 2^46.5 over all, more than a weight's 43 bits
 constexpr int kMaxChunks = 64;
 constexpr int kThreads = 1024;             // of bins_kernel
-constexpr int kSmall = 1, kLarge = 8;      // 16-byte vectors of a thread: chunks of 4096 to 65536 logits
+constexpr int kSmall = 1, kLarge = 4;      // 16-byte vectors of a thread: chunks of 4096 to 32768 logits
 constexpr int kRowThreads = 1024;          // of the choice
 constexpr int kRowWaves = kRowThreads / 64;
-constexpr int kWaveList = 256;             // tokens that each wave of the choice lists
+constexpr uint32_t kList = 4096;           // tokens of a bin that are held in LDS
 constexpr uint32_t kFew = kRowThreads / 4; // tokens that are put in order at once: four threads for each
-constexpr int kMaxStrips = 4 * kRowThreads;            // 2^20 f32 logits
 constexpr int kUnit = 43;                  // a token of the largest logit weighs 2^43
 constexpr double kCoolest = 1e-36;         // temperatures below act as this one
 
@@ -52,9 +52,10 @@ struct Args {
   int64_t row_stride;
   double temperature, top_p, min_p;
   uint64_t* sums;                          // [rows, chunks, kBins]
-  uint32_t* counts;
+  uint32_t* counts;                        // the same: where the bin's tokens start in `order`, in the upper half, and their number
   float* tops;                             // [rows, chunks]: largest logit
-  float* strips;                           // [rows, strips]: largest logit of each 64 vectors
+  uint16_t* order;                         // [rows, chunks, chunk_tokens]: places in the chunk, by bins
+  int32_t chunk_tokens;
 };
 
 // Element types by their bits, f32 by f32.
@@ -222,114 +223,121 @@ __device__ __forceinline__ int last_bin(double min_p) {
   return min_p > 0.0 ? min(kBins - 1, 2 - int(floor(log2(fmin(min_p, 1.0)) * double(kGrid)))) : kBins - 1;
 }
 
+// Tokens of a chunk: those of its vectors, and for the first and the last one the row's loose ones.
+template <class T, int VECS>
+constexpr int kChunkTokens = kThreads * VECS * Bits<T>::kVec + 16;
+
 template <class T, int VECS>
 __global__ __launch_bounds__(kThreads) void bins_kernel(Args a) {
+  constexpr int kVec = Bits<T>::kVec;
   __shared__ unsigned long long sums[kBins];
-  __shared__ uint32_t counts[kBins], part_a[kBins / 64], part_b[kBins / 64];
+  __shared__ uint32_t counts[kBins], starts[kBins], part_a[kBins / 64], part_b[kBins / 64];
+  __shared__ __attribute__((aligned(16))) uint16_t order[kChunkTokens<T, VECS>];
   __shared__ float part[kThreads / 64];
   __shared__ int last;
-  constexpr int kVec = Bits<T>::kVec;
-  const int chunk = blockIdx.x, row = blockIdx.y;
+  __shared__ uint32_t all;
+  const int chunk = blockIdx.x, row = blockIdx.y, t = threadIdx.x;
   const Row<T> r(a, row);
   u32x4_t x[VECS];
 #pragma unroll
   for (int i = 0; i < VECS; ++i) {
-    const int v = chunk * (kThreads * VECS) + i * kThreads + threadIdx.x;
+    const int v = chunk * (kThreads * VECS) + i * kThreads + t;
     x[i] = u32x4_t{Bits<T>::kNone, Bits<T>::kNone, Bits<T>::kNone, Bits<T>::kNone};
     if (v < r.vecs) x[i] = r.body[v];
   }
   const int loose = r.loose(chunk == 0, chunk == a.chunks - 1);
   const float single = loose >= 0 ? Bits<T>::one(r.p, loose) : -__builtin_inff();
-  for (int i = threadIdx.x; i < kBins; i += kThreads) sums[i] = 0, counts[i] = 0;
+  for (int i = t; i < kBins; i += kThreads) sums[i] = 0, counts[i] = 0;
   Rule rule(a, row);
   const double min_p = a.min_ps ? double(a.min_ps[row]) : a.min_p;
   const int top_k = rule.greedy ? 1 : a.top_ks ? a.top_ks[row] : a.top_k;
-  const size_t at = size_t(row) * a.chunks + chunk;
-  float* strips = a.strips + at * (kThreads / 64 * VECS) + (threadIdx.x >> 6);
-  float top = wave_max(fmaxf(single, -__builtin_inff()));            // fmaxf passes NaN by
+  float top = fmaxf(single, -__builtin_inff());         // fmaxf passes NaN by
 #pragma unroll
-  for (int i = 0; i < VECS; ++i) {
-    float v = -__builtin_inff();
+  for (int i = 0; i < VECS; ++i)
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) v = fmaxf(v, Bits<T>::get(x[i], j));
-    v = wave_max(v);
-    if ((threadIdx.x & 63) == 0) strips[i * (kThreads / 64)] = v;
-    top = fmaxf(top, v);
-  }
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+    for (int j = 0; j < kVec; ++j) top = fmaxf(top, Bits<T>::get(x[i], j));
+  top = wave_max(top);
+  if ((t & 63) == 0) part[t >> 6] = top;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kThreads / 64; ++w) top = fmaxf(top, part[w]);
-  if (threadIdx.x == 0) a.tops[at] = top;
+  const size_t at = size_t(row) * a.chunks + chunk;
+  if (t == 0) a.tops[at] = top;
   if (top == -__builtin_inff()) return;                 // its bins are not read
   rule.set_top(top);
-  // What min_p or top_k drop of a chunk by itself is no part of the row's either: no weights for it.
+  // Each token's bin and its number there.  What min_p drops of a chunk by itself is no part of the row's either.
+  constexpr uint32_t kDropped = ~0u;
   int cut = last_bin(min_p);
-  const bool first_k = top_k > 0 && top_k < a.vocab;
-  if (first_k) {
+  const auto place = [&](float l) {
+    const int b = rule.bin(l);
+    return b <= cut ? uint32_t(b) << 16 | atomicAdd(&counts[b], 1u) : kDropped;
+  };
+  uint32_t code[VECS][kVec];
 #pragma unroll
-    for (int i = 0; i < VECS; ++i) {
-      const u32x4_t v = x[i];
+  for (int i = 0; i < VECS; ++i)
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const int b = rule.bin(Bits<T>::get(v, j));
-        if (b <= cut) atomicAdd(&counts[b], 1u);
-      }
-    }
-    if (loose >= 0 && rule.bin(single) <= cut) atomicAdd(&counts[rule.bin(single)], 1u);
-    if (threadIdx.x == 0) last = cut;
-    __syncthreads();
-    const uint32_t own = threadIdx.x < kBins ? counts[threadIdx.x] : 0;
-    uint32_t upto = own, none = 0;
-    scan(upto, none, part_a, part_b);
-    if (threadIdx.x < kBins && upto >= uint32_t(top_k) && upto - own < uint32_t(top_k)) last = threadIdx.x;
-    __syncthreads();
-    cut = last;
-    if (int(threadIdx.x) < kBins && int(threadIdx.x) > cut) counts[threadIdx.x] = 0;
+    for (int j = 0; j < kVec; ++j) code[i][j] = place(Bits<T>::get(x[i], j));
+  const uint32_t code_single = loose >= 0 ? place(single) : kDropped;
+  if (t == 0) last = cut;
+  __syncthreads();
+  const uint32_t own = t < kBins ? counts[t] : 0;
+  uint32_t upto = own, none = 0;
+  scan(upto, none, part_a, part_b);
+  if (t < kBins) {
+    starts[t] = upto - own;
+    // Nor is what top_k drops.
+    if (top_k > 0 && upto >= uint32_t(top_k) && upto - own < uint32_t(top_k)) last = t;
   }
+  __syncthreads();
+  cut = last;
+  if (t == cut) all = upto;
+  // Weights, and the tokens by their bins.
+  const int base = chunk == 0 ? 0 : r.head + chunk * (kThreads * VECS * kVec);
 #pragma unroll
   for (int i = 0; i < VECS; ++i) {
-    const u32x4_t v = x[i];
-    int b[kVec];
     bool any = false;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      b[j] = rule.bin(Bits<T>::get(v, j));
-      any |= b[j] <= cut;
-    }
+    for (int j = 0; j < kVec; ++j) any |= int(code[i][j] >> 16) <= cut;
     if (!__any(any)) continue;
     // The exponentials side by side: each is one long chain.
     uint64_t w[kVec];
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) w[j] = rule.near_weight(Bits<T>::get(v, j));
+    for (int j = 0; j < kVec; ++j) w[j] = rule.near_weight(Bits<T>::get(x[i], j));
+    const int first = r.head + (chunk * (kThreads * VECS) + i * kThreads + t) * kVec - base;
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-      if (b[j] > cut) continue;
-      atomicAdd(&sums[b[j]], static_cast<unsigned long long>(w[j]));
-      if (!first_k) atomicAdd(&counts[b[j]], 1u);
+      const int b = int(code[i][j] >> 16);
+      if (b > cut) continue;
+      atomicAdd(&sums[b], static_cast<unsigned long long>(w[j]));
+      order[starts[b] + (code[i][j] & 0xFFFFu)] = uint16_t(first + j);
     }
   }
-  if (loose >= 0 && rule.bin(single) <= cut) {
-    atomicAdd(&sums[rule.bin(single)], static_cast<unsigned long long>(rule.near_weight(single)));
-    if (!first_k) atomicAdd(&counts[rule.bin(single)], 1u);
+  if (int(code_single >> 16) <= cut) {
+    const int b = int(code_single >> 16);
+    atomicAdd(&sums[b], static_cast<unsigned long long>(rule.near_weight(single)));
+    order[starts[b] + (code_single & 0xFFFFu)] = uint16_t(loose - base);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < kBins; i += kThreads) a.sums[at * kBins + i] = sums[i], a.counts[at * kBins + i] = counts[i];
+  if (t < kBins) {
+    a.sums[at * kBins + t] = sums[t];
+    a.counts[at * kBins + t] = t <= cut ? starts[t] << 16 | own : all << 16;
+  }
+  u32x4_t* out = reinterpret_cast<u32x4_t*>(a.order + at * a.chunk_tokens);
+  for (int i = t; i * 8 < int(all); i += kThreads) out[i] = reinterpret_cast<const u32x4_t*>(order)[i];
 }
 
 // LDS of the choice.
 struct Shared {
-  uint64_t list[kRowWaves][kWaveList];     // keys, each wave's own
-  uint64_t few_key[kFew], few_sum[kFew];
+  uint64_t list[kList], weights[kList];    // keys of the tokens at hand and their weights
   uint64_t sums[kBins];
   uint64_t part_a[kRowWaves], part_b[kRowWaves];
   uint32_t counts[kBins];
   uint32_t part_c[kRowWaves];
-  uint32_t listed[kRowWaves];              // keys of each wave's list
   double factor[kMaxChunks];               // of a chunk's sums
   int32_t shift[kMaxChunks];               // from the row's bins to the chunk's; kBins: no chunk to look at
-  uint16_t visit[kMaxStrips];
-  uint32_t visits, over, few, count, upto;
+  uint32_t from[kMaxChunks], past[kMaxChunks];         // of a chunk's tokens at hand: the first in its order, where they end
+  uint64_t few_key[64], few_sum[64];
+  uint32_t few, count, upto;
   int bin;
   uint64_t before, inside, key, all;
   uint32_t count_before;
@@ -378,136 +386,105 @@ struct Choice {
   const Args& a;
   const Rule& rule;
   const Row<T>& row;
-  const float (&strips)[kMaxStrips / kRowThreads];     // the thread's strips' largest logits
+  int index;                               // of the row
   // Thread t's bin (t < kBins): sum and count, by itself and through it from the top.
   uint64_t own, sum;
   uint32_t mine, count;
-  int low = 0, high = -1;                  // bins whose tokens are at hand: listed, and in order if there are few
-  bool ordered = false;
+  // Bins whose tokens are at hand: listed if they fit, and in order if there are few.
+  int low = 0, high = -1;
+  bool listed = false, ordered = false;
+  uint32_t tokens = 0;
   // Of those in order, a token for four threads: its key and weight, the sum and count from the first through it; what
   // lies above the first.
   uint64_t key = 0, weight = 0, upto = 0, above = 0;
-  uint32_t rank = 0, above_n = 0, tokens = 0;
+  uint32_t rank = 0, above_n = 0;
 
   __device__ uint64_t weight_of(uint64_t k) const { return rule.near_weight(logit_of(uint32_t(k >> 32))); }
 
-  // f(whether it is one, logit, index) for the tokens of bins lo .. hi among the others, by whole waves.
-  template <int AHEAD, class F>
-  __device__ void walk(int lo, int hi, F f) {
-    constexpr int kVec = Bits<T>::kVec;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, visits = int(s.visits);
-    const auto look = [&](float l, int i, bool there) {
-      const int b = rule.bin(l);
-      f(there && b >= lo && b <= hi, l, i);
-    };
-    for (int v = wave; v < visits; v += AHEAD * kRowWaves) {
-      u32x4_t x[AHEAD];
-      int at[AHEAD];
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
-        const int n = v + i * kRowWaves;
-        at[i] = n < visits ? s.visit[n] * 64 + lane : row.vecs;
-        x[i] = u32x4_t{Bits<T>::kNone, Bits<T>::kNone, Bits<T>::kNone, Bits<T>::kNone};
-        if (at[i] < row.vecs) x[i] = row.body[at[i]];
+  // f(place, key) for the tokens at hand, from the chunks' orders: a wave for a chunk at a time.
+  template <class F>
+  __device__ void read(F f) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    for (int c = wave; c < a.chunks; c += kRowWaves) {
+      const uint32_t at = c ? s.past[c - 1] : 0, n = s.past[c] - at, from = s.from[c];
+      const uint16_t* order = a.order + (size_t(index) * a.chunks + c) * a.chunk_tokens + from;
+      const int base = c == 0 ? 0 : row.head + (c << a.chunk_shift) * Bits<T>::kVec;
+#pragma unroll 4
+      for (uint32_t i = lane; i < n; i += 64) {
+        const int token = base + order[i];
+        f(at + i, key_of(Bits<T>::one(row.p, token), token));
       }
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i)
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) look(Bits<T>::get(x[i], j), row.head + at[i] * kVec + j, at[i] < row.vecs);
-    }
-    if (wave < 2) {
-      const int loose = row.loose(true, true);
-      look(loose >= 0 ? Bits<T>::one(row.p, loose) : 0.f, loose, loose >= 0);
     }
   }
   // Have the tokens of a bin at hand, and all above them if these are few.
   __device__ void open(int bin) {
     if (bin >= low && bin <= high) return;
-    const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
+    const int t = threadIdx.x;
     __syncthreads();
     if (t == bin) s.upto = count, s.count = mine, s.before = sum - own;
-    if (t == 0) s.visits = 0, s.over = 0;
     __syncthreads();
     const bool all = s.upto <= kFew;
-    const int lo = all ? 0 : bin;
+    low = all ? 0 : bin, high = bin;
     above = all ? 0 : s.before;
     above_n = all ? 0 : s.upto - s.count;
-    const uint32_t n = all ? s.upto : s.count;
-    const int strips_n = a.chunks << (a.chunk_shift - 6);
+    tokens = all ? s.upto : s.count;
+    if (t < 64) {
+      uint32_t n = 0;
+      if (t < a.chunks) {
+        const int first = max(low - s.shift[t], 0), last = bin - s.shift[t];
+        if (last >= 0) {
+          const uint32_t* packed = a.counts + (size_t(index) * a.chunks + t) * kBins;
+          const uint32_t end = packed[last], begin = first > 0 ? packed[first] >> 16 : 0;
+          s.from[t] = begin;
+          n = (end >> 16) + (end & 0xFFFFu) - begin;
+        }
+      }
 #pragma unroll
-    for (int i = 0; i < kMaxStrips / kRowThreads; ++i) {
-      if (i * kRowThreads >= strips_n) break;
-      const bool any = t + i * kRowThreads < strips_n && rule.bin(strips[i]) <= bin;
-      const uint64_t those = __ballot(any);
-      uint32_t at = 0;
-      if (lane == 0 && those) at = atomicAdd(&s.visits, uint32_t(__popcll(those)));
-      at = __builtin_amdgcn_readfirstlane(at);
-      if (any) s.visit[at + __popcll(those & ((uint64_t(1) << lane) - 1))] = uint16_t(t + i * kRowThreads);
+      for (int d = 1; d < 64; d *= 2) {
+        const uint32_t o = __shfl_up(n, d);
+        if (t >= d) n += o;
+      }
+      s.past[t] = n;
     }
     __syncthreads();
-    low = 0, high = -1, ordered = false;
-    if (n > kRowWaves * kWaveList) return;
-    uint32_t filled = 0;
-    walk<16 / Bits<T>::kVec>(lo, bin, [&](bool is, float l, int i) {
-      const uint64_t those = __ballot(is);
-      if (!those) return;
-      const uint32_t at = filled + __popcll(those & ((uint64_t(1) << lane) - 1));
-      if (is && at < kWaveList) s.list[wave][at] = key_of(l, i);
-      filled += __popcll(those);
+    listed = tokens <= kList;
+    ordered = tokens <= kFew;
+    if (!listed) return;
+    read([&](uint32_t i, uint64_t k) {
+      s.list[i] = k;
+      s.weights[i] = weight_of(k);
     });
-    if (lane == 0) {
-      s.listed[wave] = filled;
-      if (filled > kWaveList) s.over = 1;               // gone through again each time
-    }
     __syncthreads();
-    if (s.over) return;
-    low = lo, high = bin;
-    order();
+    if (ordered) order();
   }
-  // Put what is listed in order by counting, if it is few: the list also has tokens that top_k dropped from a chunk.
+  // Put the few tokens that are listed in order by counting.
   __device__ void order() {
-    const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
-    uint32_t from = 0, n = 0;
-#pragma unroll
-    for (int w = 0; w < kRowWaves; ++w) {
-      from += w < wave ? s.listed[w] : 0;
-      n += s.listed[w];
-    }
-    if (n > kFew) return;
-    for (uint32_t i = lane; i < s.listed[wave]; i += 64) {
-      const uint64_t k = s.list[wave][i];
-      s.few_key[from + i] = k;
-      s.few_sum[from + i] = weight_of(k);
-    }
-    __syncthreads();
-    tokens = n;
-    const uint32_t i = t >> 2;
-    key = i < n ? s.few_key[i] : 0;
-    weight = i < n ? s.few_sum[i] : 0;
+    const int t = threadIdx.x;
+    const uint32_t n = tokens, i = t >> 2;
+    key = i < n ? s.list[i] : 0;
+    weight = i < n ? s.weights[i] : 0;
     upto = 0, rank = 0;
-    if (i < ((n + 15) & ~15u)) {
+    if (i < n) {
+#pragma unroll 4
       for (uint32_t j = t & 3; j < n; j += 4)
-        if (s.few_key[j] >= key) upto += s.few_sum[j], ++rank;
+        if (s.list[j] >= key) upto += s.weights[j], ++rank;
 #pragma unroll
-      for (int m = 1; m < 4; m *= 2) upto += __shfl_xor(static_cast<unsigned long long>(upto), m), rank += __shfl_xor(rank, m);
+      for (int m = 1; m < 4; m *= 2)
+        upto += __shfl_xor(static_cast<unsigned long long>(upto), m), rank += __shfl_xor(rank, m);
+      if (rank == n) s.all = upto;
     }
-    if (i < n && rank == n) s.all = upto;
     __syncthreads();
-    ordered = true;
   }
-  // f(key) for the opened bin's tokens.
+  // f(key, weight) for the opened bin's tokens.
   template <class F>
   __device__ void each(int bin, F f) {
-    if (bin >= low && bin <= high) {
-      const int wave = threadIdx.x >> 6;
-      for (uint32_t i = threadIdx.x & 63; i < s.listed[wave]; i += 64) {
-        const uint64_t k = s.list[wave][i];
-        if (rule.bin(logit_of(uint32_t(k >> 32))) == bin) f(k);
+    if (listed) {
+      for (uint32_t i = threadIdx.x; i < tokens; i += kRowThreads) {
+        const uint64_t k = s.list[i];
+        if (rule.bin(logit_of(uint32_t(k >> 32))) == bin) f(k, s.weights[i]);
       }
     } else {
-      walk<1>(bin, bin, [&](bool is, float l, int i) {
-        if (is) f(key_of(l, i));
-      });
+      read([&](uint32_t, uint64_t k) { f(k, weight_of(k)); });       // the bin by itself
     }
   }
   // Sums over the block.
@@ -527,8 +504,8 @@ struct Choice {
     open(bin);
     uint64_t part = 0;
     uint32_t n = 0;
-    each(bin, [&](uint64_t k) {
-      if (uint32_t(k >> 32) >= border) part += weight_of(k), ++n;
+    each(bin, [&](uint64_t k, uint64_t w) {
+      if (uint32_t(k >> 32) >= border) part += w, ++n;
     });
     total(part, n);
     if (t == bin) {
@@ -570,7 +547,7 @@ struct Choice {
     else g.sum -= before;
     uint64_t lo = 0, hi = ~uint64_t(0), passed = 0, all = 0;
     uint32_t n = 0;
-    each(bin, [&](uint64_t k) { all += weight_of(k), ++n; });
+    each(bin, [&](uint64_t, uint64_t w) { all += w, ++n; });
     total(all, n);
     if (g.count) g.count = min(g.count, n);
     else if (all == 0) g.count = 1;
@@ -578,7 +555,7 @@ struct Choice {
     while (n > 64) {
       // The keys' range, then bins over it.
       uint64_t least = ~uint64_t(0), most = 0;
-      each(bin, [&](uint64_t k) {
+      each(bin, [&](uint64_t k, uint64_t) {
         if (k < lo || k > hi) return;
         least = k < least ? k : least;
         most = k > most ? k : most;
@@ -599,10 +576,10 @@ struct Choice {
         most = s.part_b[w] > most ? s.part_b[w] : most;
       }
       const int width = 64 - __builtin_clzll((most - least) | 1), shift = width > 9 ? width - 9 : 0;
-      each(bin, [&](uint64_t k) {
+      each(bin, [&](uint64_t k, uint64_t w) {
         if (k < lo || k > hi) return;
         const int b = int((most - k) >> shift);
-        atomicAdd(reinterpret_cast<unsigned long long*>(&s.sums[b]), static_cast<unsigned long long>(weight_of(k)));
+        atomicAdd(reinterpret_cast<unsigned long long*>(&s.sums[b]), static_cast<unsigned long long>(w));
         atomicAdd(&s.counts[b], 1u);
       });
       __syncthreads();
@@ -630,10 +607,10 @@ struct Choice {
     __syncthreads();
     if (t == 0) s.few = 0;
     __syncthreads();
-    each(bin, [&](uint64_t k) {
+    each(bin, [&](uint64_t k, uint64_t w) {
       if (k < lo || k > hi) return;
       const uint32_t at = atomicAdd(&s.few, 1u);
-      if (at < 64) s.few_key[at] = k, s.few_sum[at] = weight_of(k);
+      if (at < 64) s.few_key[at] = k, s.few_sum[at] = w;
     });
     __syncthreads();
     if (wave == 0) {
@@ -663,13 +640,6 @@ __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
   const float u = a.u[index];
   const size_t first_chunk = size_t(index) * a.chunks;
   const float chunk_top = a.tops[first_chunk + min(lane, a.chunks - 1)];
-  const int strips_n = a.chunks << (a.chunk_shift - 6);
-  float strips[kMaxStrips / kRowThreads];
-#pragma unroll
-  for (int i = 0; i < kMaxStrips / kRowThreads; ++i) {
-    const int at = t + i * kRowThreads;
-    strips[i] = at < strips_n ? a.strips[size_t(index) * strips_n + at] : 0.f;
-  }
   const float top = wave_max(chunk_top);
   if (top == -__builtin_inff()) {
     if (t == 0) {
@@ -695,7 +665,7 @@ __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
     const size_t from = (first_chunk + c) * kBins + max(at, 0);
     const bool here = at >= 0;
     const uint64_t sum = here ? a.sums[from] : 0;
-    mine += here ? a.counts[from] : 0;
+    mine += here ? a.counts[from] & 0xFFFFu : 0;
     const double f = s.factor[c];
     own += f == 1.0 ? sum : uint64_t(double(sum) * f);
   }
@@ -711,7 +681,7 @@ __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
   uint64_t kept = s.before;                             // the sum and the count of what is kept so far
   uint32_t left = s.count;
   const Row<T> row(a, index);
-  Choice<T> pick{s, a, rule, row, strips, own, sum, mine, count};
+  Choice<T> pick{s, a, rule, row, index, own, sum, mine, count};
   if (!rule.greedy && min_p > 0.0) {
     // The least logit with e >= min_p.
     const double least = fmin(min_p, 1.0);
@@ -751,7 +721,7 @@ __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
 // Chunks: small ones while they are few, for the blocks' number; large ones otherwise, for the bins' traffic.
 struct Chunks {
   bool large;
-  int vecs, count;
+  int vecs, count, tokens;
 };
 Chunks chunks_of(int64_t rows, int64_t vocab, int64_t type) {
   const int64_t vec = type == TQ2_TYPE_F32 ? 4 : 8, vecs = vocab / vec;
@@ -762,6 +732,7 @@ Chunks chunks_of(int64_t rows, int64_t vocab, int64_t type) {
   c.vecs = int(c.large ? large : small);
   c.count = int((vecs + c.vecs - 1) / c.vecs);
   if (c.count < 1) c.count = 1;
+  c.tokens = int(c.vecs * vec + 16);
   return c;
 }
 
@@ -782,7 +753,7 @@ hipError_t launch(const Args& a, bool large, int64_t rows, hipStream_t stream) {
 
 size_t sample_workspace(int64_t rows, int64_t vocab, int64_t type) {
   const Chunks c = chunks_of(rows, vocab, type);
-  return size_t(rows) * size_t(c.count) * (kBins * 12 + 4 + size_t(c.vecs / 64) * 4);
+  return size_t(rows) * size_t(c.count) * (kBins * 12 + size_t(c.tokens) * 2 + 4);
 }
 
 hipError_t launch_sample(const tq2_sample_args& q, hipStream_t stream) {
@@ -807,8 +778,9 @@ hipError_t launch_sample(const tq2_sample_args& q, hipStream_t stream) {
   const size_t parts = size_t(q.rows) * size_t(chunks.count);
   a.sums = static_cast<uint64_t*>(q.workspace);
   a.counts = reinterpret_cast<uint32_t*>(a.sums + parts * kBins);
-  a.tops = reinterpret_cast<float*>(a.counts + parts * kBins);
-  a.strips = a.tops + parts;
+  a.order = reinterpret_cast<uint16_t*>(a.counts + parts * kBins);
+  a.chunk_tokens = chunks.tokens;
+  a.tops = reinterpret_cast<float*>(a.order + parts * size_t(chunks.tokens));
   if (q.logits_type == TQ2_TYPE_F32) return launch<F32>(a, chunks.large, q.rows, stream);
   if (q.logits_type == TQ2_TYPE_F16) return launch<F16>(a, chunks.large, q.rows, stream);
   return launch<BF16>(a, chunks.large, q.rows, stream);
