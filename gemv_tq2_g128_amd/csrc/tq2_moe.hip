@@ -5,18 +5,20 @@
 // Bound.  Every touched expert's weights are read once against HBM (3 H I weights of 4.125 to 4.5 or 2.125 bits); a few
 // tokens meet each of them, so that everything else is kept off that stream.
 //
-// Matrix form, as in the 4-bit products: one v_mfma_f32_16x16x32_f16 takes 16 weight rows as its columns and up to
-// eight rows of x as hi and lo binary16 halves under a power of two per row and 128 columns; codes are decoded to exact
-// binary16 integers, a group's sum meets its scale in f32, then the power of two.
+// Whole numbers.  A row of x becomes 31-bit integers under a power of two per 128 columns, as four signed bytes each; the
+// codes are small integers as they lie in memory (a mask, or a shift and a mask, for four of them: a fifth of what their
+// binary16 values cost).  One v_mfma_i32_16x16x64_i8 takes 16 weight rows as its columns and four tokens' bytes as its
+// 16 rows; its sums are exact, start at minus the codes' middle times the sum of x, and a lane has one token's four bytes
+// of one weight row.  They become f32 once for each scale: bytes joined, times the scale, times the power of two.
 //
-// Work split.  Three launches: rows_kernel for gate and up (SwiGLU in its epilogue), rows_kernel for down, and the sum
-// of each token's weighted rows.  A block of rows_kernel has an expert and walks over column tiles of 16; its eight
-// waves are `wk` parts of K by 8 / wk tiles (gate and up tiles of the same columns side by side), whose partial sums meet
-// in LDS once a step.  The expert's rows of x lie in LDS, eight at a time; the next step's codes are in flight before the
-// present one is computed.
+// Work split.  rows_kernel for gate and up (SwiGLU in its epilogue), rows_kernel for down, and the sum of each token's
+// weighted rows; for few tokens down and the sum are one launch, token_kernel.  A block of rows_kernel has an expert, up to
+// eight of its tokens in LDS, and walks over column tiles of 16; its waves are parts of K by tiles (gate and up tiles of
+// the same columns side by side), whose partial sums meet in LDS once a step.  The next step's codes are in flight before
+// the present one is computed.
 //
-// Who has which expert is found by each block from ids itself (at most 2048 of them): with fewer pairs than experts a
-// block row stands for a pair and works if no earlier pair has its expert, otherwise it stands for an expert.
+// Who has which expert: up to 64 pairs are one load and a ballot in each wave; more are sorted by items_kernel into items
+// of an expert and up to eight of its pairs, so that experts of many tokens take more blocks instead of longer ones.
 #include "tq2_device.h"
 #include "tq2_internal.h"
 #include "tq2_moe_internal.h"
@@ -25,82 +27,59 @@
 namespace tq2 {
 namespace {
 
-typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
-typedef float float4_t __attribute__((ext_vector_type(4)));
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
+constexpr int kTokenWaves = 8;                  // of a block of token_kernel
+constexpr int kMaxRows = 8;                     // rows of x that a block has at a time, four to a matrix operand
 constexpr int kUnits = 4;                       // 64-byte pieces of a weight row that a wave has in flight
 constexpr int kLds = 160 * 1024;
 
-// A weight format: G, the columns of a scale; kBlocks, the 128-wide blocks of a row's 64 bytes.
+// A weight format: kGroup, the columns of a scale; kBlocks, the 128-wide blocks of a row's 64 bytes; kMiddle, the code
+// that stands for zero.
 struct Q4G32 {
-  static constexpr int kGroup = 32, kBlocks = 1;
+  static constexpr int kGroup = 32, kBlocks = 1, kMiddle = 8;
 };
 struct Q4G64 {
-  static constexpr int kGroup = 64, kBlocks = 1;
+  static constexpr int kGroup = 64, kBlocks = 1, kMiddle = 8;
 };
 struct Q4G128 {
-  static constexpr int kGroup = 128, kBlocks = 1;
+  static constexpr int kGroup = 128, kBlocks = 1, kMiddle = 8;
 };
 struct Ternary {
-  static constexpr int kGroup = 128, kBlocks = 2;
+  static constexpr int kGroup = 128, kBlocks = 2, kMiddle = 1;
 };
-
-// The masked bits of a word in binary16 mantissas.  Not in inline asm: the compiler keeps instructions that it knows, but
-// not asm, off the result registers of a matrix instruction in flight whose values nobody reads.
-__device__ __forceinline__ half2_t mantissas(uint32_t w, uint32_t mask) {
-  return __builtin_bit_cast(half2_t, (w & mask) | 0x64006400u);
-}
-
-// The 8 weights of one 4-bit word as exact binary16 values code - 8, in the order 0, 4, 1, 5, 2, 6, 3, 7: masks leave a
-// pair of nibbles 16 bits apart in the low mantissa bits of 1024 + c or of 1024 + 16 c.
-__device__ __forceinline__ half8_t decode_q4(uint32_t w) {
-  const half2_t one16 = {_Float16(0.0625f), _Float16(0.0625f)};
-  const half2_t off16 = {_Float16(-72.0f), _Float16(-72.0f)};
-  const half2_t off1 = {_Float16(-1032.0f), _Float16(-1032.0f)};
-  const uint32_t v = w >> 8;
-  const half2_t a = mantissas(w, 0x000F000Fu) + off1;
-  const half2_t b = mantissas(w, 0x00F000F0u) * one16 + off16;
-  const half2_t c = mantissas(v, 0x000F000Fu) + off1;
-  const half2_t d = mantissas(v, 0x00F000F0u) * one16 + off16;
-  return half8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
-// The lower 8 codes of each half-word of a ternary word (columns 0 .. 7 of its 16; of the word moved down by a byte,
-// columns 8 .. 15) as exact binary16 values code - 1.
-__device__ __forceinline__ half8_t decode_ternary(uint32_t w) {
-  const half2_t m1 = {_Float16(0.25f), _Float16(0.25f)};
-  const half2_t m2 = {_Float16(0.0625f), _Float16(0.0625f)};
-  const half2_t m3 = {_Float16(0.015625f), _Float16(0.015625f)};
-  const half2_t o0 = {_Float16(-1025.0f), _Float16(-1025.0f)};
-  const half2_t o1 = {_Float16(-257.0f), _Float16(-257.0f)};
-  const half2_t o2 = {_Float16(-65.0f), _Float16(-65.0f)};
-  const half2_t o3 = {_Float16(-17.0f), _Float16(-17.0f)};
-  const half2_t a = mantissas(w, 0x00030003u) + o0;
-  const half2_t b = mantissas(w, 0x000C000Cu) * m1 + o1;
-  const half2_t c = mantissas(w, 0x00300030u) * m2 + o2;
-  const half2_t d = mantissas(w, 0x00C000C0u) * m3 + o3;
-  return half8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
-// Where the eight columns 8 u .. 8 u + 7 of a 128-wide block stand in the matrix steps: step and lane group, which
-// follow from where a lane's 16 bytes of codes lie.
-//   groups of 128: a lane's word s is step s (columns 32 g + 8 s);
-//   groups of 32 and 64: after the transposition of words step s is columns 32 s + 8 g;
-//   ternary: after the swap of halves lane group g has words 4 (g & 1) + 2 (g >> 1) and the next one, two steps each.
 template <class F>
-__device__ __forceinline__ void place_of(int u, int* step, int* grp) {
+constexpr int kGroups = 128 / F::kGroup;        // scales of a block
+template <class F>
+constexpr int kSteps = F::kGroup == 32 ? 4 : 2; // matrix steps of a block, of 32 or 64 columns
+
+// Where eight columns of a 128-wide block stand in the matrix steps, which follows from where a lane's 16 bytes of codes
+// lie: step, lane group and half of the lane group's 16 bytes (steps of 32: all of its 8).  The eight are 8 u .. 8 u + 7,
+// for ternary weights 16 (u >> 1) + 4 (u & 1) and the next three, and the four that are eight further.
+//   groups of 128: a lane's words 2 s and 2 s + 1 are step s;
+//   groups of 64: after the swap of halves step s is group s, of which lane group g has half a lane's words;
+//   groups of 32: after the transposition of words step s is columns 32 s + 8 g;
+//   ternary: after the swap lane group g has words 4 (g & 1) + 2 (g >> 1) and the next one, a step each.
+template <class F>
+__device__ __forceinline__ void place_of(int u, int* step, int* grp, int* half) {
   if (F::kBlocks == 2) {
-    *step = u & 3;
-    *grp = u >> 3 | (u >> 1 & 2);
+    const int word = u >> 1;
+    *step = word & 1;
+    *grp = word >> 2 | (word & 2);
+    *half = u & 1;
   } else if (F::kGroup == 128) {
-    *step = u & 3;
+    *step = u >> 1 & 1;
     *grp = u >> 2;
+    *half = u & 1;
+  } else if (F::kGroup == 64) {
+    *step = u >> 3;
+    *grp = (u >> 2 & 1) | (u & 2);
+    *half = u & 1;
   } else {
     *step = u >> 2;
     *grp = u & 3;
+    *half = 0;
   }
 }
 
@@ -184,12 +163,12 @@ __device__ __forceinline__ float scale_of(const Codes<F>& c, int b, int s) {
 // Lane groups exchange words so that each step stays inside one scale's columns.
 template <class F>
 __device__ __forceinline__ void arrange(u32x4_t& w) {
-  if constexpr (F::kBlocks == 2) {
-    // Afterwards words 0 and 1 are of the unit's first block in all lanes, 2 and 3 of its second.
+  if constexpr (F::kBlocks == 2 || F::kGroup == 64) {
+    // Afterwards words 0 and 1 are of the first half of the lanes' columns, 2 and 3 of the second, in all lanes.
     auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
     auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
     w = u32x4_t{a[0], b[0], a[1], b[1]};
-  } else if constexpr (F::kGroup != 128) {
+  } else if constexpr (F::kGroup == 32) {
     // Lane group g holds in word s what lane group s held in word g.
     auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
     auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
@@ -199,109 +178,152 @@ __device__ __forceinline__ void arrange(u32x4_t& w) {
   }
 }
 
-// How rows of x fill the matrix operands.
-enum Mode {
-  kPacked,                                      // 8 rows as hi, and their lo as 8 more
-  kHigh,                                        // 16 rows as hi: 16-bit values need no lo
-  kBoth                                         // 16 rows as hi, and lo as an operand of its own
+// x of up to kMaxRows rows in LDS:
+//   operands  [block][step][lane group][columns_of(m)] of 16 bytes (steps of 32: 8), column 4 row + byte
+//   starts    [block][group][row] of 4 integers: minus kMiddle times the sums of the row's bytes
+//   backs     [block][row]: the power of two that undoes the row's
+// An odd number of columns keeps the lanes that write a stretch of x off each other's banks.
+__host__ __device__ inline int columns_of(int m) { return m > 1 ? 4 * m + 1 : 4; }
+template <class F>
+__host__ __device__ inline int operand_bytes(int blocks, int m) { return (blocks * 128 * columns_of(m) + 15) & ~15; }
+template <class F>
+__host__ __device__ inline int start_bytes(int blocks, int m) { return blocks * kGroups<F> * m * 16; }
+template <class F>
+__host__ __device__ inline int x_bytes(int blocks, int m) {
+  return operand_bytes<F>(blocks, m) + start_bytes<F>(blocks, m) + (blocks * m * 4 + 15) / 16 * 16;
+}
+struct Rows31 {
+  char* operands;
+  i32x4_t* starts;
+  float* backs;
 };
-template <Mode M>
-constexpr int kRowsOf = M == kPacked ? 8 : 16;
-
-// Operand words from one lane group's columns to the next's; an odd number keeps the lanes that write a stretch of x
-// off each other's banks.
-template <Mode M>
-__host__ __device__ inline int columns_of(int m) {
-  const int n = M == kHigh ? m : 2 * m;
-  return m > 4 ? n | 1 : n;
-}
-// Bytes of LDS for m rows of `blocks` 128-wide blocks (operands and powers of two), and for partial sums.
-template <Mode M>
-__host__ __device__ inline int x_bytes(int blocks, int m) { return blocks * (256 * columns_of<M>(m) + 64); }
-template <Mode M>
-constexpr int kRedBytes = 2 * kWaves * kRowsOf<M> * 16 * 4;
-
-// The column of the matrix operand x that the lane's row reads.
-template <Mode M>
-__device__ __forceinline__ int operand_column(int r16, int m) {
-  if (M == kPacked) return (r16 & 7) < m ? (r16 >> 3) * m + (r16 & 7) : 0;
-  return r16 < m ? r16 : 0;
+template <class F>
+__device__ __forceinline__ Rows31 rows_in(unsigned char* smem, int blocks, int m) {
+  Rows31 r;
+  r.operands = reinterpret_cast<char*>(smem);
+  r.starts = reinterpret_cast<i32x4_t*>(smem + operand_bytes<F>(blocks, m));
+  r.backs = reinterpret_cast<float*>(smem + operand_bytes<F>(blocks, m) + start_bytes<F>(blocks, m));
+  return r;
 }
 
-// Block b of unit j (b < F::kBlocks): four matrix steps against x, scaled into acc (rows 4 g4 + r of x, weight row r16).
-template <class F, Mode M>
-__device__ __forceinline__ void multiply(const Codes<F>& c, int j, int b, const half8_t* __restrict__ a,
-                                         const float4_t& back, int cols, int m, float (&acc)[4]) {
-  float4_t sum;
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const half8_t a0 = a[size_t(s) * 4 * cols];
-    half8_t w;
-    if constexpr (F::kBlocks == 2) {
-      const uint32_t word = c.w[j][2 * b + (s >> 1)];
-      w = decode_ternary(s & 1 ? word >> 8 : word);
-    } else {
-      w = decode_q4(c.w[j][s]);
-    }
-    const bool fresh = s % (F::kGroup / 32) == 0;
-    const bool whole = (s + 1) % (F::kGroup / 32) == 0;
-    sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, w, fresh ? float4_t{0.f, 0.f, 0.f, 0.f} : sum, 0, 0, 0);
-    if constexpr (M == kBoth)
-      sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[size_t(s) * 4 * cols + m], w, sum, 0, 0, 0);
-    if (whole) {
-      const float d = scale_of<F>(c, j * F::kBlocks + b, s);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(d * sum[r], back[r], acc[r]);
-    }
-  }
+// One DPP lane move of an integer.
+template <int CTRL>
+__device__ __forceinline__ int move(int v) { return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false); }
+
+// Four words of bytes 0 .. 3 to four words of one byte each.
+__device__ __forceinline__ u32x4_t by_byte(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const uint32_t ab01 = __builtin_amdgcn_perm(b, a, 0x05010400u), ab23 = __builtin_amdgcn_perm(b, a, 0x07030602u);
+  const uint32_t cd01 = __builtin_amdgcn_perm(d, c, 0x05010400u), cd23 = __builtin_amdgcn_perm(d, c, 0x07030602u);
+  return u32x4_t{__builtin_amdgcn_perm(cd01, ab01, 0x05040100u), __builtin_amdgcn_perm(cd01, ab01, 0x07060302u),
+                 __builtin_amdgcn_perm(cd23, ab23, 0x05040100u), __builtin_amdgcn_perm(cd23, ab23, 0x07060302u)};
 }
 
-// Largest |x| over aligned groups of 16 lanes, in every lane.
-__device__ __forceinline__ float row16_max(float v) {
-  v = fmaxf(v, dpp_move<0xB1, 0xF>(v));
-  v = fmaxf(v, dpp_move<0x4E, 0xF>(v));
-  v = fmaxf(v, dpp_move<0x141, 0xF>(v));
-  v = fmaxf(v, dpp_move<0x140, 0xF>(v));
-  return v;
-}
-
-// Convert eight columns (the u-th eight of 128-wide block kb) of row `row` of m into LDS.  The sixteen lanes of a block
-// call together: their power of two is a DPP maximum, 2^13 <= |x| 2^e < 2^14.  `share` multiplies the row.
-template <class F, Mode M, class X>
-__device__ __forceinline__ void stage8(const typename X::elem* __restrict__ src, int u, int kb, int row, int m, int cols,
-                                       float share, half8_t* __restrict__ xf, float* __restrict__ xs) {
-  const f32x4_t p = load4(X(), src), q = load4(X(), src + 4);
-  float v[8];
+// Convert eight columns (the u-th eight, as place_of says) of 128-wide block kb of row `row` of m into LDS.  The sixteen
+// lanes of a block call together: their power of two is a DPP maximum, 2^29 <= |x| 2^e < 2^30.  `share` multiplies the row.
+template <class F, class X>
+__device__ __forceinline__ void stage8(const typename X::elem* __restrict__ block, int u, int kb, int row, int m,
+                                       int cols, float share, const Rows31& r) {
+  const typename X::elem* src = block + (F::kBlocks == 2 ? (u >> 1) * 16 + (u & 1) * 4 : u * 8);
+  const f32x4_t p = load4(X(), src), q = load4(X(), src + (F::kBlocks == 2 ? 8 : 4));
+  const float v[8] = {p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
+  int top = 0;                                           // bits of the largest |x|: NaN above infinity
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[F::kBlocks == 2 ? j : 2 * j] = p[j];                     // the order of the decoded codes
-    v[F::kBlocks == 2 ? j + 4 : 2 * j + 1] = q[j];
-  }
-  float top = 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
-  top = row16_max(top);
-  const int e = int((__builtin_bit_cast(uint32_t, top) >> 23) & 255) - 127;
-  const int up = top > 0.f ? min(13 - e, 126) : 0;
+  for (int j = 0; j < 8; ++j) top = max(top, __builtin_bit_cast(int, v[j]) & 0x7FFFFFFF);
+  top = max(top, move<0xB1>(top));
+  top = max(top, move<0x4E>(top));
+  top = max(top, move<0x141>(top));
+  top = max(top, move<0x140>(top));
+  const int up = top > 0 ? min(29 + 127 - (top >> 23), 126) : 0;
   const float s = __builtin_ldexpf(1.0f, up);
-  half8_t hi, lo;
+  uint32_t b[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float t = v[j] * s;
-    hi[j] = _Float16(t);
-    lo[j] = _Float16(t - float(hi[j]));
+  for (int j = 0; j < 8; ++j) b[j] = (uint32_t(int(__builtin_rintf(v[j] * s))) + 0x00808080u) ^ 0x00808080u;   // signed bytes
+  // The order of the codes' bytes: nibbles of a word, or 2-bit fields of bytes.
+  const u32x4_t first = F::kBlocks == 2 ? by_byte(b[0], b[4], b[1], b[5]) : by_byte(b[0], b[2], b[4], b[6]);
+  const u32x4_t second = F::kBlocks == 2 ? by_byte(b[2], b[6], b[3], b[7]) : by_byte(b[1], b[3], b[5], b[7]);
+  int step, grp, half;
+  place_of<F>(u, &step, &grp, &half);
+  constexpr int kWide = F::kGroup == 32 ? 8 : 16;
+  char* dst = r.operands + (size_t(kb * kSteps<F> + step) * 4 + grp) * cols * kWide + half * 8;
+  i32x4_t sum;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    *reinterpret_cast<u32x2_t*>(dst + (row * 4 + i) * kWide) = u32x2_t{first[i], second[i]};
+    int n = __builtin_amdgcn_sdot4(int(first[i]), 0x01010101, 0, false);
+    n = __builtin_amdgcn_sdot4(int(second[i]), 0x01010101, n, false);
+    n += move<0xB1>(n);
+    n += move<0x4E>(n);                                  // four lanes: 32 columns
+    if (F::kGroup >= 64) n += move<0x141>(n);            // eight
+    if (F::kGroup == 128) n += move<0x140>(n);
+    sum[i] = -F::kMiddle * n;
   }
-  int step, grp;
-  place_of<F>(u, &step, &grp);
-  half8_t* dst = xf + (size_t(kb * 4 + step) * 4 + grp) * cols + row;
-  dst[0] = hi;
-  if (M != kHigh) dst[m] = lo;
-  if (u == 0) {
-    const float back = __builtin_ldexpf(1.0f, -up) * share;
-    xs[kb * 16 + row] = back;
-    if (M == kPacked) xs[kb * 16 + 8 + row] = back;
+  constexpr int kLanes = F::kGroup / 8;
+  if (u % kLanes == 0) r.starts[(kb * kGroups<F> + u / kLanes) * m + row] = sum;
+  if (u == 0)
+    r.backs[kb * m + row] = top >= 0x7F800000 ? __builtin_nanf("") : __builtin_ldexpf(1.0f, -up) * share;
+}
+
+// Block b of unit j (b < F::kBlocks) of the lane's weight row r16 against SETS times four rows of x: lane group g4 adds
+// row 4 set + g4's product to acc[set].  at: the lane's operand column of the first set; from, back: the lane group's row.
+template <class F, int SETS>
+__device__ __forceinline__ void multiply(const Codes<F>& c, int j, int b, int kb, const Rows31& x, int g4, int cols,
+                                         const int (&at)[SETS], const int (&row)[SETS], int m, float (&acc)[SETS]) {
+  constexpr int kWide = F::kGroup == 32 ? 8 : 16;
+  float back[SETS];
+#pragma unroll
+  for (int q = 0; q < SETS; ++q) back[q] = x.backs[kb * m + row[q]];
+#pragma unroll
+  for (int g = 0; g < kGroups<F>; ++g) {
+    i32x4_t sum[SETS];
+#pragma unroll
+    for (int q = 0; q < SETS; ++q) sum[q] = x.starts[(kb * kGroups<F> + g) * m + row[q]];
+#pragma unroll
+    for (int s = g * kSteps<F> / kGroups<F>; s < (g + 1) * kSteps<F> / kGroups<F>; ++s) {
+      const char* operand = x.operands + (size_t(kb * kSteps<F> + s) * 4 + g4) * cols * kWide;
+      if constexpr (F::kGroup == 32) {
+        const uint32_t w = c.w[j][s];
+        const u32x2_t codes = {w & 0x0F0F0F0Fu, w >> 4 & 0x0F0F0F0Fu};
+#pragma unroll
+        for (int q = 0; q < SETS; ++q)
+          sum[q] = __builtin_amdgcn_mfma_i32_16x16x32_i8(*reinterpret_cast<const long*>(operand + at[q] * kWide),
+                                                         __builtin_bit_cast(long, codes), sum[q], 0, 0, 0);
+      } else {
+        u32x4_t codes;
+        if constexpr (F::kBlocks == 2) {
+          const uint32_t w = c.w[j][2 * b + s];
+          codes = u32x4_t{w & 0x03030303u, w >> 2 & 0x03030303u, w >> 4 & 0x03030303u, w >> 6 & 0x03030303u};
+        } else {
+          const uint32_t w = c.w[j][2 * s], v = c.w[j][2 * s + 1];
+          codes = u32x4_t{w & 0x0F0F0F0Fu, w >> 4 & 0x0F0F0F0Fu, v & 0x0F0F0F0Fu, v >> 4 & 0x0F0F0F0Fu};
+        }
+#pragma unroll
+        for (int q = 0; q < SETS; ++q)
+          sum[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(*reinterpret_cast<const i32x4_t*>(operand + at[q] * kWide),
+                                                         __builtin_bit_cast(i32x4_t, codes), sum[q], 0, 0, 0);
+      }
+    }
+    const float d = scale_of<F>(c, j * F::kBlocks + b, g * (F::kGroup / 32));
+#pragma unroll
+    for (int q = 0; q < SETS; ++q) {
+      // Bytes of the integers, the lowest first; f32 holds each sum (below 2^18) and rounds the joined ones.
+      float v = __builtin_fmaf(float(sum[q][3]), 256.f, float(sum[q][2]));
+      v = __builtin_fmaf(v, 256.f, float(sum[q][1]));
+      v = __builtin_fmaf(v, 256.f, float(sum[q][0]));
+      acc[q] = __builtin_fmaf(d * v, back[q], acc[q]);
+    }
   }
 }
+
+// An expert and up to kMaxRows of its pairs, order[first .. first + count).
+struct Item {
+  int expert, first, count;
+};
+// What items_kernel leaves in the workspace.
+struct Items {
+  int* count;
+  Item* item;
+  uint16_t* order;
+};
 
 // One launch of rows_kernel; all of it follows from the sizes.
 struct Shape {
@@ -315,80 +337,104 @@ struct Shape {
   int wk_shift;              // log2 of the parts of K
   int part_units, rounds, per;         // units of a part, its rounds, units of a round
   int steps;                 // of column tiles that the block's waves take together
-  bool by_pair;
+  bool few, by_pair;         // no items: a block row for each pair, or for each expert
 };
+
+// Pairs sorted by their expert, and experts cut into items of `rows` pairs.  The order of an expert's pairs is left to the
+// atomics: a pair's row is computed from itself alone, in whichever item it is.
+constexpr int kItemThreads = 1024;
+__global__ __launch_bounds__(kItemThreads) void items_kernel(const int32_t* __restrict__ ids, int pairs, int experts,
+                                                             int rows, Items out) {
+  __shared__ uint32_t next[TQ2_MOE_MAX_EXPERTS];
+  __shared__ uint32_t part[2][kItemThreads / 64];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  constexpr int kMine = TQ2_MOE_MAX_TOKENS * TQ2_MOE_MAX_TOP_K / kItemThreads;
+  int id[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) id[i] = t + i * kItemThreads < pairs ? ids[t + i * kItemThreads] : -1;
+  next[t] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kMine; ++i)
+    if (uint32_t(id[i]) < uint32_t(experts)) atomicAdd(&next[id[i]], 1u);
+  __syncthreads();
+  // Thread t's expert: where its pairs and its items start.
+  const uint32_t n = next[t], cut = (n + rows - 1) / rows;
+  uint32_t pair = n, item = cut;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint32_t a = __shfl_up(pair, d), b = __shfl_up(item, d);
+    if (lane >= d) pair += a, item += b;
+  }
+  if (lane == 63) part[0][wave] = pair, part[1][wave] = item;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kItemThreads / 64; ++w)
+    if (w < wave) pair += part[0][w], item += part[1][w];
+  next[t] = pair - n;
+  if (t == kItemThreads - 1) *out.count = int(item);
+  for (uint32_t i = 0; i < cut; ++i)
+    out.item[item - cut + i] = Item{t, int(pair - n + i * rows), int(min(n - i * rows, uint32_t(rows)))};
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kMine; ++i)
+    if (uint32_t(id[i]) < uint32_t(experts)) out.order[atomicAdd(&next[id[i]], 1u)] = uint16_t(t + i * kItemThreads);
+}
 
 // GATE: x are the tokens' rows, out the rows between the projections, f32 [pairs, 16 tiles].  Otherwise x are those
 // and out the weighted rows, f32 [pairs, 16 tiles].
-template <class F, class X, bool GATE, Mode M>
-__global__ __launch_bounds__(kThreads, 2) void rows_kernel(Weight weight, const typename X::elem* __restrict__ x,
-                                                           const int32_t* __restrict__ ids,
-                                                           const float* __restrict__ share, float* __restrict__ out,
-                                                           Shape sh) {
+template <class F, class X, bool GATE, int WAVES, int SETS>
+__global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, const typename X::elem* __restrict__ x,
+                                                             const int32_t* __restrict__ ids, Items items,
+                                                             const float* __restrict__ share, float* __restrict__ out,
+                                                             Shape sh) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  constexpr int kRows = kRowsOf<M>;
-  half8_t* xf = reinterpret_cast<half8_t*>(smem);
-  float* xs = reinterpret_cast<float*>(smem + sh.blocks * 256 * columns_of<M>(sh.rows));
-  float* red = reinterpret_cast<float*>(smem + x_bytes<M>(sh.blocks, sh.rows));
-  int* counts = reinterpret_cast<int*>(smem + x_bytes<M>(sh.blocks, sh.rows) + kRedBytes<M>);
-  uint16_t* list = reinterpret_cast<uint16_t*>(counts + kWaves);
+  constexpr int kThreads = 64 * WAVES, kRows = 4 * SETS;
+  float* red = reinterpret_cast<float*>(smem + x_bytes<F>(sh.blocks, sh.rows));
+  uint16_t* list = reinterpret_cast<uint16_t*>(red + 2 * WAVES * kRows * 16);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
-  const bool few = sh.pairs <= 64;                       // ids of all pairs in one load
-  const int id = few && lane < sh.pairs ? ids[lane] : -1;
-  const int e = !sh.by_pair ? int(blockIdx.y)
-                : few       ? __builtin_amdgcn_readlane(id, blockIdx.y)
-                            : __builtin_amdgcn_readfirstlane(ids[blockIdx.y]);
-  if (uint32_t(e) >= uint32_t(sh.experts)) return;
-  const uint64_t mask = __ballot(id == e);
-  if (few && (mask == 0 || (sh.by_pair && __builtin_ctzll(mask) != int(blockIdx.y)))) return;
+  int e, found;
+  if (sh.few) {
+    // The ids of all pairs, at most 64, are one load; every wave lists the expert's pairs for itself.
+    const int id = lane < sh.pairs ? ids[lane] : -1;
+    e = sh.by_pair ? __builtin_amdgcn_readlane(id, blockIdx.y) : int(blockIdx.y);
+    if (uint32_t(e) >= uint32_t(sh.experts)) return;
+    const uint64_t mask = __ballot(id == e);
+    if (mask == 0 || (sh.by_pair && __builtin_ctzll(mask) != int(blockIdx.y))) return;
+    found = __popcll(mask);
+    if (id == e) list[__popcll(mask & ((uint64_t(1) << lane) - 1))] = uint16_t(lane);
+  } else {
+    if (int(blockIdx.y) >= *items.count) return;
+    const Item item = items.item[blockIdx.y];
+    e = __builtin_amdgcn_readfirstlane(item.expert);
+    found = __builtin_amdgcn_readfirstlane(item.count);
+    if (lane < found) list[lane] = items.order[item.first + lane];
+  }
+  __builtin_amdgcn_wave_barrier();
 
   // The wave's part: a tile of each step, and units of K.
   const int slot = wave >> sh.wk_shift, part = wave & ((1 << sh.wk_shift) - 1);
   const int unit0 = part * sh.part_units, mine = min(sh.part_units, sh.units - unit0);
-  const int per_step = (kWaves >> sh.wk_shift) >> (GATE ? 1 : 0);
+  const int per_step = (WAVES >> sh.wk_shift) >> (GATE ? 1 : 0);
   const int64_t width = int64_t(sh.tiles) * 16;
   const int64_t expert_row = int64_t(e) * width * (GATE ? 2 : 1);
   const uint32_t code_off = r16 * weight.row_bytes + g4 * 16, scale_off = r16 * weight.row_scales * 2;
 
   Codes<F> c[2];
   auto load = [&](int step, int round, Codes<F>& into) {
-    const bool there = step < sh.steps;
-    const int64_t tile = int64_t(there ? step : 0) * per_step + (GATE ? slot >> 1 : slot);
-    const int64_t row0 = expert_row + (GATE && (slot & 1) ? width : 0) + tile * 16;
+    const int tile = step * per_step + (GATE ? slot >> 1 : slot);
+    const bool there = step < sh.steps && tile < sh.tiles;
+    const int64_t row0 = expert_row + (GATE && (slot & 1) ? width : 0) + (there ? tile * 16 : 0);
     load_codes<F>(rows_at(weight, row0), weight.row_bytes, code_off, scale_off, uint32_t(unit0 + round * sh.per),
                   there ? min(sh.per, mine - round * sh.per) : 0, g4 * 16, into);
   };
   int step = blockIdx.x, round = 0;
-  load(step, 0, c[0]);                                   // in flight while the rows are found and converted
-
-  // The pairs of this expert, in order.
-  int found = 0;
-  if (few) {
-    found = __popcll(mask);
-    if (id == e) list[__popcll(mask & ((uint64_t(1) << lane) - 1))] = uint16_t(lane);    // by every wave, for itself
-    __builtin_amdgcn_wave_barrier();
-  } else {
-    for (int p0 = 0; p0 < sh.pairs; p0 += kThreads) {
-      const int p = p0 + threadIdx.x;
-      const bool here = p < sh.pairs && ids[p] == e;
-      const uint64_t all = __ballot(here);
-      if (lane == 0) counts[wave] = __popcll(all);
-      __syncthreads();
-      int at = found;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        at += w < wave ? counts[w] : 0;
-        found += counts[w];
-      }
-      if (here) list[at + __popcll(all & ((uint64_t(1) << lane) - 1))] = uint16_t(p);
-      __syncthreads();
-    }
-    if (found == 0 || (sh.by_pair && list[0] != blockIdx.y)) return;
-  }
+  load(step, 0, c[0]);                                   // in flight while x is converted
 
   for (int first = 0; first < found; first += sh.rows) {
-    const int m = min(sh.rows, found - first), cols = columns_of<M>(m);
+    const int m = min(sh.rows, found - first), cols = columns_of(m);
+    const Rows31 rows = rows_in<F>(smem, sh.blocks, m);
     if (first > 0) {
       step = blockIdx.x;
       round = 0;
@@ -398,11 +444,17 @@ __global__ __launch_bounds__(kThreads, 2) void rows_kernel(Weight weight, const 
     for (int i = threadIdx.x; i < m * sh.blocks * 16; i += kThreads) {
       const int row = int((uint32_t(i >> 4) * sh.blocks_inverse) >> 20), kb = (i >> 4) - row * sh.blocks;
       const uint32_t pair = list[first + row], from = GATE ? pair * sh.top_k_inverse >> 16 : pair;
-      stage8<F, M, X>(x + (int64_t(from) * sh.blocks + kb) * 128 + (i & 15) * 8, i & 15, kb, row, m, cols, 1.f, xf, xs);
+      stage8<F, X>(x + (int64_t(from) * sh.blocks + kb) * 128, i & 15, kb, row, m, cols, 1.f, rows);
     }
     __syncthreads();
-    const int col = operand_column<M>(r16, m);
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    // The lane's operand columns and its group's rows; past the last row they repeat the first one's.
+    int at[SETS], own[SETS];
+#pragma unroll
+    for (int q = 0; q < SETS; ++q) {
+      at[q] = q * 4 + (r16 >> 2) < m ? q * 16 + r16 : r16 & 3;
+      own[q] = q * 4 + g4 < m ? q * 4 + g4 : 0;
+    }
+    float acc[SETS] = {};
     int parity = 0;
     auto compute = [&](Codes<F>& from) {
 #pragma unroll
@@ -414,33 +466,30 @@ __global__ __launch_bounds__(kThreads, 2) void rows_kernel(Weight weight, const 
         for (int b = 0; b < F::kBlocks; ++b) {
           const int kb = unit * F::kBlocks + b;
           if (F::kBlocks > 1 && kb >= sh.blocks) continue;
-          multiply<F, M>(from, j, b, xf + (size_t(kb) * 16 + g4) * cols + col,
-                         *reinterpret_cast<const float4_t*>(xs + kb * 16 + g4 * 4), cols, m, acc);
+          multiply<F, SETS>(from, j, b, kb, rows, g4, cols, at, own, m, acc);
         }
       }
     };
     // Partial sums [wave][row of x][weight row] of a step meet; a buffer is written again two steps on, behind the
     // next step's barrier.
     auto finish = [&]() {
-      float* buf = red + parity * (kWaves * kRows * 16);
+      float* buf = red + parity * (WAVES * kRows * 16);
       parity ^= 1;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float v = acc[r];
-        if (M == kPacked) v += __shfl_xor(v, 32);                     // hi + lo
-        acc[r] = 0.f;
-        if (M != kPacked || g4 < 2) buf[(wave * kRows + g4 * 4 + r) * 16 + r16] = v;
+      for (int q = 0; q < SETS; ++q) {
+        buf[(wave * kRows + q * 4 + g4) * 16 + r16] = acc[q];
+        acc[q] = 0.f;
       }
       __syncthreads();
       for (int i = threadIdx.x; i < per_step * kRows * 16; i += kThreads) {
         const int n = i & 15, row = i >> 4 & (kRows - 1), tile = i / (16 * kRows);
-        if (row >= m) continue;
+        if (row >= m || step * per_step + tile >= sh.tiles) continue;
         const int p = list[first + row];
-        const float* at = buf + row * 16 + n;
+        const float* from = buf + row * 16 + n;
         float a = 0.f, b = 0.f;
         for (int w = 0; w < 1 << sh.wk_shift; ++w) {
-          a += at[(((GATE ? 2 * tile : tile) << sh.wk_shift) + w) * (kRows * 16)];
-          if (GATE) b += at[(((2 * tile + 1) << sh.wk_shift) + w) * (kRows * 16)];
+          a += from[(((GATE ? 2 * tile : tile) << sh.wk_shift) + w) * (kRows * 16)];
+          if (GATE) b += from[(((2 * tile + 1) << sh.wk_shift) + w) * (kRows * 16)];
         }
         const float v = GATE ? a / (1.f + expf(-a)) * b : a * share[p];
         out[p * width + (int64_t(step) * per_step + tile) * 16 + n] = v;
@@ -467,87 +516,80 @@ __global__ __launch_bounds__(kThreads, 2) void rows_kernel(Weight weight, const 
 // waves take rounds of units over all of the token's places in turn, and their sums meet in LDS.  An expert that several
 // tokens chose is read for each of them.
 template <class F, class X>
-__global__ __launch_bounds__(kThreads, 2) void token_kernel(Weight weight, const float* __restrict__ h,
-                                                            const int32_t* __restrict__ ids,
-                                                            const float* __restrict__ share,
-                                                            const typename X::elem* residual, typename X::elem* out,
-                                                            Shape sh) {
+__global__ __launch_bounds__(64 * kTokenWaves, 2) void token_kernel(Weight weight, const float* __restrict__ h,
+                                                                    const int32_t* __restrict__ ids,
+                                                                    const float* __restrict__ share,
+                                                                    const typename X::elem* residual,
+                                                                    typename X::elem* out, Shape sh) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  __shared__ float red[kWaves][16];
+  __shared__ float red[kTokenWaves][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4, t = blockIdx.y;
-  constexpr int kCols = 2;
-  const int all_blocks = sh.top_k * sh.blocks;
-  half8_t* xf = reinterpret_cast<half8_t*>(smem);
-  float* xs = reinterpret_cast<float*>(smem + all_blocks * 256 * kCols);
+  const int all_blocks = sh.top_k * sh.blocks, cols = columns_of(1);
+  const Rows31 rows = rows_in<F>(smem, all_blocks, 1);
   const int id = lane < sh.top_k ? ids[t * sh.top_k + lane] : -1;
   const float part = lane < sh.top_k ? share[t * sh.top_k + lane] : 0.f;
   const uint32_t code_off = r16 * weight.row_bytes + g4 * 16, scale_off = r16 * weight.row_scales * 2;
   const int64_t hidden = int64_t(sh.tiles) * 16;
 
-  // Round r is part r % rounds of place r / rounds; the wave has rounds wave, wave + kWaves, ...
+  // Round r is part r % rounds of place r / rounds; the wave has rounds wave, wave + kTokenWaves, ...
   const int all_rounds = sh.top_k * sh.rounds;
   Codes<F> c[2];
   int place = 0, round = wave;                           // of the round that is loaded next
-  auto settle = [&]() {
-    while (round >= sh.rounds && place < sh.top_k) round -= sh.rounds, ++place;
-  };
   struct At {
     int place, unit, count;
   };
   auto load = [&](Codes<F>& into) {
-    settle();
+    while (round >= sh.rounds && place < sh.top_k) round -= sh.rounds, ++place;
     const bool there = place < sh.top_k;
     const int e = __builtin_amdgcn_readlane(id, there ? place : 0);
     const bool real = there && uint32_t(e) < uint32_t(sh.experts);
     const At at = {place, round * sh.per, real ? min(sh.per, sh.units - round * sh.per) : 0};
     load_codes<F>(rows_at(weight, (real ? int64_t(e) * hidden : 0) + int64_t(blockIdx.x) * 16), weight.row_bytes,
                   code_off, scale_off, uint32_t(at.unit), at.count, g4 * 16, into);
-    round += kWaves;
+    round += kTokenWaves;
     return at;
   };
   At now = load(c[0]);
-  for (int i = threadIdx.x; i < all_blocks * 16; i += kThreads) {
+  for (int i = threadIdx.x; i < all_blocks * 16; i += 64 * kTokenWaves) {
     const int kb = i >> 4, j = int((uint32_t(kb) * sh.blocks_inverse) >> 20);
-    stage8<F, kPacked, F32>(h + (int64_t(t) * all_blocks + kb) * 128 + (i & 15) * 8, i & 15, kb, 0, 1, kCols,
-                            __shfl(part, j), xf, xs);
+    // The first lanes are among those that are here: the lanes end in front of one that is not.
+    stage8<F, F32>(h + (int64_t(t) * all_blocks + kb) * 128, i & 15, kb, 0, 1, cols, __shfl(part, j), rows);
   }
   __syncthreads();
-  const int col = operand_column<kPacked>(r16, 1);
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  auto compute = [&](Codes<F>& from, const At& at) {
+  const int at[1] = {r16 & 3}, own[1] = {0};
+  float acc[1] = {0.f};
+  auto compute = [&](Codes<F>& from, const At& a) {
 #pragma unroll
     for (int j = 0; j < kUnits; ++j) {
-      if (j >= at.count) continue;
+      if (j >= a.count) continue;
       arrange<F>(from.w[j]);
 #pragma unroll
       for (int b = 0; b < F::kBlocks; ++b) {
-        const int k = (at.unit + j) * F::kBlocks + b, kb = at.place * sh.blocks + k;
+        const int k = (a.unit + j) * F::kBlocks + b;
         if (F::kBlocks > 1 && k >= sh.blocks) continue;
-        multiply<F, kPacked>(from, j, b, xf + (size_t(kb) * 16 + g4) * kCols + col,
-                             *reinterpret_cast<const float4_t*>(xs + kb * 16 + g4 * 4), kCols, 1, acc);
+        multiply<F, 1>(from, j, b, a.place * sh.blocks + k, rows, g4, cols, at, own, 1, acc);
       }
     }
   };
   for (int done = wave; done < all_rounds;) {
     const At then = load(c[1]);
     compute(c[0], now);
-    done += kWaves;
+    done += kTokenWaves;
     if (done >= all_rounds) break;
     now = load(c[0]);
     compute(c[1], then);
-    done += kWaves;
+    done += kTokenWaves;
   }
-  const float v = acc[0] + __shfl_xor(acc[0], 32);       // row 0: hi of lane group 0, lo of lane group 2
-  if (g4 == 0) red[wave][r16] = v;
+  if (g4 == 0) red[wave][r16] = acc[0];
   __syncthreads();
   if (threadIdx.x < 16) {
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) sum += red[w][threadIdx.x];
-    const int64_t at = int64_t(t) * hidden + int64_t(blockIdx.x) * 16 + threadIdx.x;
-    if (residual) sum += float(residual[at]);
-    out[at] = typename X::elem(sum);
+    for (int w = 0; w < kTokenWaves; ++w) sum += red[w][threadIdx.x];
+    const int64_t to = int64_t(t) * hidden + int64_t(blockIdx.x) * 16 + threadIdx.x;
+    if (residual) sum += float(residual[to]);
+    out[to] = typename X::elem(sum);
   }
 }
 
@@ -567,14 +609,28 @@ __global__ __launch_bounds__(256) void sum_kernel(const float* __restrict__ y, c
   store4(X(), out + size_t(t) * hidden + n, sum);
 }
 
-// The launch for n columns and k of K over `most` parts of it.
+// Rows of x at a time for both projections: no more than an expert can have, as many as LDS holds.
 template <class F>
-Shape shape_of(const tq2_moe_experts_args& a, int64_t n, int64_t k, int most, bool gate) {
+int lds_bytes(int blocks, int rows, int waves) {
+  return x_bytes<F>(blocks, rows) + 2 * waves * (rows > 4 ? 8 : 4) * 64 + 128;
+}
+template <class F>
+int rows_at_once(const tq2_moe_experts_args& a) {
+  const int blocks = int((a.hidden > a.inter ? a.hidden : a.inter) / 128), pairs = int(a.tokens * a.top_k);
+  int rows = pairs < kMaxRows ? pairs : kMaxRows;
+  while (lds_bytes<F>(blocks, rows, 16) > kLds) --rows;
+  return rows;
+}
+
+// The launch for n columns and k of K, with at most `most` parts of it.
+template <class F>
+Shape shape_of(const tq2_moe_experts_args& a, int64_t n, int64_t k, int waves, int most, bool gate) {
   Shape s;
   s.pairs = int(a.tokens * a.top_k);
   s.top_k = int(a.top_k);
   s.experts = int(a.experts);
   s.top_k_inverse = uint32_t((65536 + a.top_k - 1) / a.top_k);
+  s.rows = rows_at_once<F>(a);
   s.blocks = int(k / 128);
   s.blocks_inverse = uint32_t(((1 << 20) + s.blocks - 1) / s.blocks);
   s.units = (s.blocks + F::kBlocks - 1) / F::kBlocks;
@@ -585,7 +641,9 @@ Shape shape_of(const tq2_moe_experts_args& a, int64_t n, int64_t k, int most, bo
   s.part_units = (s.units + (1 << s.wk_shift) - 1) >> s.wk_shift;
   s.rounds = (s.part_units + kUnits - 1) / kUnits;
   s.per = (s.part_units + s.rounds - 1) / s.rounds;
-  s.steps = s.tiles / ((kWaves >> s.wk_shift) >> (gate ? 1 : 0));
+  const int per_step = (waves >> s.wk_shift) >> (gate ? 1 : 0);
+  s.steps = (s.tiles + per_step - 1) / per_step;
+  s.few = s.pairs <= 64;
   s.by_pair = s.pairs < s.experts;
   return s;
 }
@@ -595,45 +653,47 @@ hipError_t allow_lds(const void* fn, int lds) {
                           : hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
 }
 
-// LDS of rows_kernel beside x: partial sums, the list of pairs and its counts.
-template <Mode M>
-int rest_bytes(int pairs) { return kRedBytes<M> + (kWaves * 4 + pairs * 2 + 15) / 16 * 16; }
-
-// Rows of x at a time: no more than an expert can have, as many as LDS holds.
-template <Mode M>
-int rows_at_once(int pairs, int blocks) {
-  int rows = pairs < kRowsOf<M> ? pairs : kRowsOf<M>;
-  while (x_bytes<M>(blocks, rows) + rest_bytes<M>(pairs) > kLds) --rows;
-  return rows;
+// Items that the pairs can make: as many as experts have a pair, and one for each further `rows`.
+int most_items(int pairs, int experts, int rows) {
+  const int used = pairs < experts ? pairs : experts;
+  return used + (pairs - used) / rows;
 }
 
-template <class F, class X, bool GATE, Mode M>
-hipError_t launch_rows(const tq2_moe_experts_args& a, const Weight& w, const void* x, float* out, int64_t n, int64_t k,
-                       hipStream_t stream) {
-  Shape s = shape_of<F>(a, n, k, GATE ? kWaves / 2 : kWaves, GATE);
-  s.rows = rows_at_once<M>(s.pairs, s.blocks);
-  const int lds = x_bytes<M>(s.blocks, s.rows) + rest_bytes<M>(s.pairs);
-  const int experts = s.by_pair ? s.pairs : s.experts;
-  int across = (1024 + experts - 1) / experts;
+template <class F, class X, bool GATE, int WAVES, int SETS>
+hipError_t launch_rows(const tq2_moe_experts_args& a, const Weight& w, const void* x, const Items& items, float* out,
+                       int64_t n, int64_t k, hipStream_t stream) {
+  const Shape s = shape_of<F>(a, n, k, WAVES, GATE ? WAVES / 2 : WAVES, GATE);
+  const int lds = lds_bytes<F>(s.blocks, s.rows, WAVES);
+  const int down = s.few ? (s.by_pair ? s.pairs : s.experts) : most_items(s.pairs, s.experts, s.rows);
+  int across = (1024 + down - 1) / down;
   if (across > s.steps) across = s.steps;
-  const auto fn = rows_kernel<F, X, GATE, M>;
+  const auto fn = rows_kernel<F, X, GATE, WAVES, SETS>;
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fn, dim3(across, experts), dim3(kThreads), lds, stream, w,
-                     static_cast<const typename X::elem*>(x), a.ids, a.weights, out, s);
+  hipLaunchKernelGGL(fn, dim3(across, down), dim3(64 * WAVES), lds, stream, w,
+                     static_cast<const typename X::elem*>(x), a.ids, items, a.weights, out, s);
   return hipGetLastError();
 }
 
-// Up to 16 rows of f32 at a time where experts have more than 8 and LDS holds more.
-bool many_rows(const tq2_moe_experts_args& a, int64_t k) {
-  return a.tokens * a.top_k > 6 * a.experts && rows_at_once<kBoth>(int(a.tokens * a.top_k), int(k / 128)) > 8;
+// Blocks of 8 waves where two of them share a CU's LDS, otherwise one of 16.
+template <class F, class X, bool GATE>
+hipError_t launch_rows(const tq2_moe_experts_args& a, const Weight& w, const void* x, const Items& items, float* out,
+                       int64_t n, int64_t k, hipStream_t stream) {
+  const int rows = rows_at_once<F>(a);
+  const bool two = 2 * lds_bytes<F>(int(k / 128), rows, 8) <= kLds;
+  if (rows <= 4) return two ? launch_rows<F, X, GATE, 8, 1>(a, w, x, items, out, n, k, stream)
+                            : launch_rows<F, X, GATE, 16, 1>(a, w, x, items, out, n, k, stream);
+  return two ? launch_rows<F, X, GATE, 8, 2>(a, w, x, items, out, n, k, stream)
+             : launch_rows<F, X, GATE, 16, 2>(a, w, x, items, out, n, k, stream);
 }
 
 // LDS of token_kernel, whose blocks hold all of a token's rows.
-int token_lds(const tq2_moe_experts_args& a) { return x_bytes<kPacked>(int(a.top_k * (a.inter / 128)), 1); }
+template <class F>
+int token_lds(const tq2_moe_experts_args& a) { return x_bytes<F>(int(a.top_k * (a.inter / 128)), 1); }
 
+template <class F>
 bool by_token(const tq2_moe_experts_args& a) {
-  return a.tokens * a.top_k <= 32 && token_lds(a) + kWaves * 64 <= kLds;
+  return a.tokens * a.top_k <= 32 && token_lds<F>(a) + kTokenWaves * 64 <= kLds;
 }
 
 template <class F>
@@ -649,31 +709,36 @@ Weight weight_of(const void* codes, const void* scales, int64_t rows, int64_t k)
 
 template <class F, class X>
 hipError_t launch(const tq2_moe_experts_args& a, const MoePlan& plan, hipStream_t stream) {
-  float* h = static_cast<float*>(a.workspace);
-  float* y = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + plan.y_offset);
+  char* ws = static_cast<char*>(a.workspace);
+  float* h = reinterpret_cast<float*>(ws);
+  float* y = reinterpret_cast<float*>(ws + plan.y_offset);
+  Items items;
+  items.count = reinterpret_cast<int*>(ws + plan.items_offset);
+  items.item = reinterpret_cast<Item*>(items.count + 4);
+  items.order = reinterpret_cast<uint16_t*>(items.item + a.tokens * a.top_k);
   const Weight up = weight_of<F>(a.gate_up, a.gate_up_scales, 2 * a.experts * a.inter, a.hidden);
   const Weight down = weight_of<F>(a.down, a.down_scales, a.experts * a.hidden, a.inter);
   hipError_t e;
-  if constexpr (sizeof(typename X::elem) == 2) {
-    e = launch_rows<F, X, true, kHigh>(a, up, a.x, h, a.inter, a.hidden, stream);
-  } else {
-    e = many_rows(a, a.hidden) ? launch_rows<F, X, true, kBoth>(a, up, a.x, h, a.inter, a.hidden, stream)
-                               : launch_rows<F, X, true, kPacked>(a, up, a.x, h, a.inter, a.hidden, stream);
+  if (a.tokens * a.top_k > 64) {
+    hipLaunchKernelGGL(items_kernel, dim3(1), dim3(kItemThreads), 0, stream, a.ids, int(a.tokens * a.top_k),
+                       int(a.experts), rows_at_once<F>(a), items);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
+  e = launch_rows<F, X, true>(a, up, a.x, items, h, a.inter, a.hidden, stream);
   if (e != hipSuccess) return e;
   const auto* residual = static_cast<const typename X::elem*>(a.residual);
   auto* out = static_cast<typename X::elem*>(a.out);
-  if (by_token(a)) {
-    const Shape s = shape_of<F>(a, a.hidden, a.inter, 1, false);
+  if (by_token<F>(a)) {
+    const Shape s = shape_of<F>(a, a.hidden, a.inter, 1, 1, false);
     const auto fn = token_kernel<F, X>;
-    e = allow_lds(reinterpret_cast<const void*>(fn), token_lds(a));
+    e = allow_lds(reinterpret_cast<const void*>(fn), token_lds<F>(a));
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(fn, dim3(s.tiles, uint32_t(a.tokens)), dim3(kThreads), token_lds(a), stream, down, h, a.ids,
-                       a.weights, residual, out, s);
+    hipLaunchKernelGGL(fn, dim3(s.tiles, uint32_t(a.tokens)), dim3(64 * kTokenWaves), token_lds<F>(a), stream, down, h,
+                       a.ids, a.weights, residual, out, s);
     return hipGetLastError();
   }
-  e = many_rows(a, a.inter) ? launch_rows<F, F32, false, kBoth>(a, down, h, y, a.hidden, a.inter, stream)
-                            : launch_rows<F, F32, false, kPacked>(a, down, h, y, a.hidden, a.inter, stream);
+  e = launch_rows<F, F32, false>(a, down, h, items, y, a.hidden, a.inter, stream);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(sum_kernel<X>, dim3((a.hidden + 1023) / 1024, a.tokens), dim3(256), 0, stream, y, a.ids, residual,
                      out, int(a.top_k), int(a.experts), int(a.hidden));
@@ -692,7 +757,8 @@ hipError_t launch(const tq2_moe_experts_args& a, const MoePlan& plan, hipStream_
 MoePlan plan_moe(const tq2_moe_experts_args& a) {
   MoePlan p;
   p.y_offset = align256(size_t(a.tokens) * size_t(a.top_k) * size_t(a.inter) * 4);
-  p.workspace = p.y_offset + size_t(a.tokens) * size_t(a.top_k) * size_t(a.hidden) * 4;
+  p.items_offset = p.y_offset + align256(size_t(a.tokens) * size_t(a.top_k) * size_t(a.hidden) * 4);
+  p.workspace = p.items_offset + 16 + size_t(a.tokens) * size_t(a.top_k) * (sizeof(Item) + 2);
   return p;
 }
 

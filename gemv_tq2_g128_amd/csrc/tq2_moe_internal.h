@@ -16,6 +16,7 @@ hipError_t launch_moe_route(const tq2_moe_route_args& a, hipStream_t stream);
 // Layout of a call of tq2_moe_experts.
 struct MoePlan {
   size_t y_offset;           // of the weighted rows in the workspace, behind the rows between the projections
+  size_t items_offset;       // of the pairs sorted by expert
   size_t workspace;
 };
 MoePlan plan_moe(const tq2_moe_experts_args& a);
