@@ -32,7 +32,8 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kTokenWaves = 8;                  // of a block of token_kernel
 constexpr int kMaxRows = 8;                     // rows of x that a block has at a time, four to a matrix operand
-constexpr int kUnits = 4;                       // 64-byte pieces of a weight row that a wave has in flight
+constexpr int kUnits = 2;                       // 64-byte pieces that a wave of rows_kernel takes of each row at a time
+constexpr int kTokenUnits = 4;                  // and one of token_kernel
 constexpr int kLds = 160 * 1024;
 
 // A weight format: kGroup, the columns of a scale; kBlocks, the 128-wide blocks of a row's 64 bytes; kMiddle, the code
@@ -83,13 +84,13 @@ __device__ __forceinline__ void place_of(int u, int* step, int* grp, int* half) 
   }
 }
 
-// A lane's pieces of kUnits consecutive 64-byte units of its row, and the scales of their blocks.
-template <class F>
+// A lane's pieces of N consecutive 64-byte units of its row, and the scales of their blocks.
+template <class F, int N>
 struct Codes {
-  static constexpr int kBlocks = kUnits * F::kBlocks;
+  static constexpr int kBlocks = N * F::kBlocks;
   static constexpr int kScales = kBlocks * (128 / F::kGroup);      // binary16
   static constexpr int kWords = F::kGroup == 128 ? kScales / 2 + 1 : kScales / 2;
-  u32x4_t w[kUnits];
+  u32x4_t w[N];
   uint32_t d[kWords];                                               // kGroup == 128: from bit `down` on
   uint32_t down;
 };
@@ -113,47 +114,44 @@ __device__ __forceinline__ Rows rows_at(const Weight& w, int64_t row0) {
               make_rsrc(w.scales + row0 * w.row_scales, (16 * w.row_scales * 2 + 3) & ~3u)};
 }
 
-// Units unit .. unit + kUnits - 1 of the lane's row; `count` of them are wanted.  Every load is issued, wanted or not
+// Units unit .. unit + N - 1 of the lane's row; `count` of them are wanted.  Every load is issued, wanted or not
 // (those give zeros): behind a branch the count of loads in flight would be unknown to the waits.
-template <class F>
+template <class F, int N>
 __device__ __forceinline__ void load_codes(const Rows& rows, uint32_t row_bytes, uint32_t code_off, uint32_t scale_off,
-                                           uint32_t unit, int count, uint32_t in_row, Codes<F>& c) {
+                                           uint32_t unit, int count, uint32_t in_row, Codes<F, N>& c) {
 #pragma unroll
-  for (int j = 0; j < kUnits; ++j) {
+  for (int j = 0; j < N; ++j) {
     const uint32_t at = (unit + j) * 64 + in_row;
     // The last half unit of a ternary row is the next row's.
     const bool ok = j < count && (F::kBlocks == 1 || at < row_bytes);
-    c.w[j] = __builtin_amdgcn_raw_buffer_load_b128(rows.codes, ok ? code_off + (unit + j) * 64 : kNowhere, 0,
-                                                   kStreamOnce);
+    // Without the hint that they are read once (111 us against 118 for 64 tokens, 188 against 211 for 128): a line of 128
+    // bytes is two loads, and items of one expert share its weights.
+    c.w[j] = __builtin_amdgcn_raw_buffer_load_b128(rows.codes, ok ? code_off + (unit + j) * 64 : kNowhere, 0, 0);
   }
-  const uint32_t at = count > 0 ? scale_off + unit * (F::kBlocks * 256 / F::kGroup) : kNowhere;
-  if constexpr (F::kGroup == 128) {
-    // Two-byte scales may start in the middle of a word, where buffer loads do not: the words around them.
-    if constexpr (F::kBlocks == 1) {
-      const u32x2_t d = __builtin_amdgcn_raw_buffer_load_b64(rows.scales, at & ~3u, 0, 0);
-      c.d[0] = d[0];
-      c.d[1] = d[1];
-    } else {
-      const u32x4_t d = __builtin_amdgcn_raw_buffer_load_b128(rows.scales, at & ~3u, 0, 0);
+  constexpr int kWords = Codes<F, N>::kWords;
+  uint32_t at = count > 0 ? scale_off + unit * (F::kBlocks * 256 / F::kGroup) : kNowhere;
+  // Two-byte scales may start in the middle of a word, where buffer loads do not: the words around them.
+  c.down = (at & 2) * 8;
+  at &= ~3u;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c.d[i] = d[i];
-    }
-    c.d[Codes<F>::kWords - 1] =
-        __builtin_amdgcn_raw_buffer_load_b32(rows.scales, (at & ~3u) + (Codes<F>::kWords - 1) * 4, 0, 0);
-    c.down = (at & 2) * 8;
-  } else {
+  for (int i = 0; i + 4 <= kWords; i += 4) {
+    const u32x4_t d = __builtin_amdgcn_raw_buffer_load_b128(rows.scales, at + i * 4, 0, 0);
 #pragma unroll
-    for (int i = 0; i < Codes<F>::kWords / 4; ++i) {
-      const u32x4_t d = __builtin_amdgcn_raw_buffer_load_b128(rows.scales, at + i * 16, 0, 0);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) c.d[4 * i + e] = d[e];
-    }
+    for (int e = 0; e < 4; ++e) c.d[i + e] = d[e];
   }
+  if constexpr (kWords & 2) {
+    constexpr int i = kWords & ~3;
+    const u32x2_t d = __builtin_amdgcn_raw_buffer_load_b64(rows.scales, at + i * 4, 0, 0);
+    c.d[i] = d[0];
+    c.d[i + 1] = d[1];
+  }
+  if constexpr (kWords & 1)
+    c.d[kWords - 1] = __builtin_amdgcn_raw_buffer_load_b32(rows.scales, at + (kWords - 1) * 4, 0, 0);
 }
 
 // The scale of 32-wide step s of block b.
-template <class F>
-__device__ __forceinline__ float scale_of(const Codes<F>& c, int b, int s) {
+template <class F, int N>
+__device__ __forceinline__ float scale_of(const Codes<F, N>& c, int b, int s) {
   const int i = b * (128 / F::kGroup) + s / (F::kGroup / 32);
   uint32_t w = c.d[i >> 1];
   if constexpr (F::kGroup == 128) w = __builtin_amdgcn_alignbit(c.d[(i >> 1) + 1], w, c.down);
@@ -263,53 +261,70 @@ __device__ __forceinline__ void stage8(const typename X::elem* __restrict__ bloc
     r.backs[kb * m + row] = top >= 0x7F800000 ? __builtin_nanf("") : __builtin_ldexpf(1.0f, -up) * share;
 }
 
-// Block b of unit j (b < F::kBlocks) of the lane's weight row r16 against SETS times four rows of x: lane group g4 adds
-// row 4 set + g4's product to acc[set].  at: the lane's operand column of the first set; from, back: the lane group's row.
-template <class F, int SETS>
-__device__ __forceinline__ void multiply(const Codes<F>& c, int j, int b, int kb, const Rows31& x, int g4, int cols,
-                                         const int (&at)[SETS], const int (&row)[SETS], int m, float (&acc)[SETS]) {
+// Block b of unit j (b < F::kBlocks) of TILES times 16 weight rows against SETS times four rows of x: lane group g4 adds
+// row 4 set + g4's product with weight row r16 to acc[tile][set].  at: the lane's operand columns; row: its group's rows.
+template <class F, int N, int TILES, int SETS>
+__device__ __forceinline__ void multiply(const Codes<F, N> (&c)[TILES], int j, int b, int kb, const Rows31& x, int g4,
+                                         int cols, const int (&at)[SETS], const int (&row)[SETS], int m,
+                                         float (&acc)[TILES][SETS]) {
   constexpr int kWide = F::kGroup == 32 ? 8 : 16;
   float back[SETS];
 #pragma unroll
   for (int q = 0; q < SETS; ++q) back[q] = x.backs[kb * m + row[q]];
 #pragma unroll
   for (int g = 0; g < kGroups<F>; ++g) {
-    i32x4_t sum[SETS];
+    i32x4_t sum[TILES][SETS];
 #pragma unroll
-    for (int q = 0; q < SETS; ++q) sum[q] = x.starts[(kb * kGroups<F> + g) * m + row[q]];
+    for (int q = 0; q < SETS; ++q) {
+      sum[0][q] = x.starts[(kb * kGroups<F> + g) * m + row[q]];
+#pragma unroll
+      for (int t = 1; t < TILES; ++t) sum[t][q] = sum[0][q];
+    }
 #pragma unroll
     for (int s = g * kSteps<F> / kGroups<F>; s < (g + 1) * kSteps<F> / kGroups<F>; ++s) {
       const char* operand = x.operands + (size_t(kb * kSteps<F> + s) * 4 + g4) * cols * kWide;
       if constexpr (F::kGroup == 32) {
-        const uint32_t w = c.w[j][s];
-        const u32x2_t codes = {w & 0x0F0F0F0Fu, w >> 4 & 0x0F0F0F0Fu};
+        long a[SETS];
 #pragma unroll
-        for (int q = 0; q < SETS; ++q)
-          sum[q] = __builtin_amdgcn_mfma_i32_16x16x32_i8(*reinterpret_cast<const long*>(operand + at[q] * kWide),
-                                                         __builtin_bit_cast(long, codes), sum[q], 0, 0, 0);
-      } else {
-        u32x4_t codes;
-        if constexpr (F::kBlocks == 2) {
-          const uint32_t w = c.w[j][2 * b + s];
-          codes = u32x4_t{w & 0x03030303u, w >> 2 & 0x03030303u, w >> 4 & 0x03030303u, w >> 6 & 0x03030303u};
-        } else {
-          const uint32_t w = c.w[j][2 * s], v = c.w[j][2 * s + 1];
-          codes = u32x4_t{w & 0x0F0F0F0Fu, w >> 4 & 0x0F0F0F0Fu, v & 0x0F0F0F0Fu, v >> 4 & 0x0F0F0F0Fu};
+        for (int q = 0; q < SETS; ++q) a[q] = *reinterpret_cast<const long*>(operand + at[q] * kWide);
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+          const uint32_t w = c[t].w[j][s];
+          const u32x2_t codes = {w & 0x0F0F0F0Fu, w >> 4 & 0x0F0F0F0Fu};
+#pragma unroll
+          for (int q = 0; q < SETS; ++q)
+            sum[t][q] = __builtin_amdgcn_mfma_i32_16x16x32_i8(a[q], __builtin_bit_cast(long, codes), sum[t][q], 0, 0, 0);
         }
+      } else {
+        i32x4_t a[SETS];
 #pragma unroll
-        for (int q = 0; q < SETS; ++q)
-          sum[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(*reinterpret_cast<const i32x4_t*>(operand + at[q] * kWide),
-                                                         __builtin_bit_cast(i32x4_t, codes), sum[q], 0, 0, 0);
+        for (int q = 0; q < SETS; ++q) a[q] = *reinterpret_cast<const i32x4_t*>(operand + at[q] * kWide);
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+          u32x4_t codes;
+          if constexpr (F::kBlocks == 2) {
+            const uint32_t w = c[t].w[j][2 * b + s];
+            codes = u32x4_t{w & 0x03030303u, w >> 2 & 0x03030303u, w >> 4 & 0x03030303u, w >> 6 & 0x03030303u};
+          } else {
+            const uint32_t w = c[t].w[j][2 * s], v = c[t].w[j][2 * s + 1];
+            codes = u32x4_t{w & 0x0F0F0F0Fu, w >> 4 & 0x0F0F0F0Fu, v & 0x0F0F0F0Fu, v >> 4 & 0x0F0F0F0Fu};
+          }
+#pragma unroll
+          for (int q = 0; q < SETS; ++q)
+            sum[t][q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[q], __builtin_bit_cast(i32x4_t, codes), sum[t][q], 0, 0, 0);
+        }
       }
     }
-    const float d = scale_of<F>(c, j * F::kBlocks + b, g * (F::kGroup / 32));
 #pragma unroll
-    for (int q = 0; q < SETS; ++q) {
-      // Bytes of the integers, the lowest first; f32 holds each sum (below 2^18) and rounds the joined ones.
-      float v = __builtin_fmaf(float(sum[q][3]), 256.f, float(sum[q][2]));
-      v = __builtin_fmaf(v, 256.f, float(sum[q][1]));
-      v = __builtin_fmaf(v, 256.f, float(sum[q][0]));
-      acc[q] = __builtin_fmaf(d * v, back[q], acc[q]);
+    for (int t = 0; t < TILES; ++t) {
+      const float d = scale_of<F, N>(c[t], j * F::kBlocks + b, g * (F::kGroup / 32));
+#pragma unroll
+      for (int q = 0; q < SETS; ++q) {
+        // Two bytes joined are whole numbers below 2^27; f32 rounds them and the four.
+        const i32x4_t v = sum[t][q];
+        const float four = __builtin_fmaf(float((v[3] << 8) + v[2]), 65536.f, float((v[1] << 8) + v[0]));
+        acc[t][q] = __builtin_fmaf(d * four, back[q], acc[t][q]);
+      }
     }
   }
 }
@@ -333,7 +348,7 @@ struct Shape {
   int blocks;                // 128-wide blocks of K
   uint32_t blocks_inverse;   // i * blocks_inverse >> 20 is i / blocks
   int units;                 // 64-byte pieces of a weight row
-  int tiles;                 // column tiles of an expert (of gate, and as many of up)
+  int tiles;                 // column tiles of an expert (of gate, and as many of up): a multiple of 8
   int wk_shift;              // log2 of the parts of K
   int part_units, rounds, per;         // units of a part, its rounds, units of a round
   int steps;                 // of column tiles that the block's waves take together
@@ -391,7 +406,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, cons
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   constexpr int kThreads = 64 * WAVES, kRows = 4 * SETS;
   float* red = reinterpret_cast<float*>(smem + x_bytes<F>(sh.blocks, sh.rows));
-  uint16_t* list = reinterpret_cast<uint16_t*>(red + 2 * WAVES * kRows * 16);
+  uint16_t* list = reinterpret_cast<uint16_t*>(red + 2 * WAVES * kRows * 16);    // after [wave][tile][row][column]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
   int e, found;
@@ -413,21 +428,24 @@ __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, cons
   }
   __builtin_amdgcn_wave_barrier();
 
-  // The wave's part: a tile of each step, and units of K.
+  // The wave's part: two tiles of each step (gate and up, or neighbours), which share what is read of x, and units of K.
   const int slot = wave >> sh.wk_shift, part = wave & ((1 << sh.wk_shift) - 1);
   const int unit0 = part * sh.part_units, mine = min(sh.part_units, sh.units - unit0);
-  const int per_step = (WAVES >> sh.wk_shift) >> (GATE ? 1 : 0);
+  const int per_step = WAVES >> sh.wk_shift, twos = GATE ? sh.tiles : sh.tiles / 2;
   const int64_t width = int64_t(sh.tiles) * 16;
   const int64_t expert_row = int64_t(e) * width * (GATE ? 2 : 1);
   const uint32_t code_off = r16 * weight.row_bytes + g4 * 16, scale_off = r16 * weight.row_scales * 2;
 
-  Codes<F> c[2];
-  auto load = [&](int step, int round, Codes<F>& into) {
-    const int tile = step * per_step + (GATE ? slot >> 1 : slot);
-    const bool there = step < sh.steps && tile < sh.tiles;
-    const int64_t row0 = expert_row + (GATE && (slot & 1) ? width : 0) + (there ? tile * 16 : 0);
-    load_codes<F>(rows_at(weight, row0), weight.row_bytes, code_off, scale_off, uint32_t(unit0 + round * sh.per),
-                  there ? min(sh.per, mine - round * sh.per) : 0, g4 * 16, into);
+  Codes<F, kUnits> c[2][2];
+  auto load = [&](int step, int round, Codes<F, kUnits> (&into)[2]) {
+    const int two = step * per_step + slot;
+    const bool there = two < twos;
+    const int64_t row0 = expert_row + (there ? two * (GATE ? 16 : 32) : 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      load_codes<F, kUnits>(rows_at(weight, row0 + (GATE ? i * width : i * 16)), weight.row_bytes, code_off, scale_off,
+                            uint32_t(unit0 + round * sh.per), there ? min(sh.per, mine - round * sh.per) : 0, g4 * 16,
+                            into[i]);
   };
   int step = blockIdx.x, round = 0;
   load(step, 0, c[0]);                                   // in flight while x is converted
@@ -454,48 +472,51 @@ __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, cons
       at[q] = q * 4 + (r16 >> 2) < m ? q * 16 + r16 : r16 & 3;
       own[q] = q * 4 + g4 < m ? q * 4 + g4 : 0;
     }
-    float acc[SETS] = {};
-    int parity = 0;
-    auto compute = [&](Codes<F>& from) {
+    float acc[2][SETS] = {};
+    auto compute = [&](Codes<F, kUnits> (&from)[2]) {
 #pragma unroll
       for (int j = 0; j < kUnits; ++j) {
         const int unit = unit0 + round * sh.per + j;
         if (j >= sh.per || round * sh.per + j >= mine) continue;
-        arrange<F>(from.w[j]);
+        arrange<F>(from[0].w[j]);
+        arrange<F>(from[1].w[j]);
 #pragma unroll
         for (int b = 0; b < F::kBlocks; ++b) {
           const int kb = unit * F::kBlocks + b;
           if (F::kBlocks > 1 && kb >= sh.blocks) continue;
-          multiply<F, SETS>(from, j, b, kb, rows, g4, cols, at, own, m, acc);
+          multiply<F, kUnits, 2, SETS>(from, j, b, kb, rows, g4, cols, at, own, m, acc);
         }
       }
     };
-    // Partial sums [wave][row of x][weight row] of a step meet; a buffer is written again two steps on, behind the
-    // next step's barrier.
+    // Partial sums [wave][tile][row of x][weight row] of a step meet.
     auto finish = [&]() {
-      float* buf = red + parity * (WAVES * kRows * 16);
-      parity ^= 1;
+      __syncthreads();                                   // the last step's have been read
 #pragma unroll
-      for (int q = 0; q < SETS; ++q) {
-        buf[(wave * kRows + q * 4 + g4) * 16 + r16] = acc[q];
-        acc[q] = 0.f;
-      }
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int q = 0; q < SETS; ++q) {
+          red[((wave * 2 + i) * kRows + q * 4 + g4) * 16 + r16] = acc[i][q];
+          acc[i][q] = 0.f;
+        }
       __syncthreads();
-      for (int i = threadIdx.x; i < per_step * kRows * 16; i += kThreads) {
+      // GATE: a gate and an up tile give one of the output; otherwise each tile its own.
+      constexpr int kOut = GATE ? 1 : 2;
+      for (int i = threadIdx.x; i < per_step * kOut * kRows * 16; i += kThreads) {
         const int n = i & 15, row = i >> 4 & (kRows - 1), tile = i / (16 * kRows);
-        if (row >= m || step * per_step + tile >= sh.tiles) continue;
+        const int two = step * per_step + tile / kOut;
+        if (row >= m || two >= twos) continue;
         const int p = list[first + row];
-        const float* from = buf + row * 16 + n;
+        const float* from = red + ((((tile / kOut) << sh.wk_shift) * 2 + tile % kOut) * kRows + row) * 16 + n;
         float a = 0.f, b = 0.f;
         for (int w = 0; w < 1 << sh.wk_shift; ++w) {
-          a += from[(((GATE ? 2 * tile : tile) << sh.wk_shift) + w) * (kRows * 16)];
-          if (GATE) b += from[(((2 * tile + 1) << sh.wk_shift) + w) * (kRows * 16)];
+          a += from[w * (2 * kRows * 16)];
+          if (GATE) b += from[w * (2 * kRows * 16) + kRows * 16];
         }
         const float v = GATE ? a / (1.f + expf(-a)) * b : a * share[p];
-        out[p * width + (int64_t(step) * per_step + tile) * 16 + n] = v;
+        out[p * width + int64_t(two) * (16 * kOut) + tile % kOut * 16 + n] = v;
       }
     };
-    auto walk = [&](Codes<F>& now, Codes<F>& then) {
+    auto walk = [&](Codes<F, kUnits> (&now)[2], Codes<F, kUnits> (&then)[2]) {
       const bool last = round + 1 == sh.rounds;
       const int next = last ? step + int(gridDim.x) : step, next_round = last ? 0 : round + 1;
       load(next, next_round, then);
@@ -534,19 +555,19 @@ __global__ __launch_bounds__(64 * kTokenWaves, 2) void token_kernel(Weight weigh
 
   // Round r is part r % rounds of place r / rounds; the wave has rounds wave, wave + kTokenWaves, ...
   const int all_rounds = sh.top_k * sh.rounds;
-  Codes<F> c[2];
+  Codes<F, kTokenUnits> c[2][1];
   int place = 0, round = wave;                           // of the round that is loaded next
   struct At {
     int place, unit, count;
   };
-  auto load = [&](Codes<F>& into) {
+  auto load = [&](Codes<F, kTokenUnits> (&into)[1]) {
     while (round >= sh.rounds && place < sh.top_k) round -= sh.rounds, ++place;
     const bool there = place < sh.top_k;
     const int e = __builtin_amdgcn_readlane(id, there ? place : 0);
     const bool real = there && uint32_t(e) < uint32_t(sh.experts);
     const At at = {place, round * sh.per, real ? min(sh.per, sh.units - round * sh.per) : 0};
-    load_codes<F>(rows_at(weight, (real ? int64_t(e) * hidden : 0) + int64_t(blockIdx.x) * 16), weight.row_bytes,
-                  code_off, scale_off, uint32_t(at.unit), at.count, g4 * 16, into);
+    load_codes<F, kTokenUnits>(rows_at(weight, (real ? int64_t(e) * hidden : 0) + int64_t(blockIdx.x) * 16),
+                               weight.row_bytes, code_off, scale_off, uint32_t(at.unit), at.count, g4 * 16, into[0]);
     round += kTokenWaves;
     return at;
   };
@@ -558,17 +579,17 @@ __global__ __launch_bounds__(64 * kTokenWaves, 2) void token_kernel(Weight weigh
   }
   __syncthreads();
   const int at[1] = {r16 & 3}, own[1] = {0};
-  float acc[1] = {0.f};
-  auto compute = [&](Codes<F>& from, const At& a) {
+  float acc[1][1] = {};
+  auto compute = [&](Codes<F, kTokenUnits> (&from)[1], const At& a) {
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
+    for (int j = 0; j < kTokenUnits; ++j) {
       if (j >= a.count) continue;
-      arrange<F>(from.w[j]);
+      arrange<F>(from[0].w[j]);
 #pragma unroll
       for (int b = 0; b < F::kBlocks; ++b) {
         const int k = (a.unit + j) * F::kBlocks + b;
         if (F::kBlocks > 1 && k >= sh.blocks) continue;
-        multiply<F, 1>(from, j, b, a.place * sh.blocks + k, rows, g4, cols, at, own, 1, acc);
+        multiply<F, kTokenUnits, 1, 1>(from, j, b, a.place * sh.blocks + k, rows, g4, cols, at, own, 1, acc);
       }
     }
   };
@@ -581,7 +602,7 @@ __global__ __launch_bounds__(64 * kTokenWaves, 2) void token_kernel(Weight weigh
     compute(c[1], then);
     done += kTokenWaves;
   }
-  if (g4 == 0) red[wave][r16] = acc[0];
+  if (g4 == 0) red[wave][r16] = acc[0][0];
   __syncthreads();
   if (threadIdx.x < 16) {
     float sum = 0.f;
@@ -612,19 +633,22 @@ __global__ __launch_bounds__(256) void sum_kernel(const float* __restrict__ y, c
 // Rows of x at a time for both projections: no more than an expert can have, as many as LDS holds.
 template <class F>
 int lds_bytes(int blocks, int rows, int waves) {
-  return x_bytes<F>(blocks, rows) + 2 * waves * (rows > 4 ? 8 : 4) * 64 + 128;
+  return x_bytes<F>(blocks, rows) + 2 * waves * (rows > 4 ? 8 : 4) * 64 + 128;          // sums of two tiles, the list
 }
 template <class F>
 int rows_at_once(const tq2_moe_experts_args& a) {
-  const int blocks = int((a.hidden > a.inter ? a.hidden : a.inter) / 128), pairs = int(a.tokens * a.top_k);
-  int rows = pairs < kMaxRows ? pairs : kMaxRows;
+  const int blocks = int((a.hidden > a.inter ? a.hidden : a.inter) / 128);
+  // A token hardly names an expert twice.  Four rows are one matrix operand, enough for most experts of a batch that has
+  // up to two pairs for each.
+  int rows = a.tokens < kMaxRows ? int(a.tokens) : kMaxRows;
+  if (rows > 4 && a.tokens * a.top_k <= 2 * a.experts) rows = 4;
   while (lds_bytes<F>(blocks, rows, 16) > kLds) --rows;
   return rows;
 }
 
-// The launch for n columns and k of K, with at most `most` parts of it.
+// The launch for n columns and k of K: `waves` of a block share it, `units` of a row at a time.
 template <class F>
-Shape shape_of(const tq2_moe_experts_args& a, int64_t n, int64_t k, int waves, int most, bool gate) {
+Shape shape_of(const tq2_moe_experts_args& a, int64_t n, int64_t k, int waves, int units, int twos) {
   Shape s;
   s.pairs = int(a.tokens * a.top_k);
   s.top_k = int(a.top_k);
@@ -635,16 +659,21 @@ Shape shape_of(const tq2_moe_experts_args& a, int64_t n, int64_t k, int waves, i
   s.blocks_inverse = uint32_t(((1 << 20) + s.blocks - 1) / s.blocks);
   s.units = (s.blocks + F::kBlocks - 1) / F::kBlocks;
   s.tiles = int(n / 16);
-  // Parts of K: as many as keep a wave's share at kUnits units.
-  s.wk_shift = 0;
-  while ((1 << s.wk_shift) < most && (kUnits << s.wk_shift) < s.units) ++s.wk_shift;
-  s.part_units = (s.units + (1 << s.wk_shift) - 1) >> s.wk_shift;
-  s.rounds = (s.part_units + kUnits - 1) / kUnits;
-  s.per = (s.part_units + s.rounds - 1) / s.rounds;
-  const int per_step = (waves >> s.wk_shift) >> (gate ? 1 : 0);
-  s.steps = (s.tiles + per_step - 1) / per_step;
   s.few = s.pairs <= 64;
   s.by_pair = s.pairs < s.experts;
+  // Parts of K that take the fewest rounds of all waves; among equals the most parts, whose blocks are the most.
+  int64_t best = INT64_MAX;
+  for (int shift = 0; (1 << shift) <= waves; ++shift) {
+    const int part = (s.units + (1 << shift) - 1) >> shift, rounds = (part + units - 1) / units;
+    const int per_step = waves >> shift, steps = (twos + per_step - 1) / per_step;
+    if (int64_t(rounds) * steps > best) continue;
+    best = int64_t(rounds) * steps;
+    s.wk_shift = shift;
+    s.part_units = part;
+    s.rounds = rounds;
+    s.per = (part + rounds - 1) / rounds;
+    s.steps = steps;
+  }
   return s;
 }
 
@@ -662,10 +691,13 @@ int most_items(int pairs, int experts, int rows) {
 template <class F, class X, bool GATE, int WAVES, int SETS>
 hipError_t launch_rows(const tq2_moe_experts_args& a, const Weight& w, const void* x, const Items& items, float* out,
                        int64_t n, int64_t k, hipStream_t stream) {
-  const Shape s = shape_of<F>(a, n, k, WAVES, GATE ? WAVES / 2 : WAVES, GATE);
+  const Shape s = shape_of<F>(a, n, k, WAVES, kUnits, int(n / (GATE ? 16 : 32)));
   const int lds = lds_bytes<F>(s.blocks, s.rows, WAVES);
   const int down = s.few ? (s.by_pair ? s.pairs : s.experts) : most_items(s.pairs, s.experts, s.rows);
-  int across = (1024 + down - 1) / down;
+  // Two blocks for each CU: the prologue (who, which rows, their conversion) is paid once, and an expert's steps are shared
+  // out evenly (64 tokens: 111 us with 512 blocks, 115 with 1024; 128 tokens, ternary: 188 and 225; one token, ternary: 30
+  // and 33).
+  int across = (512 + down - 1) / down;
   if (across > s.steps) across = s.steps;
   const auto fn = rows_kernel<F, X, GATE, WAVES, SETS>;
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), lds);
@@ -730,7 +762,7 @@ hipError_t launch(const tq2_moe_experts_args& a, const MoePlan& plan, hipStream_
   const auto* residual = static_cast<const typename X::elem*>(a.residual);
   auto* out = static_cast<typename X::elem*>(a.out);
   if (by_token<F>(a)) {
-    const Shape s = shape_of<F>(a, a.hidden, a.inter, 1, 1, false);
+    const Shape s = shape_of<F>(a, a.hidden, a.inter, 1, kTokenUnits, 1);
     const auto fn = token_kernel<F, X>;
     e = allow_lds(reinterpret_cast<const void*>(fn), token_lds<F>(a));
     if (e != hipSuccess) return e;
