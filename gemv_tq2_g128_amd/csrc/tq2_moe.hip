@@ -409,7 +409,10 @@ __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, cons
   uint16_t* list = reinterpret_cast<uint16_t*>(red + 2 * WAVES * kRows * 16);    // after [wave][tile][row][column]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
-  int e, found;
+  // Few pairs: the block has the steps blockIdx.x, blockIdx.x + gridDim.x, ... of its expert.  Otherwise a share of the
+  // steps of all items, one after another, which may begin and end inside one.
+  int e = 0, found = 0, step = 0, hop, end = 0;
+  int64_t now_at = 0, stop_at = 0;                       // of all items' steps
   if (sh.few) {
     // The ids of all pairs, at most 64, are one load; every wave lists the expert's pairs for itself.
     const int id = lane < sh.pairs ? ids[lane] : -1;
@@ -419,116 +422,137 @@ __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, cons
     if (mask == 0 || (sh.by_pair && __builtin_ctzll(mask) != int(blockIdx.y))) return;
     found = __popcll(mask);
     if (id == e) list[__popcll(mask & ((uint64_t(1) << lane) - 1))] = uint16_t(lane);
+    step = blockIdx.x;
+    hop = gridDim.x;
+    end = sh.steps;
   } else {
-    if (int(blockIdx.y) >= *items.count) return;
-    const Item item = items.item[blockIdx.y];
-    e = __builtin_amdgcn_readfirstlane(item.expert);
-    found = __builtin_amdgcn_readfirstlane(item.count);
-    if (lane < found) list[lane] = items.order[item.first + lane];
+    const int64_t all = int64_t(*items.count) * sh.steps;
+    now_at = all * blockIdx.x / gridDim.x;
+    stop_at = all * (blockIdx.x + 1) / gridDim.x;
+    if (now_at >= stop_at) return;
+    hop = 1;
   }
-  __builtin_amdgcn_wave_barrier();
-
   // The wave's part: two tiles of each step (gate and up, or neighbours), which share what is read of x, and units of K.
   const int slot = wave >> sh.wk_shift, part = wave & ((1 << sh.wk_shift) - 1);
   const int unit0 = part * sh.part_units, mine = min(sh.part_units, sh.units - unit0);
   const int per_step = WAVES >> sh.wk_shift, twos = GATE ? sh.tiles : sh.tiles / 2;
   const int64_t width = int64_t(sh.tiles) * 16;
-  const int64_t expert_row = int64_t(e) * width * (GATE ? 2 : 1);
   const uint32_t code_off = r16 * weight.row_bytes + g4 * 16, scale_off = r16 * weight.row_scales * 2;
 
   Codes<F, kUnits> c[2][2];
   auto load = [&](int step, int round, Codes<F, kUnits> (&into)[2]) {
     const int two = step * per_step + slot;
-    const bool there = two < twos;
-    const int64_t row0 = expert_row + (there ? two * (GATE ? 16 : 32) : 0);
+    const bool there = step < end && two < twos;
+    const int64_t row0 = int64_t(e) * width * (GATE ? 2 : 1) + (there ? two * (GATE ? 16 : 32) : 0);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       load_codes<F, kUnits>(rows_at(weight, row0 + (GATE ? i * width : i * 16)), weight.row_bytes, code_off, scale_off,
                             uint32_t(unit0 + round * sh.per), there ? min(sh.per, mine - round * sh.per) : 0, g4 * 16,
                             into[i]);
   };
-  int step = blockIdx.x, round = 0;
-  load(step, 0, c[0]);                                   // in flight while x is converted
-
-  for (int first = 0; first < found; first += sh.rows) {
-    const int m = min(sh.rows, found - first), cols = columns_of(m);
-    const Rows31 rows = rows_in<F>(smem, sh.blocks, m);
-    if (first > 0) {
-      step = blockIdx.x;
+  int round = 0, begin = 0;
+  for (bool more = true; more;) {
+    if (!sh.few) {
+      const int at = int(now_at / sh.steps);
+      const Item item = items.item[at];
+      e = __builtin_amdgcn_readfirstlane(item.expert);
+      found = __builtin_amdgcn_readfirstlane(item.count);
+      begin = int(now_at - int64_t(at) * sh.steps);
+      end = int(min(int64_t(sh.steps), begin + stop_at - now_at));
+      now_at += end - begin;
+      more = now_at < stop_at;
+      step = begin;
       round = 0;
+      load(step, 0, c[0]);                               // in flight while x is converted
+      __syncthreads();                                   // the last item's rows, sums and list have been read
+      if (lane < found) list[lane] = items.order[item.first + lane];
+    } else {
+      begin = blockIdx.x;
       load(step, 0, c[0]);
-      __syncthreads();                                   // the last step has read x and red
+      more = false;
     }
-    for (int i = threadIdx.x; i < m * sh.blocks * 16; i += kThreads) {
-      const int row = int((uint32_t(i >> 4) * sh.blocks_inverse) >> 20), kb = (i >> 4) - row * sh.blocks;
-      const uint32_t pair = list[first + row], from = GATE ? pair * sh.top_k_inverse >> 16 : pair;
-      stage8<F, X>(x + (int64_t(from) * sh.blocks + kb) * 128, i & 15, kb, row, m, cols, 1.f, rows);
-    }
-    __syncthreads();
-    // The lane's operand columns and its group's rows; past the last row they repeat the first one's.
-    int at[SETS], own[SETS];
-#pragma unroll
-    for (int q = 0; q < SETS; ++q) {
-      at[q] = q * 4 + (r16 >> 2) < m ? q * 16 + r16 : r16 & 3;
-      own[q] = q * 4 + g4 < m ? q * 4 + g4 : 0;
-    }
-    float acc[2][SETS] = {};
-    auto compute = [&](Codes<F, kUnits> (&from)[2]) {
-#pragma unroll
-      for (int j = 0; j < kUnits; ++j) {
-        const int unit = unit0 + round * sh.per + j;
-        if (j >= sh.per || round * sh.per + j >= mine) continue;
-        arrange<F>(from[0].w[j]);
-        arrange<F>(from[1].w[j]);
-#pragma unroll
-        for (int b = 0; b < F::kBlocks; ++b) {
-          const int kb = unit * F::kBlocks + b;
-          if (F::kBlocks > 1 && kb >= sh.blocks) continue;
-          multiply<F, kUnits, 2, SETS>(from, j, b, kb, rows, g4, cols, at, own, m, acc);
-        }
+    __builtin_amdgcn_wave_barrier();
+
+    for (int first = 0; first < found; first += sh.rows) {
+      const int m = min(sh.rows, found - first), cols = columns_of(m);
+      const Rows31 rows = rows_in<F>(smem, sh.blocks, m);
+      if (first > 0) {
+        step = begin;
+        round = 0;
+        load(step, 0, c[0]);
+        __syncthreads();                                   // the last step has read x and red
       }
-    };
-    // Partial sums [wave][tile][row of x][weight row] of a step meet.
-    auto finish = [&]() {
-      __syncthreads();                                   // the last step's have been read
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int q = 0; q < SETS; ++q) {
-          red[((wave * 2 + i) * kRows + q * 4 + g4) * 16 + r16] = acc[i][q];
-          acc[i][q] = 0.f;
-        }
+      for (int i = threadIdx.x; i < m * sh.blocks * 16; i += kThreads) {
+        const int row = int((uint32_t(i >> 4) * sh.blocks_inverse) >> 20), kb = (i >> 4) - row * sh.blocks;
+        const uint32_t pair = list[first + row], from = GATE ? pair * sh.top_k_inverse >> 16 : pair;
+        stage8<F, X>(x + (int64_t(from) * sh.blocks + kb) * 128, i & 15, kb, row, m, cols, 1.f, rows);
+      }
       __syncthreads();
-      // GATE: a gate and an up tile give one of the output; otherwise each tile its own.
-      constexpr int kOut = GATE ? 1 : 2;
-      for (int i = threadIdx.x; i < per_step * kOut * kRows * 16; i += kThreads) {
-        const int n = i & 15, row = i >> 4 & (kRows - 1), tile = i / (16 * kRows);
-        const int two = step * per_step + tile / kOut;
-        if (row >= m || two >= twos) continue;
-        const int p = list[first + row];
-        const float* from = red + ((((tile / kOut) << sh.wk_shift) * 2 + tile % kOut) * kRows + row) * 16 + n;
-        float a = 0.f, b = 0.f;
-        for (int w = 0; w < 1 << sh.wk_shift; ++w) {
-          a += from[w * (2 * kRows * 16)];
-          if (GATE) b += from[w * (2 * kRows * 16) + kRows * 16];
-        }
-        const float v = GATE ? a / (1.f + expf(-a)) * b : a * share[p];
-        out[p * width + int64_t(two) * (16 * kOut) + tile % kOut * 16 + n] = v;
+      // The lane's operand columns and its group's rows; past the last row they repeat the first one's.
+      int at[SETS], own[SETS];
+#pragma unroll
+      for (int q = 0; q < SETS; ++q) {
+        at[q] = q * 4 + (r16 >> 2) < m ? q * 16 + r16 : r16 & 3;
+        own[q] = q * 4 + g4 < m ? q * 4 + g4 : 0;
       }
-    };
-    auto walk = [&](Codes<F, kUnits> (&now)[2], Codes<F, kUnits> (&then)[2]) {
-      const bool last = round + 1 == sh.rounds;
-      const int next = last ? step + int(gridDim.x) : step, next_round = last ? 0 : round + 1;
-      load(next, next_round, then);
-      compute(now);
-      if (last) finish();
-      step = next;
-      round = next_round;
-    };
-    while (step < sh.steps) {
-      walk(c[0], c[1]);
-      if (step >= sh.steps) break;
-      walk(c[1], c[0]);
+      float acc[2][SETS] = {};
+      auto compute = [&](Codes<F, kUnits> (&from)[2]) {
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j) {
+          const int unit = unit0 + round * sh.per + j;
+          if (j >= sh.per || round * sh.per + j >= mine) continue;
+          arrange<F>(from[0].w[j]);
+          arrange<F>(from[1].w[j]);
+#pragma unroll
+          for (int b = 0; b < F::kBlocks; ++b) {
+            const int kb = unit * F::kBlocks + b;
+            if (F::kBlocks > 1 && kb >= sh.blocks) continue;
+            multiply<F, kUnits, 2, SETS>(from, j, b, kb, rows, g4, cols, at, own, m, acc);
+          }
+        }
+      };
+      // Partial sums [wave][tile][row of x][weight row] of a step meet.
+      auto finish = [&]() {
+        __syncthreads();                                   // the last step's have been read
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int q = 0; q < SETS; ++q) {
+            red[((wave * 2 + i) * kRows + q * 4 + g4) * 16 + r16] = acc[i][q];
+            acc[i][q] = 0.f;
+          }
+        __syncthreads();
+        // GATE: a gate and an up tile give one of the output; otherwise each tile its own.
+        constexpr int kOut = GATE ? 1 : 2;
+        for (int i = threadIdx.x; i < per_step * kOut * kRows * 16; i += kThreads) {
+          const int n = i & 15, row = i >> 4 & (kRows - 1), tile = i / (16 * kRows);
+          const int two = step * per_step + tile / kOut;
+          if (row >= m || two >= twos) continue;
+          const int p = list[first + row];
+          const float* from = red + ((((tile / kOut) << sh.wk_shift) * 2 + tile % kOut) * kRows + row) * 16 + n;
+          float a = 0.f, b = 0.f;
+          for (int w = 0; w < 1 << sh.wk_shift; ++w) {
+            a += from[w * (2 * kRows * 16)];
+            if (GATE) b += from[w * (2 * kRows * 16) + kRows * 16];
+          }
+          const float v = GATE ? a / (1.f + expf(-a)) * b : a * share[p];
+          out[p * width + int64_t(two) * (16 * kOut) + tile % kOut * 16 + n] = v;
+        }
+      };
+      auto walk = [&](Codes<F, kUnits> (&now)[2], Codes<F, kUnits> (&then)[2]) {
+        const bool last = round + 1 == sh.rounds;
+        const int next = last ? step + hop : step, next_round = last ? 0 : round + 1;
+        load(next, next_round, then);
+        compute(now);
+        if (last) finish();
+        step = next;
+        round = next_round;
+      };
+      while (step < end) {
+        walk(c[0], c[1]);
+        if (step >= end) break;
+        walk(c[1], c[0]);
+      }
     }
   }
 }
@@ -682,27 +706,24 @@ hipError_t allow_lds(const void* fn, int lds) {
                           : hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
 }
 
-// Items that the pairs can make: as many as experts have a pair, and one for each further `rows`.
-int most_items(int pairs, int experts, int rows) {
-  const int used = pairs < experts ? pairs : experts;
-  return used + (pairs - used) / rows;
-}
-
 template <class F, class X, bool GATE, int WAVES, int SETS>
 hipError_t launch_rows(const tq2_moe_experts_args& a, const Weight& w, const void* x, const Items& items, float* out,
                        int64_t n, int64_t k, hipStream_t stream) {
   const Shape s = shape_of<F>(a, n, k, WAVES, kUnits, int(n / (GATE ? 16 : 32)));
   const int lds = lds_bytes<F>(s.blocks, s.rows, WAVES);
-  const int down = s.few ? (s.by_pair ? s.pairs : s.experts) : most_items(s.pairs, s.experts, s.rows);
-  // Two blocks for each CU: the prologue (who, which rows, their conversion) is paid once, and an expert's steps are shared
-  // out evenly (64 tokens: 111 us with 512 blocks, 115 with 1024; 128 tokens, ternary: 188 and 225; one token, ternary: 30
-  // and 33).
-  int across = (512 + down - 1) / down;
-  if (across > s.steps) across = s.steps;
+  // As many blocks as the card holds at a time, two of 8 waves or one of 16 for each CU: the prologue (who, which rows,
+  // their conversion) is paid once, and steps are shared out evenly.
+  const int blocks = 256 * (16 / WAVES);
+  dim3 grid(blocks);
+  if (s.few) {
+    grid.y = s.by_pair ? s.pairs : s.experts;
+    grid.x = (512 + grid.y - 1) / grid.y;
+    if (grid.x > uint32_t(s.steps)) grid.x = s.steps;
+  }
   const auto fn = rows_kernel<F, X, GATE, WAVES, SETS>;
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(fn), lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fn, dim3(across, down), dim3(64 * WAVES), lds, stream, w,
+  hipLaunchKernelGGL(fn, grid, dim3(64 * WAVES), lds, stream, w,
                      static_cast<const typename X::elem*>(x), a.ids, items, a.weights, out, s);
   return hipGetLastError();
 }
