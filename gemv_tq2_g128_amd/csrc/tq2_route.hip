@@ -5,9 +5,9 @@
 // 32- and 16-bit operands are exact in f64.
 //
 // Scores, two forms.  dot_kernel: a wave for one expert and up to kDots tokens, on the vector ALUs; the weight is read
-// once, which is all there is to a few tokens.  tile_kernel: v_mfma_f64_16x16x4_f64 over 16 tokens by 16 experts, a
-// block's waves and further blocks sharing the hidden axis; its bound is the f64 rate (78.6 TFLOP/s, as the vector
-// ALUs', but with no conversion or operand read in its way).
+// once, which is all there is to a few tokens.  tile_kernel: v_mfma_f64_16x16x4_f64 over 16 tokens by 16 or 32 experts, a
+// block's waves and further blocks sharing the hidden axis; its bound is the f64 rate of the matrix cores (4099 tokens by 60
+// experts, K = 4096: 51 us, 39 TFLOP/s), no faster than the vector ALUs' but with no operand conversion in its way.
 // The order of a sum over the hidden axis is fixed by the sizes alone.
 //
 // Choice.  A wave for each token: f64 scores as unsigned keys of the same order, one maximum over the wave (DPP moves)
@@ -69,50 +69,73 @@ __global__ __launch_bounds__(64 * kDotWaves) void dot_kernel(const typename X::e
   }
 }
 
-constexpr int kTileWaves = 4;
+constexpr int kTileWaves = 8;
+constexpr int kMaxParts = 8;
 
-// scores f64 [parts, tokens, experts]; part blockIdx.z takes `span` of the hidden axis (a multiple of 32), its waves a
-// 32-wide step each in turn.  A lane holds eight neighbouring values of one row: lane group g's j-th is column
-// 8 g + j of the step, in both operands.
-template <class X, class W>
+// scores f64 [parts, tokens, experts] of 16 tokens by 16 TILES experts; part blockIdx.z takes `span` of the hidden axis (a
+// multiple of 32), its waves a 32-wide step each in turn.  A lane holds eight neighbouring values of one row: lane group
+// g's j-th is column 8 g + j of the step, in both operands.  Several tiles share the conversion of x to f64.
+template <class X, class W, int TILES>
 __global__ __launch_bounds__(64 * kTileWaves) void tile_kernel(const typename X::elem* __restrict__ x,
                                                                const typename W::elem* __restrict__ w, int tokens,
                                                                int experts, int hidden, int span,
                                                                double* __restrict__ scores) {
-  __shared__ double join[kTileWaves - 1][256];
+  __shared__ double join[kTileWaves][TILES * 256];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
-  const int t = blockIdx.y * 16 + r16, e = blockIdx.x * 16 + r16;
+  const int t0 = blockIdx.x * 16, e0 = blockIdx.y * 16 * TILES;
   // Rows past the end repeat the last one; their products are not stored.
-  const typename X::elem* xr = x + size_t(min(t, tokens - 1)) * hidden;
-  const typename W::elem* wr = w + size_t(min(e, experts - 1)) * hidden;
+  const typename X::elem* xr = x + size_t(min(t0 + r16, tokens - 1)) * hidden;
+  const typename W::elem* wr[TILES];
+#pragma unroll
+  for (int i = 0; i < TILES; ++i) wr[i] = w + size_t(min(e0 + i * 16 + r16, experts - 1)) * hidden;
   const int from = blockIdx.z * span, end = min(hidden, from + span);
-  f64x4_t acc = {0.0, 0.0, 0.0, 0.0};
-  for (int h0 = from + wave * 32; h0 < end; h0 += 32 * kTileWaves) {
-    const int h = h0 + g4 * 8;
-    float a[8] = {}, b[8] = {};
+  f64x4_t acc[TILES] = {};
+  float a[8] = {}, b[TILES][8] = {};
+  const auto load = [&](int h) {
     if (h < end) {
       load8<X>(xr + h, a);
-      load8<W>(wr + h, b);
+#pragma unroll
+      for (int i = 0; i < TILES; ++i) load8<W>(wr[i] + h, b[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        a[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) b[i][j] = 0.f;
+      }
     }
+  };
+  load(from + wave * 32 + g4 * 8);
+  for (int h0 = from + wave * 32; h0 < end; h0 += 32 * kTileWaves) {
+    float c[8], d[TILES][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      acc = __builtin_amdgcn_mfma_f64_16x16x4f64(double(a[j]), double(b[j]), acc, 0, 0, 0);
-  }
-  if (wave > 0) {
+    for (int j = 0; j < 8; ++j) {
+      c[j] = a[j];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) join[wave - 1][r * 64 + lane] = acc[r];
+      for (int i = 0; i < TILES; ++i) d[i][j] = b[i][j];
+    }
+    load(h0 + 32 * kTileWaves + g4 * 8);                // the next step's, under this one's products
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const double v = double(c[j]);
+#pragma unroll
+      for (int i = 0; i < TILES; ++i) acc[i] = __builtin_amdgcn_mfma_f64_16x16x4f64(v, double(d[i][j]), acc[i], 0, 0, 0);
+    }
   }
+#pragma unroll
+  for (int i = 0; i < TILES; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) join[wave][(i * 4 + r) * 64 + lane] = acc[i][r];
   __syncthreads();
-  if (wave > 0) return;
   double* out = scores + size_t(blockIdx.z) * tokens * experts;
+  for (int at = threadIdx.x; at < TILES * 256; at += 64 * kTileWaves) {
+    double v = 0.0;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    double v = acc[r];
-#pragma unroll
-    for (int i = 0; i < kTileWaves - 1; ++i) v += join[i][r * 64 + lane];
-    const int row = blockIdx.y * 16 + r * 4 + g4;      // lane group g holds rows g, 4 + g, 8 + g, 12 + g
-    if (row < tokens && e < experts) out[size_t(row) * experts + e] = v;
+    for (int i = 0; i < kTileWaves; ++i) v += join[i][at];
+    // Lane group g holds rows g, 4 + g, 8 + g, 12 + g.
+    const int t = t0 + (at >> 6 & 3) * 4 + (at >> 4 & 3), e = e0 + (at >> 8) * 16 + (at & 15);
+    if (t < tokens && e < experts) out[size_t(t) * experts + e] = v;
   }
 }
 
@@ -124,22 +147,18 @@ __device__ __forceinline__ uint64_t key_of(double v) {
 }
 
 template <int CTRL, int ROW_MASK>
-__device__ __forceinline__ uint64_t dpp_max(uint64_t v) {
-  const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(v), CTRL, ROW_MASK, 0xF, false);
-  const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(v >> 32), CTRL, ROW_MASK, 0xF, false);
-  const uint64_t o = uint64_t(hi) << 32 | lo;
-  return o > v ? o : v;
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  return max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, ROW_MASK, 0xF, false)));
 }
 
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   v = dpp_max<0xB1, 0xF>(v);
   v = dpp_max<0x4E, 0xF>(v);
   v = dpp_max<0x141, 0xF>(v);
   v = dpp_max<0x140, 0xF>(v);
   v = dpp_max<0x142, 0xA>(v);
   v = dpp_max<0x143, 0xC>(v);
-  const uint32_t lo = __builtin_amdgcn_readlane(int(v), 63), hi = __builtin_amdgcn_readlane(int(v >> 32), 63);
-  return uint64_t(hi) << 32 | lo;
+  return uint32_t(__builtin_amdgcn_readlane(int(v), 63));
 }
 
 constexpr int kChoiceWaves = 4;
@@ -163,8 +182,14 @@ __global__ __launch_bounds__(64 * kChoiceWaves) void choice_kernel(const double*
     const int e = lane + 64 * i;
     p[i] = low;
     if (e < experts) {
-      p[i] = scores[size_t(t) * experts + e];
-      for (int s = 1; s < parts; ++s) p[i] += scores[(size_t(s) * tokens + t) * experts + e];
+      // All parts are loaded at once; those that are not there count as zeros.
+      double part[kMaxParts];
+#pragma unroll
+      for (int s = 0; s < kMaxParts; ++s)
+        part[s] = s < parts ? scores[(size_t(s) * tokens + t) * experts + e] : 0.0;
+      p[i] = part[0];
+#pragma unroll
+      for (int s = 1; s < kMaxParts; ++s) p[i] += part[s];
     }
     key[i] = e < experts ? key_of(p[i]) : 0;
   }
@@ -198,10 +223,15 @@ __global__ __launch_bounds__(64 * kChoiceWaves) void choice_kernel(const double*
   double mine = 0.0, total = 0.0;                         // lane j keeps the j-th choice
   int id = 0;
   for (int j = 0; j < top_k; ++j) {
-    uint64_t best = key[0];
+    // The largest key, by its upper and then its lower half.
+    uint32_t upper = 0, lower = 0;
 #pragma unroll
-    for (int i = 1; i < NE; ++i) best = key[i] > best ? key[i] : best;
-    best = wave_max(best);
+    for (int i = 0; i < NE; ++i) upper = max(upper, uint32_t(key[i] >> 32));
+    upper = wave_max(upper);
+#pragma unroll
+    for (int i = 0; i < NE; ++i) lower = max(lower, uint32_t(key[i] >> 32) == upper ? uint32_t(key[i]) : 0);
+    lower = wave_max(lower);
+    const uint64_t best = uint64_t(upper) << 32 | lower;
     double chosen = 0.0;
     int at = -1;
 #pragma unroll
@@ -229,20 +259,44 @@ __global__ __launch_bounds__(64 * kChoiceWaves) void choice_kernel(const double*
 // Few tokens by the vector ALUs, from 9 on by tiles of 16.
 constexpr int64_t kDotTokens = 8;
 
+// Expert tiles of a block, and parts of the hidden axis.  Two tiles share x's conversion where that leaves a block for
+// each of the 256 CUs.  Parts: fewest rounds of blocks over the CUs, 3 hundredths of a round for each part's sums (4099
+// tokens by 60 experts, K = 4096, two tiles: 71 us in one part, 58 in four to six; 64 by 256, K = 7168, one tile: 32 in one,
+// 15 in four; 1024 by 128, K = 2048: 18 in one, 22 in six).
+struct Split {
+  int tiles, parts;
+};
+Split split_of(int64_t tokens, int64_t experts, int64_t hidden) {
+  const int64_t rows = (tokens + 15) / 16, two = rows * ((experts + 31) / 32), one = rows * ((experts + 15) / 16);
+  Split s = {two >= 256 ? 2 : 1, 1};
+  const int64_t blocks = s.tiles == 2 ? two : one;
+  const int64_t most = hidden / (32 * kTileWaves);       // at least a step for each wave
+  int64_t least = INT64_MAX;
+  for (int parts = 1; parts <= kMaxParts && (parts == 1 || parts <= most); ++parts) {
+    const int64_t cost = (blocks * parts + 255) / 256 * 100 / parts + 3 * parts;
+    if (cost < least) least = cost, s.parts = parts;
+  }
+  return s;
+}
+
 }  // namespace
 
 int route_parts(int64_t tokens, int64_t experts, int64_t hidden) {
-  if (tokens <= kDotTokens) return 1;
-  // Blocks for every CU, of at least two 32-wide steps a wave.
-  const int64_t tiles = ((tokens + 15) / 16) * ((experts + 15) / 16);
-  const int64_t most = hidden / (32 * kTileWaves * 2);
-  int64_t parts = 512 / tiles;
-  if (parts > most) parts = most;
-  if (parts > 8) parts = 8;
-  return parts < 1 ? 1 : int(parts);
+  return tokens <= kDotTokens ? 1 : split_of(tokens, experts, hidden).parts;
 }
 
 namespace {
+
+template <class X, class W, int TILES>
+hipError_t launch_tiles(const tq2_moe_route_args& a, int parts, hipStream_t stream) {
+  const int tokens = int(a.tokens), experts = int(a.experts), hidden = int(a.hidden);
+  const int span = ((hidden + parts - 1) / parts + 31) & ~31;
+  const dim3 grid((tokens + 15) / 16, (experts + 16 * TILES - 1) / (16 * TILES), parts);
+  hipLaunchKernelGGL((tile_kernel<X, W, TILES>), grid, dim3(64 * kTileWaves), 0, stream,
+                     static_cast<const typename X::elem*>(a.x), static_cast<const typename W::elem*>(a.weight), tokens,
+                     experts, hidden, span, static_cast<double*>(a.workspace));
+  return hipGetLastError();
+}
 
 template <class X, class W>
 hipError_t launch_scores(const tq2_moe_route_args& a, int parts, hipStream_t stream) {
@@ -254,10 +308,8 @@ hipError_t launch_scores(const tq2_moe_route_args& a, int parts, hipStream_t str
     const dim3 grid((experts + kDotWaves - 1) / kDotWaves, (tokens + kDots - 1) / kDots);
     hipLaunchKernelGGL((dot_kernel<X, W>), grid, dim3(64 * kDotWaves), 0, stream, x, w, tokens, experts, hidden, scores);
   } else {
-    const int span = ((hidden + parts - 1) / parts + 31) & ~31;
-    const dim3 grid((experts + 15) / 16, (tokens + 15) / 16, parts);
-    hipLaunchKernelGGL((tile_kernel<X, W>), grid, dim3(64 * kTileWaves), 0, stream, x, w, tokens, experts, hidden, span,
-                       scores);
+    return split_of(tokens, experts, hidden).tiles == 1 ? launch_tiles<X, W, 1>(a, parts, stream)
+                                                        : launch_tiles<X, W, 2>(a, parts, stream);
   }
   return hipGetLastError();
 }
