@@ -30,7 +30,6 @@ constexpr int kBins = 512;
 constexpr float kGrid = 11.f;              // bins of a factor of two: 2^46.5 over all, more than a weight's 43 bits
 constexpr int kMaxChunks = 64;
 constexpr int kThreads = 1024;             // of bins_kernel
-constexpr int kSmall = 1, kLarge = 4;      // 16-byte vectors of a thread: chunks of 4096 to 32768 logits
 constexpr int kRowThreads = 1024;          // of the choice
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr uint32_t kList = 4096;           // tokens of a bin that are held in LDS
@@ -256,6 +255,7 @@ __global__ __launch_bounds__(kThreads) void bins_kernel(Args a) {
   for (int i = 0; i < VECS; ++i)
 #pragma unroll
     for (int j = 0; j < kVec; ++j) top = fmaxf(top, Bits<T>::get(x[i], j));
+  const float mine = top;
   top = wave_max(top);
   if ((t & 63) == 0) part[t >> 6] = top;
   __syncthreads();
@@ -268,15 +268,40 @@ __global__ __launch_bounds__(kThreads) void bins_kernel(Args a) {
   // Each token's bin and its number there.  What min_p drops of a chunk by itself is no part of the row's either.
   constexpr uint32_t kDropped = ~0u;
   int cut = last_bin(min_p);
+  if (top_k > 0 && top_k <= kThreads / 2) {
+    // Nor is what lies below top_k threads' own largest tokens: a first cut by these, one a thread.
+    const int b = rule.bin(mine);
+    if (b < kBins) atomicAdd(&counts[b], 1u);
+    if (t == 0) last = cut;
+    __syncthreads();
+    const uint32_t own = t < kBins ? counts[t] : 0;
+    uint32_t upto = own, none = 0;
+    scan(upto, none, part_a, part_b);
+    if (t < kBins && upto >= uint32_t(top_k) && upto - own < uint32_t(top_k)) last = min(cut, t);
+    if (t < kBins) counts[t] = 0;
+    __syncthreads();
+    cut = last;
+  }
+  // A sieve by one bound, a little below the last bin's: (base - bin) / grid is off by a few 2^-24 of itself.
+  const float edge = (rule.base - float(cut)) / rule.grid;
+  const float from = fabsf(edge) < 3e38f ? edge - fabsf(edge) * 0x1p-20f : -__builtin_inff();
   const auto place = [&](float l) {
     const int b = rule.bin(l);
     return b <= cut ? uint32_t(b) << 16 | atomicAdd(&counts[b], 1u) : kDropped;
   };
   uint32_t code[VECS][kVec];
 #pragma unroll
-  for (int i = 0; i < VECS; ++i)
+  for (int i = 0; i < VECS; ++i) {
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      code[i][j] = kDropped;
+      any |= Bits<T>::get(x[i], j) >= from;
+    }
+    if (!__any(any)) continue;
 #pragma unroll
     for (int j = 0; j < kVec; ++j) code[i][j] = place(Bits<T>::get(x[i], j));
+  }
   const uint32_t code_single = loose >= 0 ? place(single) : kDropped;
   if (t == 0) last = cut;
   __syncthreads();
@@ -336,7 +361,7 @@ struct Shared {
   double factor[kMaxChunks];               // of a chunk's sums
   int32_t shift[kMaxChunks];               // from the row's bins to the chunk's; kBins: no chunk to look at
   uint32_t from[kMaxChunks], past[kMaxChunks];         // of a chunk's tokens at hand: the first in its order, where they end
-  uint64_t few_key[64], few_sum[64];
+  uint64_t few_key[kFew], few_sum[kFew];
   uint32_t few, count, upto;
   int bin;
   uint64_t before, inside, key, all;
@@ -347,6 +372,12 @@ struct Shared {
 struct Goal {
   uint32_t count;
   uint64_t sum;
+  // Sums of tokens weighed at the row's top may miss those of the chunks by their last units: no more than is there.
+  __device__ void cut(uint64_t all, uint32_t n) {
+    if (count) count = min(count, n);
+    else if (all == 0) count = 1;
+    else sum = sum < all ? sum : all;
+  }
   __device__ bool here(uint64_t upto, uint64_t own, uint32_t upto_n, uint32_t n) const {
     return count ? upto_n >= count && upto_n - n < count : upto >= sum && upto - own < sum;
   }
@@ -455,19 +486,19 @@ struct Choice {
       s.weights[i] = weight_of(k);
     });
     __syncthreads();
-    if (ordered) order();
+    if (ordered) count_order(s.list, s.weights, tokens);
   }
-  // Put the few tokens that are listed in order by counting.
-  __device__ void order() {
+  // Put at most kFew tokens in order by counting: key, weight, upto and rank of the thread's.
+  __device__ void count_order(const uint64_t* keys, const uint64_t* weights, uint32_t n) {
     const int t = threadIdx.x;
-    const uint32_t n = tokens, i = t >> 2;
-    key = i < n ? s.list[i] : 0;
-    weight = i < n ? s.weights[i] : 0;
+    const uint32_t i = t >> 2;
+    key = i < n ? keys[i] : 0;
+    weight = i < n ? weights[i] : 0;
     upto = 0, rank = 0;
     if (i < n) {
 #pragma unroll 4
       for (uint32_t j = t & 3; j < n; j += 4)
-        if (s.list[j] >= key) upto += s.weights[j], ++rank;
+        if (keys[j] >= key) upto += weights[j], ++rank;
 #pragma unroll
       for (int m = 1; m < 4; m *= 2)
         upto += __shfl_xor(static_cast<unsigned long long>(upto), m), rank += __shfl_xor(rank, m);
@@ -530,12 +561,11 @@ struct Choice {
     const uint64_t before = s.before, end = before + s.inside;
     const uint32_t before_n = s.count_before;
     open(bin);
-    // Sums of tokens weighed at the row's top may miss those of the chunks by their last units: goals are cut to what
-    // is there, and no more is kept than the bins hold, so that what is drawn lies in the kept run.
+    // No more is kept than the bins hold, so that what is drawn lies in the kept run.
     if (ordered) {
-      if (g.count) g.count = min(g.count - above_n, tokens);
-      else g.sum = g.sum - above < s.all ? g.sum - above : s.all;
-      if (g.sum == 0 && g.count == 0) g.count = 1;
+      if (g.count) g.count -= above_n;
+      else g.sum -= above;
+      g.cut(s.all, tokens);
       __syncthreads();
       if (uint32_t(t >> 2) < tokens && g.here(upto, weight, rank, 1)) s.key = key, s.before = upto;
       __syncthreads();
@@ -545,14 +575,9 @@ struct Choice {
     }
     if (g.count) g.count -= before_n;
     else g.sum -= before;
-    uint64_t lo = 0, hi = ~uint64_t(0), passed = 0, all = 0;
-    uint32_t n = 0;
-    each(bin, [&](uint64_t, uint64_t w) { all += w, ++n; });
-    total(all, n);
-    if (g.count) g.count = min(g.count, n);
-    else if (all == 0) g.count = 1;
-    else g.sum = g.sum < all ? g.sum : all;
-    while (n > 64) {
+    uint64_t lo = 0, hi = ~uint64_t(0), passed = 0;
+    uint32_t n = tokens;
+    while (n > kFew) {
       // The keys' range, then bins over it.
       uint64_t least = ~uint64_t(0), most = 0;
       each(bin, [&](uint64_t k, uint64_t) {
@@ -571,6 +596,7 @@ struct Choice {
       if (lane == 0) s.part_a[wave] = least, s.part_b[wave] = most;
       if (t < kBins) s.sums[t] = 0, s.counts[t] = 0;
       __syncthreads();
+#pragma unroll
       for (int w = 0; w < kRowWaves; ++w) {
         least = s.part_a[w] < least ? s.part_a[w] : least;
         most = s.part_b[w] > most ? s.part_b[w] : most;
@@ -588,6 +614,9 @@ struct Choice {
       uint64_t upto_b = part;
       uint32_t upto_n = part_n;
       scan(upto_b, upto_n, s.part_a, s.part_c);
+      if (t == kBins - 1) s.all = upto_b;
+      __syncthreads();
+      g.cut(s.all, n);
       if (t < kBins && g.here(upto_b, part, upto_n, part_n)) {
         s.bin = t;
         s.before = upto_b - part;
@@ -603,24 +632,19 @@ struct Choice {
       if (g.count) g.count -= s.count_before;
       else g.sum -= s.before;
     }
-    // At most 64: one wave puts them in order by counting.
+    // Few: put in order by counting.
     __syncthreads();
     if (t == 0) s.few = 0;
     __syncthreads();
     each(bin, [&](uint64_t k, uint64_t w) {
       if (k < lo || k > hi) return;
       const uint32_t at = atomicAdd(&s.few, 1u);
-      if (at < 64) s.few_key[at] = k, s.few_sum[at] = w;
+      if (at < kFew) s.few_key[at] = k, s.few_sum[at] = w;
     });
     __syncthreads();
-    if (wave == 0) {
-      const uint64_t k = lane < int(n) ? s.few_key[lane] : 0, w = lane < int(n) ? s.few_sum[lane] : 0;
-      uint64_t sum_k = 0;
-      uint32_t n_k = 0;
-      for (uint32_t j = 0; j < n; ++j)
-        if (s.few_key[j] >= k) sum_k += s.few_sum[j], ++n_k;
-      if (lane < int(n) && g.here(sum_k, w, n_k, 1)) s.key = k, s.before = sum_k;
-    }
+    count_order(s.few_key, s.few_sum, n);
+    g.cut(s.all, n);
+    if (uint32_t(t >> 2) < n && g.here(upto, weight, rank, 1)) s.key = key, s.before = upto;
     __syncthreads();
     const uint64_t got = before + passed + s.before;
     *through = got < end ? got : end;
@@ -718,28 +742,28 @@ __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
   }
 }
 
-// Chunks: small ones while they are few, for the blocks' number; large ones otherwise, for the bins' traffic.
+// Chunks of 1, 2 or 4 vectors a thread: small ones for the number of blocks, but at most 16, which the choice joins
+// (131,072 logits: 33 us with 32 chunks of one vector, 28 with 16 of two), and large ones once there are blocks enough.
 struct Chunks {
-  bool large;
-  int vecs, count, tokens;
+  int vecs, count, tokens;                 // vectors of a thread, chunks of a row, places of a chunk's order
 };
 Chunks chunks_of(int64_t rows, int64_t vocab, int64_t type) {
   const int64_t vec = type == TQ2_TYPE_F32 ? 4 : 8, vecs = vocab / vec;
-  const int64_t small = kThreads * kSmall, large = kThreads * kLarge;
-  const int64_t n = (vecs + small - 1) / small;
   Chunks c;
-  c.large = n > kMaxChunks || rows * n > 2048;
-  c.vecs = int(c.large ? large : small);
-  c.count = int((vecs + c.vecs - 1) / c.vecs);
+  for (c.vecs = 1; c.vecs < 4; c.vecs *= 2) {
+    const int64_t n = (vecs + kThreads * c.vecs - 1) / (kThreads * c.vecs);
+    if (n <= 16 && rows * n <= 2048) break;
+  }
+  c.count = int((vecs + kThreads * c.vecs - 1) / (kThreads * c.vecs));
   if (c.count < 1) c.count = 1;
-  c.tokens = int(c.vecs * vec + 16);
+  c.tokens = int(kThreads * c.vecs * vec + 16);
   return c;
 }
 
 template <class T>
-hipError_t launch(const Args& a, bool large, int64_t rows, hipStream_t stream) {
+hipError_t launch(const Args& a, int vecs, int64_t rows, hipStream_t stream) {
   const dim3 grid(a.chunks, uint32_t(rows));
-  const auto bins = large ? bins_kernel<T, kLarge> : bins_kernel<T, kSmall>;
+  const auto bins = vecs == 1 ? bins_kernel<T, 1> : vecs == 2 ? bins_kernel<T, 2> : bins_kernel<T, 4>;
   hipLaunchKernelGGL(bins, grid, dim3(kThreads), 0, stream, a);
   const auto fn = choice_kernel<T>;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
@@ -770,7 +794,7 @@ hipError_t launch_sample(const tq2_sample_args& q, hipStream_t stream) {
   a.top_k = int32_t(q.top_k < 0 ? 0 : q.top_k < TQ2_SAMPLE_MAX_VOCAB ? q.top_k : TQ2_SAMPLE_MAX_VOCAB);
   a.vocab = int32_t(q.vocab);
   a.chunks = chunks.count;
-  a.chunk_shift = __builtin_ctz(unsigned(chunks.vecs));
+  a.chunk_shift = __builtin_ctz(unsigned(kThreads * chunks.vecs));
   a.row_stride = q.row_stride;
   a.temperature = q.temperature;
   a.top_p = q.top_p;
@@ -781,9 +805,9 @@ hipError_t launch_sample(const tq2_sample_args& q, hipStream_t stream) {
   a.order = reinterpret_cast<uint16_t*>(a.counts + parts * kBins);
   a.chunk_tokens = chunks.tokens;
   a.tops = reinterpret_cast<float*>(a.order + parts * size_t(chunks.tokens));
-  if (q.logits_type == TQ2_TYPE_F32) return launch<F32>(a, chunks.large, q.rows, stream);
-  if (q.logits_type == TQ2_TYPE_F16) return launch<F16>(a, chunks.large, q.rows, stream);
-  return launch<BF16>(a, chunks.large, q.rows, stream);
+  if (q.logits_type == TQ2_TYPE_F32) return launch<F32>(a, chunks.vecs, q.rows, stream);
+  if (q.logits_type == TQ2_TYPE_F16) return launch<F16>(a, chunks.vecs, q.rows, stream);
+  return launch<BF16>(a, chunks.vecs, q.rows, stream);
 }
 
 }  // namespace tq2
