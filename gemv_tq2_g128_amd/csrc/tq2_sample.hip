@@ -316,7 +316,10 @@ __global__ __launch_bounds__(kThreads) void bins_kernel(Args a) {
   __syncthreads();
   cut = last;
   if (t == cut) all = upto;
-  // Weights, and the tokens by their bins.
+  __syncthreads();
+  // The tokens by their bins, and weights.  Where most were dropped the others are gone through as they are ordered, their
+  // logits read again; otherwise from the registers, a vector's exponentials side by side: each is one long chain.
+  const bool sparse = all * 4 <= uint32_t(kChunkTokens<T, VECS>);
   const int base = chunk == 0 ? 0 : r.head + chunk * (kThreads * VECS * kVec);
 #pragma unroll
   for (int i = 0; i < VECS; ++i) {
@@ -324,25 +327,35 @@ __global__ __launch_bounds__(kThreads) void bins_kernel(Args a) {
 #pragma unroll
     for (int j = 0; j < kVec; ++j) any |= int(code[i][j] >> 16) <= cut;
     if (!__any(any)) continue;
-    // The exponentials side by side: each is one long chain.
-    uint64_t w[kVec];
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) w[j] = rule.near_weight(Bits<T>::get(x[i], j));
     const int first = r.head + (chunk * (kThreads * VECS) + i * kThreads + t) * kVec - base;
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
       const int b = int(code[i][j] >> 16);
-      if (b > cut) continue;
-      atomicAdd(&sums[b], static_cast<unsigned long long>(w[j]));
-      order[starts[b] + (code[i][j] & 0xFFFFu)] = uint16_t(first + j);
+      if (b <= cut) order[starts[b] + (code[i][j] & 0xFFFFu)] = uint16_t(first + j);
+    }
+    if (sparse) continue;
+    uint64_t w[kVec];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) w[j] = rule.near_weight(Bits<T>::get(x[i], j));
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const int b = int(code[i][j] >> 16);
+      if (b <= cut) atomicAdd(&sums[b], static_cast<unsigned long long>(w[j]));
     }
   }
   if (int(code_single >> 16) <= cut) {
     const int b = int(code_single >> 16);
-    atomicAdd(&sums[b], static_cast<unsigned long long>(rule.near_weight(single)));
+    if (!sparse) atomicAdd(&sums[b], static_cast<unsigned long long>(rule.near_weight(single)));
     order[starts[b] + (code_single & 0xFFFFu)] = uint16_t(loose - base);
   }
   __syncthreads();
+  if (sparse) {
+    for (uint32_t i = t; i < all; i += kThreads) {
+      const float l = Bits<T>::one(r.p, base + order[i]);
+      atomicAdd(&sums[rule.bin(l)], static_cast<unsigned long long>(rule.near_weight(l)));
+    }
+    __syncthreads();
+  }
   if (t < kBins) {
     a.sums[at * kBins + t] = sums[t];
     a.counts[at * kBins + t] = t <= cut ? starts[t] << 16 | own : all << 16;
