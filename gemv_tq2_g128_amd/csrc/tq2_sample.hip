@@ -30,7 +30,7 @@ constexpr int kBins = 512;
 constexpr float kGrid = 11.f;              // bins of a factor of two: 2^46.5 over all, more than a weight's 43 bits
 constexpr int kMaxChunks = 64;
 constexpr int kThreads = 1024;             // of bins_kernel
-constexpr int kRowThreads = 1024;          // of the choice
+constexpr int kRowThreads = kBins;         // of the choice: a thread for each bin
 constexpr int kRowWaves = kRowThreads / 64;
 constexpr uint32_t kList = 4096;           // tokens of a bin that are held in LDS
 constexpr uint32_t kFew = kRowThreads / 4; // tokens that are put in order at once: four threads for each
@@ -431,7 +431,7 @@ struct Choice {
   const Rule& rule;
   const Row<T>& row;
   int index;                               // of the row
-  // Thread t's bin (t < kBins): sum and count, by itself and through it from the top.
+  // Thread t's bin: sum and count, by itself and through it from the top.
   uint64_t own, sum;
   uint32_t mine, count;
   // Bins whose tokens are at hand: listed if they fit, and in order if there are few.
@@ -453,7 +453,6 @@ struct Choice {
       const uint32_t at = c ? s.past[c - 1] : 0, n = s.past[c] - at, from = s.from[c];
       const uint16_t* order = a.order + (size_t(index) * a.chunks + c) * a.chunk_tokens + from;
       const int base = c == 0 ? 0 : row.head + (c << a.chunk_shift) * Bits<T>::kVec;
-#pragma unroll 4
       for (uint32_t i = lane; i < n; i += 64) {
         const int token = base + order[i];
         f(at + i, key_of(Bits<T>::one(row.p, token), token));
@@ -563,7 +562,7 @@ struct Choice {
   __device__ uint64_t find(Goal g, uint64_t* through) {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     __syncthreads();
-    if (t < kBins && g.here(sum, own, count, mine)) {
+    if (g.here(sum, own, count, mine)) {
       s.bin = t;
       s.before = sum - own;
       s.inside = own;
@@ -607,7 +606,8 @@ struct Choice {
       }
       __syncthreads();
       if (lane == 0) s.part_a[wave] = least, s.part_b[wave] = most;
-      if (t < kBins) s.sums[t] = 0, s.counts[t] = 0;
+      s.sums[t] = 0;
+      s.counts[t] = 0;
       __syncthreads();
 #pragma unroll
       for (int w = 0; w < kRowWaves; ++w) {
@@ -622,15 +622,15 @@ struct Choice {
         atomicAdd(&s.counts[b], 1u);
       });
       __syncthreads();
-      const uint64_t part = t < kBins ? s.sums[t] : 0;
-      const uint32_t part_n = t < kBins ? s.counts[t] : 0;
+      const uint64_t part = s.sums[t];
+      const uint32_t part_n = s.counts[t];
       uint64_t upto_b = part;
       uint32_t upto_n = part_n;
       scan(upto_b, upto_n, s.part_a, s.part_c);
       if (t == kBins - 1) s.all = upto_b;
       __syncthreads();
       g.cut(s.all, n);
-      if (t < kBins && g.here(upto_b, part, upto_n, part_n)) {
+      if (g.here(upto_b, part, upto_n, part_n)) {
         s.bin = t;
         s.before = upto_b - part;
         s.count_before = upto_n - part_n;
@@ -692,13 +692,12 @@ __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
     s.factor[t] = any ? rule.e(chunk_top) : 0.0;
   }
   __syncthreads();
-  // The row's bins: half of the threads join the even chunks, the others the odd ones.
+  // The thread's bin of the row, from all chunks.
   uint64_t own = 0;
   uint32_t mine = 0;
-  const int bin_of_thread = t & (kBins - 1);
-#pragma unroll 8
-  for (int c = t / kBins; c < a.chunks; c += kRowThreads / kBins) {
-    const int at = bin_of_thread - s.shift[c];
+#pragma unroll 4
+  for (int c = 0; c < a.chunks; ++c) {
+    const int at = t - s.shift[c];
     const size_t from = (first_chunk + c) * kBins + max(at, 0);
     const bool here = at >= 0;
     const uint64_t sum = here ? a.sums[from] : 0;
@@ -706,10 +705,6 @@ __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
     const double f = s.factor[c];
     own += f == 1.0 ? sum : uint64_t(double(sum) * f);
   }
-  if (t >= kBins) s.sums[bin_of_thread] = own, s.counts[bin_of_thread] = mine;
-  __syncthreads();
-  own = t < kBins ? own + s.sums[t] : 0;
-  mine = t < kBins ? mine + s.counts[t] : 0;
   uint64_t sum = own;
   uint32_t count = mine;
   scan(sum, count, s.part_a, s.part_c);
