@@ -106,10 +106,13 @@ size_t tq2_moe_experts_workspace_bytes(const tq2_moe_experts_args* args);
  * another.  TQ2_MOE_TERNARY: gate_up and down are the resident weights that
  * tq2_reformat_aos_to_soa gives for n = experts * 2 * inter rows of hidden and
  * n = experts * hidden rows of inter; the scales are NULL.
- * Accuracy: weights exact; x and the products between the projections as two
- * binary16 parts under a power of two per row and 128 columns, f32 sums: each
- * projection keeps the bounds of tq2_q4_gemv, the output is rounded once to its
- * type.  The order of all sums is fixed: a call repeats its results.
+ * Accuracy: weights exact; x and the rows between the projections as 31-bit
+ * integers under a power of two per row and 128 columns, products and their
+ * sums over a scale's columns exact, f32 beyond: each projection is within
+ * 1e-5 * sum_k |x w| + 2^-30 * sum_k X_k |w|, with X_k the largest |x| of k's 128
+ * columns (128 j .. 128 j + 127); the second term counts where a column far
+ * above the others meets weights of almost zero.  The output is rounded once
+ * to its type.  The order of all sums is fixed: a call repeats its results.
  * Only rows of x whose token chose an expert meet that expert's weights: a row
  * that is not finite reaches its own output alone.
  * x, residual, out, codes, scales, workspace: 16-byte aligned; ids and

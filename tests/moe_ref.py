@@ -34,6 +34,11 @@ def ternary_values(blocks, experts, n, k):
     return oracle.dequantize(blocks, experts * n, k).astype(np.float64).reshape(experts, n, k)
 
 
+def units(row):
+    """2^-30 of the largest of each 128 columns, for each column."""
+    return np.repeat(np.abs(row).reshape(-1, 128).max(1), 128) * 2.0 ** -30
+
+
 def silu(v):
     with np.errstate(over="ignore"):
         return v / (1 + np.exp(-v))
@@ -42,7 +47,8 @@ def silu(v):
 def experts(x, gate_up, down, ids, weights, residual, tol):
     """out, and how far a kernel may be from it whose projections keep tol * sum |x w|.
 
-    gate_up f64 [experts, 2 inter, hidden], down f64 [experts, hidden, inter].  silu's slope is below 1.1; its f32
+    gate_up f64 [experts, 2 inter, hidden], down f64 [experts, hidden, inter].  A projection keeps tol * sum |x w| and half
+    a unit of its 31-bit integers, 2^-30 of the largest of the row's 128 columns.  silu's slope is below 1.1; its f32
     exponential, quotient and product add 4 roundings, the weighted sum one for each place and two more."""
     x = x.astype(np.float64)
     out = np.zeros(x.shape) if residual is None else residual.astype(np.float64).copy()
@@ -52,14 +58,14 @@ def experts(x, gate_up, down, ids, weights, residual, tol):
         for j, e in enumerate(ids[t]):
             if not 0 <= e < gate_up.shape[0]:
                 continue
-            both, s = gate_up[e] @ x[t], np.abs(gate_up[e]) @ np.abs(x[t])
+            both, s = gate_up[e] @ x[t], np.abs(gate_up[e]) @ (np.abs(x[t]) + units(x[t]) / tol)
             g, u, dg, du = both[:inter], both[inter:], tol * s[:inter], tol * s[inter:]
             h = silu(g) * u
             dh = 1.1 * dg * (np.abs(u) + du) + np.abs(silu(g)) * du + 4 * step * np.abs(h)
             w = float(weights[t, j])
             out[t] += w * (down[e] @ h)
             reach = abs(w) * (np.abs(down[e]) @ np.abs(h))
-            bound[t] += abs(w) * (np.abs(down[e]) @ dh) * (1 + tol) + tol * reach
+            bound[t] += abs(w) * (np.abs(down[e]) @ (dh + units(h))) * (1 + tol) + tol * reach
             size[t] += reach
     return out, bound + (len(ids[0]) + 2) * step * size if len(ids) else bound
 

@@ -1,8 +1,8 @@
 """GPU tests of tq2_moe_experts against the definition in float64 (tests/moe_ref.py, which carries the bound).
 
-Each projection keeps 1e-5 * sum |x w| as the 4-bit products do (x = hi + lo within 2^-22, f32 sums of fewer than 150
-roundings of 2^-24); ternary weights have one scale for 128 columns and no other rounding.  A 16-bit output adds half a
-step of itself.
+Each projection keeps 1e-5 * sum |x w|: sums over a scale's columns are whole numbers, joined and scaled in four f32
+roundings of 2^-24, and a row meets fewer than 70 of them in a wave and 16 waves.  Beside that x is rounded to 31 bits.
+A 16-bit output adds half a step of itself.
 """
 
 import numpy as np
@@ -157,6 +157,32 @@ def test_scales_of_x_and_repetition(moe):
         y = c.run(moe)
         c.check(y)
         assert torch.equal(y, c.run(moe))
+
+
+@pytest.mark.parametrize("fmt,group", FORMATS)
+def test_a_column_far_above_the_others(moe, fmt, group):
+    # Columns of 1e6 among those of 1, one of them under weights of zero (codes 8 and 1 stand for zero).
+    c = Case(14, 3, 2, 2, 384, 256, fmt, group)
+    c.x[:, 70], c.x[1, 200] = 1e6, -1e6
+    c.up[:, :, 70] = 0
+    if fmt == "q4":
+        c.weights_on[0][0][:, :, 35] = c.weights_on[0][0][:, :, 35] & 0xF0 | 8
+    else:
+        from gemv_tq2_g128_amd import tq2
+        blocks = M.ternary_weight(np.random.default_rng(14), 2, 512, 384)     # the case's own, drawn first
+        fields = blocks.reshape(2, 512, 3, 34)
+        fields[:, :, 0, 70 // 4] = fields[:, :, 0, 70 // 4] & (0xFF - (3 << 2 * (70 % 4))) | 1 << 2 * (70 % 4)
+        c.weights_on[0] = tq2.reformat_aos_to_soa(torch.from_numpy(blocks).cuda(), 2 * 512, 384)
+    c.check(c.run(moe))
+
+
+@pytest.mark.parametrize("fmt", ["q4", "tq2"])
+def test_rows_of_zeros_and_tiny_values(moe, fmt):
+    c = Case(15, 4, 2, 3, 256, 256, fmt)
+    c.x[0], c.x[1, 128:], c.x[2] = 0, 0, c.x[2] * 1e-38
+    y = c.run(moe)
+    c.check(y)
+    assert bool((y[0] == 0).all())
 
 
 def test_graph_another_stream_and_caller_memory(moe):
