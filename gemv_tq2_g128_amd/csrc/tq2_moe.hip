@@ -345,9 +345,10 @@ struct Shape {
   int pairs, top_k, experts;
   uint32_t top_k_inverse;    // pair * top_k_inverse >> 16 is its token
   int rows;                  // of x in LDS at a time
-  int blocks;                // 128-wide blocks of K
+  int row_blocks;            // 128-wide blocks of K
+  int pieces, blocks;        // K in pieces of `blocks`, whose rows fit LDS; each piece's sums are rows of their own
   uint32_t blocks_inverse;   // i * blocks_inverse >> 20 is i / blocks
-  int units;                 // 64-byte pieces of a weight row
+  int units;                 // 64-byte units of a weight row in a piece
   int tiles;                 // column tiles of an expert (of gate, and as many of up): a multiple of 8
   int wk_shift;              // log2 of the parts of K
   int part_units, rounds, per;         // units of a part, its rounds, units of a round
@@ -397,7 +398,7 @@ __global__ __launch_bounds__(kItemThreads) void items_kernel(const int32_t* __re
 }
 
 // GATE: x are the tokens' rows, out the rows between the projections, f32 [pairs, 16 tiles].  Otherwise x are those
-// and out the weighted rows, f32 [pairs, 16 tiles].
+// and out the weighted rows, f32 [pieces, pairs, 16 tiles].
 template <class F, class X, bool GATE, int WAVES, int SETS>
 __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, const typename X::elem* __restrict__ x,
                                                              const int32_t* __restrict__ ids, Items items,
@@ -411,7 +412,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, cons
   const int r16 = lane & 15, g4 = lane >> 4;
   // Few pairs: the block has the steps blockIdx.x, blockIdx.x + gridDim.x, ... of its expert.  Otherwise a share of the
   // steps of all items, one after another, which may begin and end inside one.
-  int e = 0, found = 0, step = 0, hop, end = 0;
+  int e = 0, found = 0, step = 0, hop, end = 0, piece = sh.few ? blockIdx.z : 0;
   int64_t now_at = 0, stop_at = 0;                       // of all items' steps
   if (sh.few) {
     // The ids of all pairs, at most 64, are one load; every wave lists the expert's pairs for itself.
@@ -426,7 +427,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, cons
     hop = gridDim.x;
     end = sh.steps;
   } else {
-    const int64_t all = int64_t(*items.count) * sh.steps;
+    const int64_t all = int64_t(*items.count) * sh.pieces * sh.steps;
     now_at = all * blockIdx.x / gridDim.x;
     stop_at = all * (blockIdx.x + 1) / gridDim.x;
     if (now_at >= stop_at) return;
@@ -434,7 +435,12 @@ __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, cons
   }
   // The wave's part: two tiles of each step (gate and up, or neighbours), which share what is read of x, and units of K.
   const int slot = wave >> sh.wk_shift, part = wave & ((1 << sh.wk_shift) - 1);
-  const int unit0 = part * sh.part_units, mine = min(sh.part_units, sh.units - unit0);
+  const int unit0 = part * sh.part_units;
+  int blocks = 0, mine = 0;                              // of the piece, and the wave's units of it
+  auto take = [&]() {
+    blocks = min(sh.blocks, sh.row_blocks - piece * sh.blocks);
+    mine = min(sh.part_units, (blocks + F::kBlocks - 1) / F::kBlocks - unit0);
+  };
   const int per_step = WAVES >> sh.wk_shift, twos = GATE ? sh.tiles : sh.tiles / 2;
   const int64_t width = int64_t(sh.tiles) * 16;
   const uint32_t code_off = r16 * weight.row_bytes + g4 * 16, scale_off = r16 * weight.row_scales * 2;
@@ -447,14 +453,15 @@ __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, cons
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       load_codes<F, kUnits>(rows_at(weight, row0 + (GATE ? i * width : i * 16)), weight.row_bytes, code_off, scale_off,
-                            uint32_t(unit0 + round * sh.per), there ? min(sh.per, mine - round * sh.per) : 0, g4 * 16,
-                            into[i]);
+                            uint32_t(piece * sh.units + unit0 + round * sh.per),
+                            there ? min(sh.per, mine - round * sh.per) : 0, g4 * 16, into[i]);
   };
   int round = 0, begin = 0;
   for (bool more = true; more;) {
     if (!sh.few) {
       const int at = int(now_at / sh.steps);
-      const Item item = items.item[at];
+      const Item item = items.item[GATE ? at : at / sh.pieces];
+      piece = GATE ? 0 : at % sh.pieces;
       e = __builtin_amdgcn_readfirstlane(item.expert);
       found = __builtin_amdgcn_readfirstlane(item.count);
       begin = int(now_at - int64_t(at) * sh.steps);
@@ -463,11 +470,13 @@ __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, cons
       more = now_at < stop_at;
       step = begin;
       round = 0;
+      take();
       load(step, 0, c[0]);                               // in flight while x is converted
       __syncthreads();                                   // the last item's rows, sums and list have been read
       if (lane < found) list[lane] = items.order[item.first + lane];
     } else {
       begin = blockIdx.x;
+      take();
       load(step, 0, c[0]);
       more = false;
     }
@@ -485,7 +494,9 @@ __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, cons
       for (int i = threadIdx.x; i < m * sh.blocks * 16; i += kThreads) {
         const int row = int((uint32_t(i >> 4) * sh.blocks_inverse) >> 20), kb = (i >> 4) - row * sh.blocks;
         const uint32_t pair = list[first + row], from = GATE ? pair * sh.top_k_inverse >> 16 : pair;
-        stage8<F, X>(x + (int64_t(from) * sh.blocks + kb) * 128, i & 15, kb, row, m, cols, 1.f, rows);
+        if (kb < blocks)
+          stage8<F, X>(x + (int64_t(from) * sh.row_blocks + piece * sh.blocks + kb) * 128, i & 15, kb, row, m, cols, 1.f,
+                       rows);
       }
       __syncthreads();
       // The lane's operand columns and its group's rows; past the last row they repeat the first one's.
@@ -506,7 +517,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, cons
 #pragma unroll
           for (int b = 0; b < F::kBlocks; ++b) {
             const int kb = unit * F::kBlocks + b;
-            if (F::kBlocks > 1 && kb >= sh.blocks) continue;
+            if (F::kBlocks > 1 && kb >= blocks) continue;
             multiply<F, kUnits, 2, SETS>(from, j, b, kb, rows, g4, cols, at, own, m, acc);
           }
         }
@@ -536,7 +547,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, cons
             if (GATE) b += from[w * (2 * kRows * 16) + kRows * 16];
           }
           const float v = GATE ? a / (1.f + expf(-a)) * b : a * share[p];
-          out[p * width + int64_t(two) * (16 * kOut) + tile % kOut * 16 + n] = v;
+          out[(int64_t(piece) * sh.pairs + p) * width + int64_t(two) * (16 * kOut) + tile % kOut * 16 + n] = v;
         }
       };
       auto walk = [&](Codes<F, kUnits> (&now)[2], Codes<F, kUnits> (&then)[2]) {
@@ -638,48 +649,69 @@ __global__ __launch_bounds__(64 * kTokenWaves, 2) void token_kernel(Weight weigh
   }
 }
 
-// out[t] = residual[t] + the token's weighted rows in the order of their places; four columns a thread.
+// out[t] = residual[t] + the token's weighted rows in the order of their places and pieces; four columns a thread.
 template <class X>
 __global__ __launch_bounds__(256) void sum_kernel(const float* __restrict__ y, const int32_t* __restrict__ ids,
-                                                  const typename X::elem* residual, typename X::elem* out, int top_k,
-                                                  int experts, int hidden) {
+                                                  const typename X::elem* residual, typename X::elem* out, int pieces,
+                                                  int pairs, int top_k, int experts, int hidden) {
   const int n = (blockIdx.x * 256 + threadIdx.x) * 4, t = blockIdx.y;
   if (n >= hidden) return;
   f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
   for (int j = 0; j < top_k; ++j) {
     const int p = t * top_k + j;
-    if (uint32_t(ids[p]) < uint32_t(experts)) sum += load4(F32(), y + size_t(p) * hidden + n);
+    if (uint32_t(ids[p]) >= uint32_t(experts)) continue;
+    for (int i = 0; i < pieces; ++i) sum += load4(F32(), y + (size_t(i) * pairs + p) * hidden + n);
   }
   if (residual) sum += load4(X(), residual + size_t(t) * hidden + n);
   store4(X(), out + size_t(t) * hidden + n, sum);
 }
 
-// Rows of x at a time for both projections: no more than an expert can have, as many as LDS holds.
+// Blocks of each of `pieces` of a row, whole units.
+template <class F>
+int piece_blocks(int blocks, int pieces) {
+  const int units = (blocks + F::kBlocks - 1) / F::kBlocks, each = (units + pieces - 1) / pieces * F::kBlocks;
+  return each < blocks ? each : blocks;
+}
+
+// LDS of rows_kernel.
 template <class F>
 int lds_bytes(int blocks, int rows, int waves) {
   return x_bytes<F>(blocks, rows) + 2 * waves * (rows > 4 ? 8 : 4) * 64 + 128;          // sums of two tiles, the list
 }
+
+// Rows of x at a time: as many as LDS holds of the hidden axis.  A token hardly names an expert twice.  Four rows are one
+// matrix operand, enough for most experts of a batch that has up to two pairs for each.
 template <class F>
 int rows_at_once(const tq2_moe_experts_args& a) {
-  const int blocks = int((a.hidden > a.inter ? a.hidden : a.inter) / 128);
-  // A token hardly names an expert twice.  Four rows are one matrix operand, enough for most experts of a batch that has
-  // up to two pairs for each.
   int rows = a.tokens < kMaxRows ? int(a.tokens) : kMaxRows;
   if (rows > 4 && a.tokens * a.top_k <= 2 * a.experts) rows = 4;
-  while (lds_bytes<F>(blocks, rows, 16) > kLds) --rows;
+  while (lds_bytes<F>(int(a.hidden / 128), rows, 16) > kLds) --rows;
   return rows;
+}
+
+// Pieces of K for down, so that LDS holds as many rows of each as gate and up have: two or three rows at a time would read
+// an expert's weights again for every few tokens.
+template <class F>
+int pieces_of(const tq2_moe_experts_args& a) {
+  const int rows = rows_at_once<F>(a), blocks = int(a.inter / 128);
+  int pieces = 1;
+  while (lds_bytes<F>(piece_blocks<F>(blocks, pieces), rows, 16) > kLds) ++pieces;
+  const int each = piece_blocks<F>(blocks, pieces);
+  return (blocks + each - 1) / each;                     // no empty ones
 }
 
 // The launch for n columns and k of K: `waves` of a block share it, `units` of a row at a time.
 template <class F>
-Shape shape_of(const tq2_moe_experts_args& a, int64_t n, int64_t k, int waves, int units, int twos) {
+Shape shape_of(const tq2_moe_experts_args& a, int64_t n, int64_t k, int waves, int units, int twos, int pieces) {
   Shape s;
   s.pairs = int(a.tokens * a.top_k);
   s.top_k = int(a.top_k);
   s.experts = int(a.experts);
   s.top_k_inverse = uint32_t((65536 + a.top_k - 1) / a.top_k);
   s.rows = rows_at_once<F>(a);
-  s.blocks = int(k / 128);
+  s.row_blocks = int(k / 128);
+  s.blocks = piece_blocks<F>(s.row_blocks, pieces);
+  s.pieces = (s.row_blocks + s.blocks - 1) / s.blocks;
   s.blocks_inverse = uint32_t(((1 << 20) + s.blocks - 1) / s.blocks);
   s.units = (s.blocks + F::kBlocks - 1) / F::kBlocks;
   s.tiles = int(n / 16);
@@ -708,15 +740,15 @@ hipError_t allow_lds(const void* fn, int lds) {
 
 template <class F, class X, bool GATE, int WAVES, int SETS>
 hipError_t launch_rows(const tq2_moe_experts_args& a, const Weight& w, const void* x, const Items& items, float* out,
-                       int64_t n, int64_t k, hipStream_t stream) {
-  const Shape s = shape_of<F>(a, n, k, WAVES, kUnits, int(n / (GATE ? 16 : 32)));
+                       int64_t n, int64_t k, int pieces, hipStream_t stream) {
+  const Shape s = shape_of<F>(a, n, k, WAVES, kUnits, int(n / (GATE ? 16 : 32)), pieces);
   const int lds = lds_bytes<F>(s.blocks, s.rows, WAVES);
   // As many blocks as the card holds at a time, two of 8 waves or one of 16 for each CU: the prologue (who, which rows,
   // their conversion) is paid once, and steps are shared out evenly.
-  const int blocks = 256 * (16 / WAVES);
-  dim3 grid(blocks);
+  dim3 grid(256 * (16 / WAVES));
   if (s.few) {
     grid.y = s.by_pair ? s.pairs : s.experts;
+    grid.z = s.pieces;
     grid.x = (512 + grid.y - 1) / grid.y;
     if (grid.x > uint32_t(s.steps)) grid.x = s.steps;
   }
@@ -731,13 +763,13 @@ hipError_t launch_rows(const tq2_moe_experts_args& a, const Weight& w, const voi
 // Blocks of 8 waves where two of them share a CU's LDS, otherwise one of 16.
 template <class F, class X, bool GATE>
 hipError_t launch_rows(const tq2_moe_experts_args& a, const Weight& w, const void* x, const Items& items, float* out,
-                       int64_t n, int64_t k, hipStream_t stream) {
+                       int64_t n, int64_t k, int pieces, hipStream_t stream) {
   const int rows = rows_at_once<F>(a);
-  const bool two = 2 * lds_bytes<F>(int(k / 128), rows, 8) <= kLds;
-  if (rows <= 4) return two ? launch_rows<F, X, GATE, 8, 1>(a, w, x, items, out, n, k, stream)
-                            : launch_rows<F, X, GATE, 16, 1>(a, w, x, items, out, n, k, stream);
-  return two ? launch_rows<F, X, GATE, 8, 2>(a, w, x, items, out, n, k, stream)
-             : launch_rows<F, X, GATE, 16, 2>(a, w, x, items, out, n, k, stream);
+  const bool two = 2 * lds_bytes<F>(piece_blocks<F>(int(k / 128), pieces), rows, 8) <= kLds;
+  if (rows <= 4) return two ? launch_rows<F, X, GATE, 8, 1>(a, w, x, items, out, n, k, pieces, stream)
+                            : launch_rows<F, X, GATE, 16, 1>(a, w, x, items, out, n, k, pieces, stream);
+  return two ? launch_rows<F, X, GATE, 8, 2>(a, w, x, items, out, n, k, pieces, stream)
+             : launch_rows<F, X, GATE, 16, 2>(a, w, x, items, out, n, k, pieces, stream);
 }
 
 // LDS of token_kernel, whose blocks hold all of a token's rows.
@@ -746,7 +778,11 @@ int token_lds(const tq2_moe_experts_args& a) { return x_bytes<F>(int(a.top_k * (
 
 template <class F>
 bool by_token(const tq2_moe_experts_args& a) {
-  return a.tokens * a.top_k <= 32 && token_lds<F>(a) + kTokenWaves * 64 <= kLds;
+  // Against a second launch of 4 us: weights that several tokens share come from the caches again, up to 32 MB of them
+  // (8 tokens on two of 8 experts of 12 MB each: 141 us by tokens, 133 by experts; 4 on all of 8 of 0.8 MB: 16 and 20).
+  const int64_t pairs = a.tokens * a.top_k, twice = pairs > a.experts ? pairs - a.experts : 0;
+  return pairs <= 32 && twice * a.hidden * a.inter * (F::kBlocks == 2 ? 17 : 34) / 64 <= int64_t(32) << 20 &&
+         token_lds<F>(a) + kTokenWaves * 64 <= kLds;
 }
 
 template <class F>
@@ -778,12 +814,12 @@ hipError_t launch(const tq2_moe_experts_args& a, const MoePlan& plan, hipStream_
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  e = launch_rows<F, X, true>(a, up, a.x, items, h, a.inter, a.hidden, stream);
+  e = launch_rows<F, X, true>(a, up, a.x, items, h, a.inter, a.hidden, 1, stream);
   if (e != hipSuccess) return e;
   const auto* residual = static_cast<const typename X::elem*>(a.residual);
   auto* out = static_cast<typename X::elem*>(a.out);
   if (by_token<F>(a)) {
-    const Shape s = shape_of<F>(a, a.hidden, a.inter, 1, kTokenUnits, 1);
+    const Shape s = shape_of<F>(a, a.hidden, a.inter, 1, kTokenUnits, 1, 1);
     const auto fn = token_kernel<F, X>;
     e = allow_lds(reinterpret_cast<const void*>(fn), token_lds<F>(a));
     if (e != hipSuccess) return e;
@@ -791,10 +827,10 @@ hipError_t launch(const tq2_moe_experts_args& a, const MoePlan& plan, hipStream_
                        a.ids, a.weights, residual, out, s);
     return hipGetLastError();
   }
-  e = launch_rows<F, F32, false>(a, down, h, items, y, a.hidden, a.inter, stream);
+  e = launch_rows<F, F32, false>(a, down, h, items, y, a.hidden, a.inter, pieces_of<F>(a), stream);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(sum_kernel<X>, dim3((a.hidden + 1023) / 1024, a.tokens), dim3(256), 0, stream, y, a.ids, residual,
-                     out, int(a.top_k), int(a.experts), int(a.hidden));
+                     out, pieces_of<F>(a), int(a.tokens * a.top_k), int(a.top_k), int(a.experts), int(a.hidden));
   return hipGetLastError();
 }
 
@@ -808,10 +844,15 @@ hipError_t launch(const tq2_moe_experts_args& a, const MoePlan& plan, hipStream_
 }  // namespace
 
 MoePlan plan_moe(const tq2_moe_experts_args& a) {
+  const int pieces = a.format == TQ2_MOE_TERNARY ? pieces_of<Ternary>(a)
+                     : a.group == 32             ? pieces_of<Q4G32>(a)
+                     : a.group == 64             ? pieces_of<Q4G64>(a)
+                                                 : pieces_of<Q4G128>(a);
+  const size_t pairs = size_t(a.tokens) * size_t(a.top_k);
   MoePlan p;
-  p.y_offset = align256(size_t(a.tokens) * size_t(a.top_k) * size_t(a.inter) * 4);
-  p.items_offset = p.y_offset + align256(size_t(a.tokens) * size_t(a.top_k) * size_t(a.hidden) * 4);
-  p.workspace = p.items_offset + 16 + size_t(a.tokens) * size_t(a.top_k) * (sizeof(Item) + 2);
+  p.y_offset = align256(pairs * size_t(a.inter) * 4);
+  p.items_offset = p.y_offset + align256(pairs * size_t(pieces) * size_t(a.hidden) * 4);
+  p.workspace = p.items_offset + 16 + pairs * (sizeof(Item) + 2);
   return p;
 }
 
