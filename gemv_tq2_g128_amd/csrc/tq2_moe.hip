@@ -30,7 +30,7 @@ namespace {
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kTokenWaves = 8;                  // of a block of token_kernel
+constexpr int kTokenWaves = 16;                 // of a block of token_kernel
 constexpr int kMaxRows = 8;                     // rows of x that a block has at a time, four to a matrix operand
 constexpr int kUnits = 2;                       // 64-byte pieces that a wave of rows_kernel takes of each row at a time
 constexpr int kTokenUnits = 4;                  // and one of token_kernel
@@ -572,7 +572,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, cons
 // waves take rounds of units over all of the token's places in turn, and their sums meet in LDS.  An expert that several
 // tokens chose is read for each of them.
 template <class F, class X>
-__global__ __launch_bounds__(64 * kTokenWaves, 2) void token_kernel(Weight weight, const float* __restrict__ h,
+__global__ __launch_bounds__(64 * kTokenWaves) void token_kernel(Weight weight, const float* __restrict__ h,
                                                                     const int32_t* __restrict__ ids,
                                                                     const float* __restrict__ share,
                                                                     const typename X::elem* residual,
