@@ -16,7 +16,7 @@ int check_sizes(const tq2_sample_args& a) {
   if (!size_ok(a.rows, 0, TQ2_SAMPLE_MAX_ROWS) || !size_ok(a.vocab, 1, TQ2_SAMPLE_MAX_VOCAB)) return TQ2_ERR_INVALID;
   if (a.logits_type != TQ2_TYPE_F32 && a.logits_type != TQ2_TYPE_F16 && a.logits_type != TQ2_TYPE_BF16)
     return TQ2_ERR_INVALID;
-  if (a.rows > 1 && !size_ok(a.row_stride, a.vocab, int64_t(1) << 40)) return TQ2_ERR_INVALID;
+  if (a.rows > 1 && !size_ok(a.row_stride, 0, int64_t(1) << 40)) return TQ2_ERR_INVALID;
   return TQ2_OK;
 }
 

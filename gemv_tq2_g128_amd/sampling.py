@@ -33,7 +33,7 @@ def sample_workspace_bytes_ptr(args: bytes) -> int:
 
 
 def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, logprob=None):
-    """The next token of each row of logits [rows, vocab] (float32, float16 or bfloat16; rows may be strided), int32
+    """The next token of each row of logits [rows, vocab] (float32, float16 or bfloat16; rows may be strided, expanded or overlapping), int32
     [rows], by the random numbers ``u`` f32 [rows] in [0, 1).
 
     In falling order of the logits (the lowest index first among equals) the first ``top_k`` tokens are kept, of these

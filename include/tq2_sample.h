@@ -33,7 +33,7 @@ typedef struct tq2_sample_args {
   const float* min_ps;           /* f32 [rows] or NULL */
   int64_t rows;                  /* 0 .. TQ2_SAMPLE_MAX_ROWS */
   int64_t vocab;                 /* 1 .. TQ2_SAMPLE_MAX_VOCAB */
-  int64_t row_stride;            /* at least vocab, if rows > 1 */
+  int64_t row_stride;            /* 0 (one row for all) or more, if rows > 1 */
   int64_t logits_type;           /* TQ2_TYPE_F32, F16 or BF16 */
   int64_t top_k;
   double temperature;
@@ -58,13 +58,14 @@ size_t tq2_sample_workspace_bytes(const tq2_sample_args* args);
  * logprob is the token's log of e over step 3's sum.
  * A temperature that is not above zero takes the largest logit, the lowest
  * index among equals, with logprob 0.  Settings past their range act as the
- * nearest that is in it, NaN as none (u: 0).  Logits that are NaN count as -infinity,
- * which is never taken; a row of nothing else gives -1 and logprob -infinity;
- * +infinity shares all of e among its equals.
+ * nearest that is in it (temperatures below 1e-36 as 1e-36), NaN as none (u:
+ * 0).  Logits that are NaN count as -infinity, which is never taken; a row of
+ * nothing else gives -1 and logprob -infinity; +infinity shares all of e among
+ * its equals.
  * Accuracy: e in 64 bits, held in units of 2^-43 of the largest (tokens below
  * half a unit are never taken) and summed as whole numbers: the token does
- * not hang on any order, and differs from the real numbers' only where u lies
- * within about vocab * 2^-43 of a border.
+ * not hang on any order, and differs from the real numbers' only where u times
+ * the sum lies within about vocab * 2^-43 of a border.
  * logits: aligned to their type; u, ids, logprob and settings: 4-byte aligned.
  * rows == 0 is a no-op.  Errors: INVALID (null pointer, size or type out of
  * range, a scalar setting that is NaN, a negative temperature, a workspace that

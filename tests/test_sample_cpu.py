@@ -50,7 +50,7 @@ def test_header_and_binding_agree():
 
 @pytest.mark.parametrize("over", [dict(logits=0), dict(u=0), dict(ids=0), dict(workspace=0), dict(rows=-1),
                                   dict(rows=4097), dict(vocab=0), dict(vocab=-5), dict(vocab=(1 << 20) + 1),
-                                  dict(row_stride=999), dict(row_stride=-1024), dict(row_stride=(1 << 40) + 1),
+                                  dict(row_stride=-1), dict(row_stride=-1024), dict(row_stride=(1 << 40) + 1),
                                   dict(logits_type=3), dict(logits_type=-1), dict(workspace_bytes=0),
                                   dict(workspace_bytes=-1), dict(temperatures=0, temperature=-0.5),
                                   dict(temperatures=0, temperature=NAN), dict(top_ps=0, top_p=NAN),
