@@ -57,20 +57,21 @@ struct Args {
   int32_t chunk_tokens;
 };
 
-// Element types by their bits, f32 by f32.
+// Element types by their bits, f32 by f32.  kNone, a NaN, fills places past the row: it has no bin at any temperature,
+// where -infinity times a large enough grid shares one with finite logits.
 template <class T>
 struct Bits;
 template <>
 struct Bits<F32> {
   static constexpr int kVec = 4;
-  static constexpr uint32_t kNone = 0xFF800000u;                     // -infinity
+  static constexpr uint32_t kNone = 0x7FC00000u;
   static __device__ float get(u32x4_t v, int i) { return __builtin_bit_cast(float, uint32_t(v[i])); }
   static __device__ float one(const void* p, int i) { return static_cast<const float*>(p)[i]; }
 };
 template <>
 struct Bits<F16> {
   static constexpr int kVec = 8;
-  static constexpr uint32_t kNone = 0xFC00FC00u;
+  static constexpr uint32_t kNone = 0x7E007E00u;
   static __device__ float get(u32x4_t v, int i) {
     const uint32_t w = v[i >> 1];
     return float(__builtin_bit_cast(_Float16, uint16_t(i & 1 ? w >> 16 : w)));
@@ -80,7 +81,7 @@ struct Bits<F16> {
 template <>
 struct Bits<BF16> {
   static constexpr int kVec = 8;
-  static constexpr uint32_t kNone = 0xFF80FF80u;
+  static constexpr uint32_t kNone = 0x7FC07FC0u;
   static __device__ float get(u32x4_t v, int i) {
     const uint32_t w = v[i >> 1];
     return __builtin_bit_cast(float, i & 1 ? w & 0xFFFF0000u : w << 16);
@@ -127,7 +128,7 @@ struct Rule {
     const double heat = a.temperatures ? double(a.temperatures[row]) : a.temperature;
     greedy = !(heat > 0.0);                // the first of the order, at any temperature
     rate = 1.4426950408889634 / (greedy ? 1.0 : fmax(heat, kCoolest));
-    grid = kGrid * float(rate);
+    grid = fmaxf(kGrid * float(rate), 0x1p-126f);       // at an infinite temperature too
   }
   __device__ void set_top(float l) {
     top = l;
@@ -271,7 +272,7 @@ __global__ __launch_bounds__(kThreads) void bins_kernel(Args a) {
   if (top_k > 0 && top_k <= kThreads / 2) {
     // Nor is what lies below top_k threads' own largest tokens: a first cut by these, one a thread.
     const int b = rule.bin(mine);
-    if (b < kBins) atomicAdd(&counts[b], 1u);
+    if (b < kBins && mine > -__builtin_inff()) atomicAdd(&counts[b], 1u);
     if (t == 0) last = cut;
     __syncthreads();
     const uint32_t own = t < kBins ? counts[t] : 0;
@@ -282,12 +283,13 @@ __global__ __launch_bounds__(kThreads) void bins_kernel(Args a) {
     __syncthreads();
     cut = last;
   }
-  // A sieve by one bound, a little below the last bin's: (base - bin) / grid is off by a few 2^-24 of itself.
+  // A sieve by one bound, a little below the last bin's: (base - bin) / grid is off by a few 2^-24 of itself,
+  // or by half of the least subnormal.
   const float edge = (rule.base - float(cut)) / rule.grid;
-  const float from = fabsf(edge) < 3e38f ? edge - fabsf(edge) * 0x1p-20f : -__builtin_inff();
+  const float from = fabsf(edge) < 3e38f ? edge - fabsf(edge) * 0x1p-20f - 0x1p-146f : -__builtin_inff();
   const auto place = [&](float l) {
     const int b = rule.bin(l);
-    return b <= cut ? uint32_t(b) << 16 | atomicAdd(&counts[b], 1u) : kDropped;
+    return b <= cut && l > -__builtin_inff() ? uint32_t(b) << 16 | atomicAdd(&counts[b], 1u) : kDropped;
   };
   uint32_t code[VECS][kVec];
 #pragma unroll

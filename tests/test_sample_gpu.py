@@ -167,6 +167,81 @@ def test_strided_rows_at_any_place(sampling, kind, offset):
     assert torch.equal(sampling.sample(view, u.cuda(), top_p=0.9), want)
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("temperature", [1e-38, 1e-30, 1e-3, 1.0, 1e30, float("inf")])
+def test_rows_of_the_lowest_values_at_any_temperature(sampling, kind, temperature):
+    # Logits times the grid of bins pass the largest f32, or all fall into one bin; around the rows lies +infinity.
+    low, rows, vocab = torch.finfo(TYPES[kind]).min, 6, 1003
+    logits = torch.full((rows, vocab), low, dtype=TYPES[kind])
+    logits[1, ::3] = -float("inf")
+    logits[2, 500] = low / 2
+    logits[3, 700:] = low / 2
+    logits[4] = -torch.arange(vocab).to(TYPES[kind]) - 30
+    logits[5, 77] = float("inf")
+    u = (torch.arange(rows) * 2 + 1).float() / 13
+    around = torch.full((rows, 3 * vocab), float("inf"), dtype=TYPES[kind], device="cuda")
+    around[:, vocab:2 * vocab] = logits.cuda()
+    heat = torch.full((rows,), temperature)
+    for settings in (dict(), dict(top_k=40), dict(top_k=600), dict(top_p=0.7), dict(min_p=0.2)):
+        want = check(sampling, logits, u, heat, **settings)
+        assert torch.equal(sampling.sample(around[:, vocab:2 * vocab], u.cuda(), heat.cuda(), **settings), want)
+
+
+def test_subnormal_logits(sampling):
+    tiny = torch.arange(900).float().repeat(3, 1) * 2.0 ** -149
+    u = torch.tensor([0.11, 0.52, 0.93])
+    check(sampling, tiny, u)
+    check(sampling, tiny, u, top_k=300)
+    check(sampling, tiny, u, temperature=1e-36, min_p=0.5)
+
+
+def test_one_row_for_many_draws(sampling):
+    # Rows of stride 0, and of windows that overlap.
+    logits, _ = logits_of(11, 1, 5000)
+    u = (torch.arange(64) + 0.37).float() / 64
+    want = check(sampling, logits.repeat(64, 1), u, top_p=0.9)
+    assert torch.equal(sampling.sample(logits.cuda().expand(64, 5000), u.cuda(), top_p=0.9), want)
+    windows = logits[0].as_strided((64, 4000), (13, 1))
+    want = check(sampling, windows, u)
+    assert torch.equal(sampling.sample(logits[0].cuda().as_strided((64, 4000), (13, 1)), u.cuda()), want)
+
+
+@pytest.mark.parametrize("rows,vocab", [
+    (3, 4096), (3, 8191), (3, 8193), (2, 16384), (2, 16390), (2, 32769), (2, 65541), (2, 131075), (300, 32775),
+    (140, 65536), (140, 131079)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("offset", [0, 1, 5, 7])
+def test_borders_of_chunks(sampling, rows, vocab, kind, offset):
+    # A few distinct rows, at places from which chunks and vectors start differently; some are drawn among the last tokens.
+    few = 3
+    logits, u = logits_of(12, few, vocab, kind, spread=1.0, sure=3.0)
+    logits[1, -3:] = 6.0
+    logits[2, :2] = 6.0
+    wide = torch.full((rows * (vocab + 3) + 8,), float("inf"), dtype=TYPES[kind], device="cuda")
+    view = wide.as_strided((rows, vocab), (vocab + 3, 1), offset)
+    view.copy_(logits.cuda()[torch.arange(rows, device="cuda") % few])
+    us = u.repeat(rows // few + 1)[:rows].cuda()
+    for settings in (dict(), dict(top_k=300), dict(top_p=0.8, top_k=vocab // 2)):
+        want = check(sampling, logits, u, **settings)
+        got = sampling.sample(view, us, **settings)
+        assert torch.equal(got, want.repeat(rows // few + 1)[:rows])
+
+
+def test_two_calls_at_once(sampling):
+    logits, u = (t.cuda() for t in logits_of(13, 32, 50000, "f16"))
+    want = [sampling.sample(logits, u, top_p=p) for p in (0.5, 0.95)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(sampling.sample(logits, u, top_p=(0.5, 0.95)[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+
+
 def test_graph_another_stream_and_caller_memory(sampling):
     logits, u = (t.cuda() for t in logits_of(9, 16, 32000, "bf16"))
     out, lp = torch.empty(16, dtype=torch.int32, device="cuda"), torch.empty(16, device="cuda")
