@@ -118,6 +118,39 @@ def test_the_same_expert_twice_and_no_expert(moe, fmt, group):
             assert torch.equal(y[2].cpu(), still)
 
 
+@pytest.mark.parametrize("fmt,group", FORMATS)
+@pytest.mark.parametrize("residual", [False, True])
+def test_many_pairs_with_none_twice_and_beyond(moe, fmt, group, residual):
+    # More than 64 pairs, which are sorted by their expert.
+    rng = np.random.default_rng(16)
+    ids = rng.integers(-2, 13, (50, 4))                  # 11 experts; -2, -1, 11 and 12 are none
+    ids[3] = [5, 5, 5, 5]
+    ids[7] = [-1, 11, -2 ** 31, 2 ** 31 - 1]
+    ids[20:45, 0] = 2
+    c = Case(17, 50, 4, 11, 384, 256, fmt, group, residual=residual, ids=ids)
+    y = c.run(moe)
+    c.check(y)
+    assert torch.equal(y[7].cpu(), c.residual[7] if residual else torch.zeros(384))
+    none = c.run(moe, ids=torch.full((50, 4), -1, dtype=torch.int32, device="cuda"))
+    assert torch.equal(none.cpu(), c.residual if residual else torch.zeros(50, 384))
+
+
+def test_two_calls_at_once(moe):
+    for tokens in (3, 40):
+        cases = [Case(18 + i, tokens, 4, 16, 512, 384, "tq2", act="bf16") for i in range(2)]
+        on = [dict(x=c.x.cuda(), ids=c.ids.cuda(), weights=c.share.cuda()) for c in cases]
+        want = [c.run(moe, **t) for c, t in zip(cases, on)]
+        torch.cuda.synchronize()
+        streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+        for _ in range(8):
+            for i, stream in enumerate(streams):
+                with torch.cuda.stream(stream):
+                    got[i].append(cases[i].run(moe, **on[i]))
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert all(torch.equal(g, want[i]) for g in got[i])
+
+
 def test_most_tokens_and_places(moe):
     c = Case(6, 128, 16, 48, 128, 128)
     c.check(c.run(moe))
