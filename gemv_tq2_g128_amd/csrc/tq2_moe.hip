@@ -261,32 +261,39 @@ __device__ __forceinline__ void stage8(const typename X::elem* __restrict__ bloc
     r.backs[kb * m + row] = top >= 0x7F800000 ? __builtin_nanf("") : __builtin_ldexpf(1.0f, -up) * share;
 }
 
+// Bytes from a step's operands to lane group g4's of a column.
+template <class F>
+__device__ __forceinline__ int operand_at(int g4, int cols, int column) {
+  return (g4 * cols + column) * (F::kGroup == 32 ? 8 : 16);
+}
+
 // Block b of unit j (b < F::kBlocks) of TILES times 16 weight rows against SETS times four rows of x: lane group g4 adds
-// row 4 set + g4's product with weight row r16 to acc[tile][set].  at: the lane's operand columns; row: its group's rows.
+// row 4 set + g4's product with weight row r16 to acc[tile][set].  at: the bytes from a step's operands to the lane's; row:
+// its group's rows.  All other terms of the addresses are the wave's own.
 template <class F, int N, int TILES, int SETS>
-__device__ __forceinline__ void multiply(const Codes<F, N> (&c)[TILES], int j, int b, int kb, const Rows31& x, int g4,
-                                         int cols, const int (&at)[SETS], const int (&row)[SETS], int m,
+__device__ __forceinline__ void multiply(const Codes<F, N> (&c)[TILES], int j, int b, int kb, const Rows31& x, int cols,
+                                         const int (&at)[SETS], const int (&row)[SETS], int m,
                                          float (&acc)[TILES][SETS]) {
   constexpr int kWide = F::kGroup == 32 ? 8 : 16;
   float back[SETS];
 #pragma unroll
-  for (int q = 0; q < SETS; ++q) back[q] = x.backs[kb * m + row[q]];
+  for (int q = 0; q < SETS; ++q) back[q] = (x.backs + kb * m)[row[q]];
 #pragma unroll
   for (int g = 0; g < kGroups<F>; ++g) {
     i32x4_t sum[TILES][SETS];
 #pragma unroll
     for (int q = 0; q < SETS; ++q) {
-      sum[0][q] = x.starts[(kb * kGroups<F> + g) * m + row[q]];
+      sum[0][q] = (x.starts + (kb * kGroups<F> + g) * m)[row[q]];
 #pragma unroll
       for (int t = 1; t < TILES; ++t) sum[t][q] = sum[0][q];
     }
 #pragma unroll
     for (int s = g * kSteps<F> / kGroups<F>; s < (g + 1) * kSteps<F> / kGroups<F>; ++s) {
-      const char* operand = x.operands + (size_t(kb * kSteps<F> + s) * 4 + g4) * cols * kWide;
+      const char* operand = x.operands + (kb * kSteps<F> + s) * 4 * cols * kWide;
       if constexpr (F::kGroup == 32) {
         long a[SETS];
 #pragma unroll
-        for (int q = 0; q < SETS; ++q) a[q] = *reinterpret_cast<const long*>(operand + at[q] * kWide);
+        for (int q = 0; q < SETS; ++q) a[q] = *reinterpret_cast<const long*>(operand + at[q]);
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
           const uint32_t w = c[t].w[j][s];
@@ -298,7 +305,7 @@ __device__ __forceinline__ void multiply(const Codes<F, N> (&c)[TILES], int j, i
       } else {
         i32x4_t a[SETS];
 #pragma unroll
-        for (int q = 0; q < SETS; ++q) a[q] = *reinterpret_cast<const i32x4_t*>(operand + at[q] * kWide);
+        for (int q = 0; q < SETS; ++q) a[q] = *reinterpret_cast<const i32x4_t*>(operand + at[q]);
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
           u32x4_t codes;
@@ -428,8 +435,11 @@ __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, cons
     end = sh.steps;
   } else {
     const int64_t all = int64_t(*items.count) * sh.pieces * sh.steps;
-    now_at = all * blockIdx.x / gridDim.x;
-    stop_at = all * (blockIdx.x + 1) / gridDim.x;
+    // Blocks go round the dies by number: neighbouring shares are one die's, whose L2 then has an expert's weights for
+    // its second item too (128 tokens, ternary: 165 us with shares in the blocks' order, 159 so).
+    const int per_die = gridDim.x / 8, block = (blockIdx.x & 7) * per_die + (blockIdx.x >> 3);
+    now_at = all * block / gridDim.x;
+    stop_at = all * (block + 1) / gridDim.x;
     if (now_at >= stop_at) return;
     hop = 1;
   }
@@ -503,7 +513,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, cons
       int at[SETS], own[SETS];
 #pragma unroll
       for (int q = 0; q < SETS; ++q) {
-        at[q] = q * 4 + (r16 >> 2) < m ? q * 16 + r16 : r16 & 3;
+        at[q] = operand_at<F>(g4, cols, q * 4 + (r16 >> 2) < m ? q * 16 + r16 : r16 & 3);
         own[q] = q * 4 + g4 < m ? q * 4 + g4 : 0;
       }
       float acc[2][SETS] = {};
@@ -518,7 +528,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void rows_kernel(Weight weight, cons
           for (int b = 0; b < F::kBlocks; ++b) {
             const int kb = unit * F::kBlocks + b;
             if (F::kBlocks > 1 && kb >= blocks) continue;
-            multiply<F, kUnits, 2, SETS>(from, j, b, kb, rows, g4, cols, at, own, m, acc);
+            multiply<F, kUnits, 2, SETS>(from, j, b, kb, rows, cols, at, own, m, acc);
           }
         }
       };
@@ -613,7 +623,7 @@ __global__ __launch_bounds__(64 * kTokenWaves) void token_kernel(Weight weight, 
     stage8<F, F32>(h + (int64_t(t) * all_blocks + kb) * 128, i & 15, kb, 0, 1, cols, __shfl(part, j), rows);
   }
   __syncthreads();
-  const int at[1] = {r16 & 3}, own[1] = {0};
+  const int at[1] = {operand_at<F>(g4, cols, r16 & 3)}, own[1] = {0};
   float acc[1][1] = {};
   auto compute = [&](Codes<F, kTokenUnits> (&from)[1], const At& a) {
 #pragma unroll
@@ -624,7 +634,7 @@ __global__ __launch_bounds__(64 * kTokenWaves) void token_kernel(Weight weight, 
       for (int b = 0; b < F::kBlocks; ++b) {
         const int k = (a.unit + j) * F::kBlocks + b;
         if (F::kBlocks > 1 && k >= sh.blocks) continue;
-        multiply<F, kTokenUnits, 1, 1>(from, j, b, a.place * sh.blocks + k, rows, g4, cols, at, own, 1, acc);
+        multiply<F, kTokenUnits, 1, 1>(from, j, b, a.place * sh.blocks + k, rows, cols, at, own, 1, acc);
       }
     }
   };
@@ -717,13 +727,16 @@ Shape shape_of(const tq2_moe_experts_args& a, int64_t n, int64_t k, int waves, i
   s.tiles = int(n / 16);
   s.few = s.pairs <= 64;
   s.by_pair = s.pairs < s.experts;
-  // Parts of K that take the fewest rounds of all waves; among equals the most parts, whose blocks are the most.
+  // Parts of K that take the fewest rounds of all waves; among equals the most parts, whose steps are shared out most
+  // evenly.  Where blocks walk over many steps, one of a single round pays an eighth more for meeting in LDS (64 tokens on
+  // 128 experts of 768: 102 us with single rounds, 99 with two; on 64 of 1408: 110 and 107).
   int64_t best = INT64_MAX;
   for (int shift = 0; (1 << shift) <= waves; ++shift) {
     const int part = (s.units + (1 << shift) - 1) >> shift, rounds = (part + units - 1) / units;
     const int per_step = waves >> shift, steps = (twos + per_step - 1) / per_step;
-    if (int64_t(rounds) * steps > best) continue;
-    best = int64_t(rounds) * steps;
+    const int64_t cost = int64_t(steps) * (rounds == 1 && !s.few ? 9 : 8 * rounds);
+    if (cost > best) continue;
+    best = cost;
     s.wk_shift = shift;
     s.part_units = part;
     s.rounds = rounds;
