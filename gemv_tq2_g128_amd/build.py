@@ -45,19 +45,23 @@ PROBE_LIB_NAME = "libtq2_probe.so"
 PROBE_SOURCES = ["tq2_probe.hip"]
 BINDING_NAME = "_binding.so"
 BINDING_SOURCE = "tq2_binding.cpp"
+DECODE_NAME = "_decode.so"
+DECODE_SOURCE = "tq2_decode.cpp"
 
 
 def build(verbose: bool = False) -> str:
     """Compile every HIP source into ``libtq2.so`` (and the benchmark's
     reference kernels into ``libtq2_probe.so``); returns the library path.
     Where PyTorch is installed, the tensor marshalling of ``attn`` and ``q4``
-    is compiled into ``_binding.so`` as well; the C ABI does without it."""
+    is compiled into ``_binding.so`` and that of ``moe`` and ``sampling`` into
+    ``_decode.so`` as well; the C ABI does without them."""
     _compile(PROBE_SOURCES, PROBE_LIB_NAME, verbose)
     lib = _compile(SOURCES, LIB_NAME, verbose)
     if importlib.util.find_spec("torch") is not None:
         _compile_binding(verbose)
+        _compile_module(DECODE_NAME, DECODE_SOURCE, verbose)
     else:
-        print("PyTorch is not installed: %s is left out" % BINDING_NAME, flush=True)
+        print("PyTorch is not installed: %s and %s are left out" % (BINDING_NAME, DECODE_NAME), flush=True)
     return lib
 
 
@@ -68,17 +72,21 @@ def host_compiler():
 
 
 def _compile_binding(verbose):
-    """The host-only Python module, against PyTorch's headers and libtq2.so."""
+    _compile_module(BINDING_NAME, BINDING_SOURCE, verbose)
+
+
+def _compile_module(name, source, verbose):
+    """A host-only Python module, against PyTorch's headers and libtq2.so."""
     import torch
     root = os.path.dirname(torch.__file__)
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
-    out = os.path.join(PKG_DIR, BINDING_NAME)
+    out = os.path.join(PKG_DIR, name)
     tmp = out + ".tmp%d" % os.getpid()
     includes = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                 os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]
     _run([host_compiler(), "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
-          *("-I" + i for i in includes), os.path.join(CSRC, BINDING_SOURCE), "-o", tmp,
+          *("-I" + i for i in includes), os.path.join(CSRC, source), "-o", tmp,
           "-L" + PKG_DIR, "-l:" + LIB_NAME, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu",
           "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"], verbose)
     os.replace(tmp, out)

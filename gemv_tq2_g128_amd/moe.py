@@ -7,7 +7,7 @@
   another.
 
 ``gate_up`` has n = 2 * inter rows for each expert, its gate rows first, and ``down`` n = hidden.  Argument marshalling
-only, as in ``tq2``: tensors go through the compiled module ``_binding`` (csrc/tq2_binding.cpp), raw pointers through ctypes.
+only, as in ``tq2``: tensors go through the compiled module ``_decode`` (csrc/tq2_decode.cpp), raw pointers through ctypes.
 """
 
 from __future__ import annotations
@@ -15,8 +15,8 @@ from __future__ import annotations
 import ctypes
 import struct
 
-from .tq2 import _result, lib     # first: it loads torch and libtq2, which _binding needs
-from . import _binding            # isort: skip
+from .tq2 import _result, lib     # first: it loads torch and libtq2, which _decode needs
+from . import _decode             # isort: skip
 
 EXPORTED_SYMBOLS = ("tq2_moe_experts", "tq2_moe_experts_workspace_bytes", "tq2_moe_route",
                     "tq2_moe_route_workspace_bytes")
@@ -61,7 +61,7 @@ def route(x, weight, top_k, bias=None, scoring="softmax", renormalize=True, scal
     or bfloat16, each its own; ``weights`` and ``ids`` are made if absent."""
     if scoring not in SCORING:
         raise ValueError("scoring must be one of %s" % (SCORING,))
-    return _result(_binding.moe_route(x, weight, top_k, bias, SCORING.index(scoring), bool(renormalize), scale, weights,
+    return _result(_decode.moe_route(x, weight, top_k, bias, SCORING.index(scoring), bool(renormalize), scale, weights,
                                       ids), "moe.route")
 
 
@@ -74,4 +74,4 @@ def experts(x, gate_up, down, ids, weights, experts=None, residual=None, out=Non
     residual itself.  ``experts`` is needed for ternary weights, whose tensors do not tell how many there are."""
     g, gs = gate_up if isinstance(gate_up, (tuple, list)) else (gate_up, None)
     d, ds = down if isinstance(down, (tuple, list)) else (down, None)
-    return _result(_binding.moe_experts(x, g, gs, d, ds, ids, weights, experts, residual, out), "moe.experts")
+    return _result(_decode.moe_experts(x, g, gs, d, ds, ids, weights, experts, residual, out), "moe.experts")

@@ -1,6 +1,6 @@
 """Python binding of the token choice (include/tq2_sample.h).
 
-Argument marshalling only, as in ``tq2``: tensors go through the compiled module ``_binding`` (csrc/tq2_binding.cpp), raw
+Argument marshalling only, as in ``tq2``: tensors go through the compiled module ``_decode`` (csrc/tq2_decode.cpp), raw
 pointers through ctypes.
 """
 
@@ -9,8 +9,8 @@ from __future__ import annotations
 import ctypes
 import struct
 
-from .tq2 import _result, lib     # first: it loads torch and libtq2, which _binding needs
-from . import _binding            # isort: skip
+from .tq2 import _result, lib     # first: it loads torch and libtq2, which _decode needs
+from . import _decode             # isort: skip
 
 EXPORTED_SYMBOLS = ("tq2_sample", "tq2_sample_workspace_bytes")
 MAX_ROWS, MAX_VOCAB = 4096, 1 << 20
@@ -42,4 +42,4 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, 
     device tensor of one for each row (top_k int32, the others f32); temperature 0 takes the largest logit.  ``logprob``
     f32 [rows], if given, gets the token's log probability among those kept.  A row without a logit above -infinity
     gives -1."""
-    return _result(_binding.sample(logits, u, temperature, top_k, top_p, min_p, out, logprob), "sampling.sample")
+    return _result(_decode.sample(logits, u, temperature, top_k, top_p, min_p, out, logprob), "sampling.sample")
