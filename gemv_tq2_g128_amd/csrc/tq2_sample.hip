@@ -15,6 +15,10 @@
 // bin.  What min_p or top_k drop of a chunk alone is dropped at once.  choice_kernel: a block for each row, which joins the
 // chunks' bins at the row's largest logit and reads the tokens of the bins it needs.  Bound: logits are read from HBM
 // once, two bytes are written for each that is not dropped.
+//
+// Measured (us): one row of 32,000 f32 logits with top-k and top-p 5.6 and 12.9, one of 131,072 with top-p 8 and 14 to 26 (more for others),
+// by how many tokens share the run's last bin: chains of dependent steps, not bytes.  64 rows of 128,255 in bf16 of mixed
+// settings 20 and 34.  256 rows of 151,936 f32 logits with min-p 50 (3.1 TB/s) and 21.
 #include "tq2_device.h"
 #include "tq2_sample_internal.h"
 #include "tq2_types.h"
@@ -753,7 +757,7 @@ __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
 }
 
 // Chunks of 1, 2 or 4 vectors a thread: small ones for the number of blocks, but at most 16, which the choice joins
-// (131,072 logits: 33 us with 32 chunks of one vector, 28 with 16 of two), and large ones once there are blocks enough.
+// (131,072 logits, both kernels: 33 us with 32 chunks of one vector, 28 with 16 of two), and large ones once there are blocks enough.
 struct Chunks {
   int vecs, count, tokens;                 // vectors of a thread, chunks of a row, places of a chunk's order
 };
