@@ -20,6 +20,7 @@
 // by how many tokens share the run's last bin: chains of dependent steps, not bytes.  64 rows of 128,255 in bf16 of mixed
 // settings 20 and 34.  256 rows of 151,936 f32 logits with min-p 50 (3.1 TB/s) and 21.
 #include "tq2_device.h"
+#include "tq2_sample_bins.h"
 #include "tq2_sample_internal.h"
 #include "tq2_types.h"
 
@@ -30,8 +31,6 @@ namespace {
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kBins = 512;
-constexpr float kGrid = 11.f;              // bins of a factor of two: 2^46.5 over all, more than a weight's 43 bits
 constexpr int kMaxChunks = 64;
 constexpr int kThreads = 1024;             // of bins_kernel
 constexpr int kRowThreads = kBins;         // of the choice: a thread for each bin
@@ -122,26 +121,20 @@ struct Row {
 };
 
 // A row's settings, and what becomes of a logit; `top` is the largest logit that weights are counted from.
-struct Rule {
+struct Rule : Bins {
   double rate;                             // log2(e) / T
-  float grid;                              // bins of the logits' unit
-  float top, base;
+  float top;
   bool greedy;
 
   __device__ Rule(const Args& a, int row) {
     const double heat = a.temperatures ? double(a.temperatures[row]) : a.temperature;
     greedy = !(heat > 0.0);                // the first of the order, at any temperature
     rate = 1.4426950408889634 / (greedy ? 1.0 : fmax(heat, kCoolest));
-    grid = fmaxf(kGrid * float(rate), 0x1p-126f);       // at an infinite temperature too
+    set_rate(rate);
   }
   __device__ void set_top(float l) {
     top = l;
-    base = floorf(l * grid);
-  }
-  // Bins from the top's; NaN and what is too far give kBins.
-  __device__ int bin(float l) const {
-    const float b = floorf(l * grid), d = b == base ? 0.f : base - b;
-    return d < float(kBins) ? int(d) : kBins;
+    Bins::set_top(l);
   }
   __device__ double power(float l) const { return l == top ? 0.0 : (double(l) - double(top)) * rate; }
   // 2^y, y <= 0: f = y - n, |f| <= 1/2, by the Taylor polynomial of degree 11, which leaves 6.3e-15 of it.
@@ -222,11 +215,6 @@ __device__ __forceinline__ void scan(A& sum, uint32_t& count, A* part_sum, uint3
     if (w < wave) sum += part_sum[w], count += part_count[w];
 }
 
-// The last bin that min_p leaves anything of, for a largest logit that is the row's or below it, with one to spare.
-__device__ __forceinline__ int last_bin(double min_p) {
-  return min_p > 0.0 ? min(kBins - 1, 2 - int(floor(log2(fmin(min_p, 1.0)) * double(kGrid)))) : kBins - 1;
-}
-
 // Tokens of a chunk: those of its vectors, and for the first and the last one the row's loose ones.
 template <class T, int VECS>
 constexpr int kChunkTokens = kThreads * VECS * Bits<T>::kVec + 16;
@@ -287,10 +275,7 @@ __global__ __launch_bounds__(kThreads) void bins_kernel(Args a) {
     __syncthreads();
     cut = last;
   }
-  // A sieve by one bound, a little below the last bin's: (base - bin) / grid is off by a few 2^-24 of itself,
-  // or by half of the least subnormal.
-  const float edge = (rule.base - float(cut)) / rule.grid;
-  const float from = fabsf(edge) < 3e38f ? edge - fabsf(edge) * 0x1p-20f - 0x1p-146f : -__builtin_inff();
+  const float from = rule.sieve(cut);                   // one comparison for most tokens
   const auto place = [&](float l) {
     const int b = rule.bin(l);
     return b <= cut && l > -__builtin_inff() ? uint32_t(b) << 16 | atomicAdd(&counts[b], 1u) : kDropped;
@@ -684,11 +669,14 @@ __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
   const size_t first_chunk = size_t(index) * a.chunks;
   const float chunk_top = a.tops[first_chunk + min(lane, a.chunks - 1)];
   const float top = wave_max(chunk_top);
-  if (top == -__builtin_inff()) {
+  const auto none = [&]() {
     if (t == 0) {
       a.ids[index] = -1;
       if (a.logprob) a.logprob[index] = -__builtin_inff();
     }
+  };
+  if (top == -__builtin_inff()) {
+    none();
     return;
   }
   rule.set_top(top);
@@ -718,6 +706,11 @@ __global__ __launch_bounds__(kRowThreads) void choice_kernel(Args a) {
   __syncthreads();
   uint64_t kept = s.before;                             // the sum and the count of what is kept so far
   uint32_t left = s.count;
+  // The top weighs 2^kUnit.  Were it missing, no bin would hold what is looked for: a search needs a sum above zero.
+  if (kept == 0) {
+    none();
+    return;
+  }
   const Row<T> row(a, index);
   Choice<T> pick{s, a, rule, row, index, own, sum, mine, count};
   if (!rule.greedy && min_p > 0.0) {

@@ -1,0 +1,48 @@
+// Bins of a row's logits: plain arithmetic, shared by the kernels of the token choice and
+// (compiled for the host) their CPU test.
+#pragma once
+
+#include <math.h>
+#include <stdint.h>
+
+#ifdef __HIP__
+#define TQ2_HD __host__ __device__ __forceinline__
+#else
+#define TQ2_HD inline
+#endif
+
+namespace tq2 {
+
+constexpr int kBins = 512;
+constexpr float kGrid = 11.f;              // bins of a factor of two: 2^46.5 over all, more than a weight's 43 bits
+
+// A logit's bin is floor(l * grid) below the top's; the grid is absolute, so that chunks of a row agree on it.
+struct Bins {
+  float grid;                              // bins of the logits' unit
+  float base;                              // the top's, on the grid
+
+  // rate: log2(e) / T.
+  TQ2_HD void set_rate(double rate) { grid = fmaxf(kGrid * float(rate), 0x1p-126f); }       // at an infinite T too
+  TQ2_HD void set_top(float l) { base = floorf(l * grid); }
+  // Bins from the top's; NaN and what is too far give kBins.
+  TQ2_HD int bin(float l) const {
+    const float b = floorf(l * grid), d = b == base ? 0.f : base - b;
+    return d < float(kBins) ? int(d) : kBins;
+  }
+  // A bound that no logit of bins 0 .. cut lies below.  edge is off by a few 2^-24 of itself, or by half of the least
+  // subnormal.  l * grid rounds to whole least subnormals as well, half of which are 2^-150 / grid in l: at high
+  // temperatures negative logits lie far below 0 and still share its bin.
+  TQ2_HD float sieve(int cut) const {
+    const float edge = (base - float(cut)) / grid;
+    return fabsf(edge) < 3e38f ? edge - fabsf(edge) * 0x1p-20f - fmaxf(0x1p-146f, 0x1p-147f / grid) : -INFINITY;
+  }
+};
+
+// The last bin that min_p leaves anything of, for a largest logit that is the row's or below it, with one to spare.
+TQ2_HD int last_bin(double min_p) {
+  if (!(min_p > 0.0)) return kBins - 1;
+  const int last = 2 - int(floor(log2(fmin(min_p, 1.0)) * double(kGrid)));
+  return last < kBins - 1 ? last : kBins - 1;
+}
+
+}  // namespace tq2
