@@ -276,8 +276,7 @@ __global__ __launch_bounds__(kThreads) void bins_kernel(Args a) {
     cut = last;
   }
   const float from = rule.sieve(cut);                   // one comparison for most tokens
-  const auto place = [&](float l) {
-    const int b = rule.bin(l);
+  const auto place = [&](float l, int b) {
     return b <= cut && l > -__builtin_inff() ? uint32_t(b) << 16 | atomicAdd(&counts[b], 1u) : kDropped;
   };
   uint32_t code[VECS][kVec];
@@ -290,10 +289,15 @@ __global__ __launch_bounds__(kThreads) void bins_kernel(Args a) {
       any |= Bits<T>::get(x[i], j) >= from;
     }
     if (!__any(any)) continue;
+    if (rule.far) {
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) code[i][j] = place(Bits<T>::get(x[i], j));
+      for (int j = 0; j < kVec; ++j) code[i][j] = place(Bits<T>::get(x[i], j), rule.far_bin(Bits<T>::get(x[i], j)));
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) code[i][j] = place(Bits<T>::get(x[i], j), rule.near_bin(Bits<T>::get(x[i], j)));
+    }
   }
-  const uint32_t code_single = loose >= 0 ? place(single) : kDropped;
+  const uint32_t code_single = loose >= 0 ? place(single, rule.bin(single)) : kDropped;
   if (t == 0) last = cut;
   __syncthreads();
   const uint32_t own = t < kBins ? counts[t] : 0;

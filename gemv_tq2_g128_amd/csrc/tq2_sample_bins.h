@@ -16,24 +16,45 @@ namespace tq2 {
 constexpr int kBins = 512;
 constexpr float kGrid = 11.f;              // bins of a factor of two: 2^46.5 over all, more than a weight's 43 bits
 
-// A logit's bin is floor(l * grid) below the top's; the grid is absolute, so that chunks of a row agree on it.
+// Places on the grid below this are f32, which has quarters there; larger ones are f64, where l * grid is exact.
+constexpr float kNear = 0x1p22f;
+
+// A logit's place is floor(l * grid), its bin how far that lies below the top's place; the grid is absolute, so that chunks
+// of a row agree on it.  Logits around a top far from zero, or at low temperatures, have large places: f32 would move a
+// bin by the step of its numbers, and so past what min_p keeps or past the last bin.
 struct Bins {
   float grid;                              // bins of the logits' unit
-  float base;                              // the top's, on the grid
+  bool far;                                // from the top's place on logits of the bins may lie past kNear
+  float base;                              // the top's place
+  double far_base;
 
   // rate: log2(e) / T.
   TQ2_HD void set_rate(double rate) { grid = fmaxf(kGrid * float(rate), 0x1p-126f); }       // at an infinite T too
-  TQ2_HD void set_top(float l) { base = floorf(l * grid); }
+  // Rises with l: f32 rounds no product to a whole number that the other side of kNear passes.
+  TQ2_HD double place(float l) const {
+    const float p = l * grid;
+    return fabsf(p) < kNear ? double(floorf(p)) : floor(double(l) * double(grid));
+  }
+  TQ2_HD void set_top(float l) {
+    base = floorf(l * grid);
+    far = !(fabsf(base) < kNear - 2 * kBins);
+    far_base = place(l);
+  }
   // Bins from the top's; NaN and what is too far give kBins.
-  TQ2_HD int bin(float l) const {
-    const float b = floorf(l * grid), d = b == base ? 0.f : base - b;
+  TQ2_HD int near_bin(float l) const {
+    const float d = base - floorf(l * grid);
     return d < float(kBins) ? int(d) : kBins;
   }
+  TQ2_HD int far_bin(float l) const {
+    const double p = place(l), d = p == far_base ? 0.0 : far_base - p;      // +infinity is one place
+    return d < double(kBins) ? int(d) : kBins;
+  }
+  TQ2_HD int bin(float l) const { return far ? far_bin(l) : near_bin(l); }
   // A bound that no logit of bins 0 .. cut lies below.  edge is off by a few 2^-24 of itself, or by half of the least
   // subnormal.  l * grid rounds to whole least subnormals as well, half of which are 2^-150 / grid in l: at high
   // temperatures negative logits lie far below 0 and still share its bin.
   TQ2_HD float sieve(int cut) const {
-    const float edge = (base - float(cut)) / grid;
+    const float edge = far ? float((far_base - cut) / double(grid)) : (base - float(cut)) / grid;
     return fabsf(edge) < 3e38f ? edge - fabsf(edge) * 0x1p-20f - fmaxf(0x1p-146f, 0x1p-147f / grid) : -INFINITY;
   }
 };

@@ -82,3 +82,36 @@ def test_what_lies_above_the_top_or_is_no_number(host):
     for temperature in TEMPERATURES:
         for top in (INF, 3.0, -1e-20, -3e38):
             assert bins(host, temperature, top, [np.nan, top]).tolist() == [512, 0]
+    assert bins(host, 1.0, INF, [3e38, 0.0]).tolist() == [512, 512]
+
+
+@pytest.mark.parametrize("temperature", [t for t in TEMPERATURES if t < 1e38])
+def test_bins_are_as_far_as_the_logits(host, temperature):
+    """11 bins for each factor of two in e: the distance, rounded down at both ends to whole bins and, near, to eighths.  The
+    grid is rounded twice to 24 bits, less than 2^-12 over 512 bins."""
+    rng = np.random.default_rng(2)
+    for top in TOPS:
+        logits = below(top, rng)
+        at = bins(host, temperature, top, logits)
+        far = (np.float64(np.float32(top)) - logits.astype(np.float64)) * 11 * 1.4426950408889634 / temperature
+        off = np.abs(at - far)[far < 510]
+        assert off.max() < 1.25 + 2.0 ** -12, (top, off.max())
+        assert (at[far < 510] < 512).all() and (at[far > 514] == 512).all()
+
+
+@pytest.mark.parametrize("temperature", TEMPERATURES)
+def test_chunks_agree_on_their_bins(host, temperature):
+    """A logit's bin below a row's top is its chunk's top's and its own below that, on whichever side of the border between
+    f32 and f64 each top lies."""
+    rng = np.random.default_rng(3)
+    border = 2.0 ** 22 * temperature / (11 * 1.4426950408889634)
+    tops = TOPS + [s * border * (1 + d) for s in (1, -1) for d in (-1025 / 2 ** 22, -1023 / 2 ** 22, -1e-5, -1e-7, 1e-7, 1e-4)
+                   if border < 3e38]
+    for top in tops:
+        logits = below(top, rng)
+        row = bins(host, temperature, top, logits)
+        logits, row = logits[row < 512], row[row < 512]
+        for i in rng.integers(0, len(logits), 12):
+            mine = logits <= logits[i]
+            chunk = bins(host, temperature, logits[i], logits[mine])
+            assert (row[i] + chunk == row[mine]).all(), (top, logits[i])
