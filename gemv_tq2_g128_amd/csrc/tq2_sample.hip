@@ -260,7 +260,7 @@ __global__ __launch_bounds__(kThreads) void bins_kernel(Args a) {
   rule.set_top(top);
   // Each token's bin and its number there.  What min_p drops of a chunk by itself is no part of the row's either.
   constexpr uint32_t kDropped = ~0u;
-  int cut = last_bin(min_p);
+  int cut = rule.last_bin(min_p, rule.rate);
   if (top_k > 0 && top_k <= kThreads / 2) {
     // Nor is what lies below top_k threads' own largest tokens: a first cut by these, one a thread.
     const int b = rule.bin(mine);

@@ -57,13 +57,13 @@ struct Bins {
     const float edge = far ? float((far_base - cut) / double(grid)) : (base - float(cut)) / grid;
     return fabsf(edge) < 3e38f ? edge - fabsf(edge) * 0x1p-20f - fmaxf(0x1p-146f, 0x1p-147f / grid) : -INFINITY;
   }
+  // The last bin that min_p leaves anything of, for a largest logit that is the row's or below it, with one to spare.  Past
+  // T = 1e39 the grid is finer than 11 bins for a factor of two, and e of logits far apart is 1 up to its own rounding.
+  TQ2_HD int last_bin(double min_p, double rate) const {
+    if (!(min_p > 0.0)) return kBins - 1;
+    const double bins = (0x1p-40 - log2(fmin(min_p, 1.0))) * (double(grid) / rate);
+    return bins < double(kBins - 3) ? 2 + int(ceil(bins)) : kBins - 1;
+  }
 };
-
-// The last bin that min_p leaves anything of, for a largest logit that is the row's or below it, with one to spare.
-TQ2_HD int last_bin(double min_p) {
-  if (!(min_p > 0.0)) return kBins - 1;
-  const int last = 2 - int(floor(log2(fmin(min_p, 1.0)) * double(kGrid)));
-  return last < kBins - 1 ? last : kBins - 1;
-}
 
 }  // namespace tq2

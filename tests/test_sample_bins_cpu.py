@@ -22,6 +22,12 @@ extern "C" float sieve(double temperature, float top, int cut) {
   b.set_top(top);
   return b.sieve(cut);
 }
+extern "C" int last_bin(double temperature, double min_p) {
+  tq2::Bins b;
+  const double rate = 1.4426950408889634 / temperature;
+  b.set_rate(rate);
+  return b.last_bin(min_p, rate);
+}
 """
 INF = float("inf")
 
@@ -115,3 +121,19 @@ def test_chunks_agree_on_their_bins(host, temperature):
             mine = logits <= logits[i]
             chunk = bins(host, temperature, logits[i], logits[mine])
             assert (row[i] + chunk == row[mine]).all(), (top, logits[i])
+
+
+@pytest.mark.parametrize("temperature", TEMPERATURES)
+def test_min_p_keeps_its_bins(host, temperature):
+    rng = np.random.default_rng(4)
+    for top in TOPS:
+        logits = below(top, rng)
+        logits = logits[np.isfinite(logits)]
+        at = bins(host, temperature, top, logits)
+        e = np.exp2((logits.astype(np.float64) - np.float64(logits[0])) * (1.4426950408889634 / temperature))
+        for least in (1.0, 0.999, 0.9, 0.5, 0.02, 1e-6, 1e-12, 1e-14):
+            last = host.last_bin(ctypes.c_double(temperature), ctypes.c_double(least))
+            lost = logits[(e >= least) & (at > last)]
+            assert len(lost) == 0 or (least < 1e-13 and (at[(e >= least) & (at > last)] == 512).all()), (top, least, lost[:3])
+    assert host.last_bin(ctypes.c_double(temperature), ctypes.c_double(0.0)) == 511
+    assert host.last_bin(ctypes.c_double(0.7), ctypes.c_double(0.5)) in (2 + 11, 2 + 12)

@@ -71,3 +71,16 @@ def test_a_row_whose_chunks_lie_on_both_sides_of_the_border(sampling):  # noqa: 
     for settings in (dict(), dict(top_k=300), dict(top_p=0.7), dict(min_p=0.01), dict(temperature=2.0), dict(temperature=0.5)):
         check(sampling, logits, u, **settings)
         check(sampling, logits.flip(1), u, **settings)
+
+
+@pytest.mark.parametrize("temperature", [1e40, 1e300, INF])
+@pytest.mark.parametrize("least", [1.0, 0.9, 0.5])
+def test_min_p_at_temperatures_past_f32(sampling, temperature, least):  # noqa: F811
+    # e is 1 wherever the logits lie (at 1e40 within 1.7e-2 of it), over several bins.
+    g = torch.Generator().manual_seed(5)
+    logits = (torch.rand(3, 9000, generator=g) * 2 - 1) * 3.3e38
+    logits[1, 8000] = 3.4e38
+    logits[2, 3::7] = -INF
+    u = torch.tensor([0.31, 0.62, 0.93])
+    check(sampling, logits, u, temperature=temperature, min_p=least)
+    check(sampling, logits, u, temperature=temperature, min_p=least, top_k=4000)
