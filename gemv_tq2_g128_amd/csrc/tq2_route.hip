@@ -197,6 +197,7 @@ __global__ __launch_bounds__(64 * kChoiceWaves) void choice_kernel(const double*
     key[i] = e < experts ? key_of(p[i]) : 0;
   }
   double sum = 0.0;                                       // of the softmax, over all experts
+  bool nan = false;
   if (sigmoid) {
 #pragma unroll
     for (int i = 0; i < NE; ++i) p[i] = 1.0 / (1.0 + exp(-p[i]));
@@ -213,6 +214,18 @@ __global__ __launch_bounds__(64 * kChoiceWaves) void choice_kernel(const double*
     }
 #pragma unroll
     for (int m = 32; m; m >>= 1) sum += shuffle_xor(sum, m);
+    nan = sum != sum;
+    if (nan && bias) {
+      // The choice goes on without the NaN scores: equals of an infinite top share the softmax.
+      sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        if (p[i] != p[i] && key[i] > 1) p[i] = 1.0;       // infinity less itself
+        if (p[i] == p[i]) sum += p[i];
+      }
+#pragma unroll
+      for (int m = 32; m; m >>= 1) sum += shuffle_xor(sum, m);
+    }
 #pragma unroll
     for (int i = 0; i < NE; ++i) p[i] /= sum;
   }
@@ -254,6 +267,7 @@ __global__ __launch_bounds__(64 * kChoiceWaves) void choice_kernel(const double*
   }
   if (lane < top_k) {
     if (renormalize) mine /= total;
+    if (nan) mine = __builtin_nan("");
     weights[size_t(t) * top_k + lane] = float(mine * scale);
     ids[size_t(t) * top_k + lane] = id;
   }

@@ -63,8 +63,11 @@ size_t tq2_moe_route_workspace_bytes(const tq2_moe_route_args* args);
  * p, by `renormalize` and `scale`.
  * Accuracy: products and sums in 64 bits, so that only scores closer than
  * about 1e-14 of sum |x w| change places; weights are rounded once to f32.
- * Scores that are NaN come after all others; a token with one has NaN weights
- * where they enter its sum.
+ * Scores that are NaN come after all others, with a bias too, for which the
+ * softmax is then that of the others (those at +infinity share it; where all
+ * are -infinity, these do).  The weights of a token with a NaN score are NaN
+ * where it enters their sum, and its softmax weights where the largest score is
+ * infinite.
  * x, weight and workspace: 16-byte aligned; the others 4-byte aligned.
  * tokens == 0 is a no-op.  Errors: INVALID (null pointer, size or type out of
  * range, a scale that is not finite, a workspace that is too small), SHAPE
