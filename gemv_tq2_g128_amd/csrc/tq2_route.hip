@@ -265,6 +265,22 @@ __global__ __launch_bounds__(64 * kChoiceWaves) void choice_kernel(const double*
     total += chosen;
     if (lane == j) mine = chosen, id = at;
   }
+  if (renormalize && total < 0x1p-800) {
+    // Probabilities near or past f64's least number, of which the sum knows too little or nothing: their ratios are those
+    // of exp(score), for the sigmoid too, whose 1 + exp(score) is 1 here.
+    double score = low;
+    if (lane < top_k) {
+      score = 0.0;
+      for (int s = 0; s < parts; ++s) score += scores[(size_t(s) * tokens + t) * experts + id];
+    }
+    double most = score;
+#pragma unroll
+    for (int m = 32; m; m >>= 1) most = fmax(most, shuffle_xor(most, m));
+    mine = lane >= top_k ? 0.0 : score == most ? 1.0 : exp(score - most);
+    total = mine;
+#pragma unroll
+    for (int m = 32; m; m >>= 1) total += shuffle_xor(total, m);
+  }
   if (lane < top_k) {
     if (renormalize) mine /= total;
     if (nan) mine = __builtin_nan("");

@@ -67,7 +67,9 @@ size_t tq2_moe_route_workspace_bytes(const tq2_moe_route_args* args);
  * softmax is then that of the others (those at +infinity share it; where all
  * are -infinity, these do).  The weights of a token with a NaN score are NaN
  * where it enters their sum, and its softmax weights where the largest score is
- * infinite.
+ * infinite.  Where all chosen probabilities lie near or below the least f64
+ * number their shares, which `renormalize` gives, are those of exp(score), equal
+ * ones where all chosen scores are -infinity.
  * x, weight and workspace: 16-byte aligned; the others 4-byte aligned.
  * tokens == 0 is a no-op.  Errors: INVALID (null pointer, size or type out of
  * range, a scale that is not finite, a workspace that is too small), SHAPE

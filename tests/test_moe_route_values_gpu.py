@@ -91,3 +91,44 @@ def test_infinite_scores_with_a_bias(moe, tokens):
         weights, ids = run(moe, tokens, s, 6, given, scoring="sigmoid", renormalize=False)
         at = order((s == INF) * 1.0 + given.double().numpy())[:6]
         assert ids.tolist() == at.tolist() and np.array_equal(weights, (s[at] == INF) * 1.0)
+
+
+def shares(scores, at):
+    """exp(score) of the chosen by their sum, in extended precision."""
+    e = np.exp(scores[at].astype(np.longdouble) - scores[at].astype(np.longdouble).max())
+    return (e / e.sum()).astype(np.float64)
+
+
+@pytest.mark.parametrize("tokens", [1, 20])
+@pytest.mark.parametrize("experts", [40, 300])
+@pytest.mark.parametrize("low", [-560.0, -700.0, -720.0, -745.0, -900.0, -30000.0, -3e38])
+def test_shares_of_probabilities_below_the_least_number(moe, tokens, experts, low):
+    rng = np.random.default_rng(2)
+    scores = (low + rng.uniform(-3, 0, experts)).astype(np.float32)
+    weights, ids = run(moe, tokens, scores, 8, scoring="sigmoid", scale=2.5)
+    at = order(scores.astype(np.float64))[:8]
+    assert ids.tolist() == at.tolist()
+    assert np.abs(weights / (2.5 * shares(scores, at)) - 1).max() <= TOL
+    # Softmax: one expert has it all, and a bias brings others forward.
+    scores[11] = 0.0
+    bias = torch.zeros(experts)
+    bias[11] = -2.0
+    bias[20:26] = 1.0
+    weights, ids = run(moe, tokens, scores, 6, bias)
+    at = np.arange(20, 26)
+    assert sorted(ids.tolist()) == at.tolist()
+    assert np.abs(weights / shares(scores, ids) - 1).max() <= TOL
+    # With it among them there is a sum, and the others' shares are zero in f32.
+    weights, ids = run(moe, tokens, scores, 7, bias * 0)
+    assert ids[0] == 11 and weights.tolist() == [1.0] + [0.0] * 6
+
+
+def test_shares_of_scores_at_minus_infinity(moe):
+    scores = np.full(20, -INF, dtype=np.float32)
+    weights, ids = run(moe, 3, scores, 4, scoring="sigmoid")
+    assert ids.tolist() == [0, 1, 2, 3] and weights.tolist() == [0.25] * 4
+    scores[[5, 9]] = -800.0
+    weights, ids = run(moe, 3, scores, 4, scoring="sigmoid")
+    assert ids.tolist() == [5, 9, 0, 1] and weights.tolist() == [0.5, 0.5, 0.0, 0.0]
+    weights, ids = run(moe, 3, scores, 4, scoring="sigmoid", renormalize=False)
+    assert weights.tolist() == [0.0] * 4
