@@ -156,13 +156,18 @@ __device__ __forceinline__ void load_codes(const Rows& rows, uint32_t row_bytes,
     c.d[kWords - 1] = __builtin_amdgcn_raw_buffer_load_b32(rows.scales, at + (kWords - 1) * 4, 0, 0);
 }
 
-// The scale of 32-wide step s of block b.
+// The power of two that undoes a row's is split, so that both parts and what they meet stay normal numbers of f32 for all
+// rows: 2^-kInScale goes with the scales (in the step that converts them, at no cost), the rest with the row.
+constexpr int kInScale = 24;
+constexpr int kMostUp = 126 + kInScale;
+
+// The scale of 32-wide step s of block b, times 2^-kInScale.
 template <class F, int N>
 __device__ __forceinline__ float scale_of(const Codes<F, N>& c, int b, int s) {
   const int i = b * (128 / F::kGroup) + s / (F::kGroup / 32);
   uint32_t w = c.d[i >> 1];
   if constexpr (F::kGroup == 128) w = __builtin_amdgcn_alignbit(c.d[(i >> 1) + 1], w, c.down);
-  return float(__builtin_bit_cast(_Float16, uint16_t(w >> (16 * (i & 1)))));
+  return __builtin_fmaf(float(__builtin_bit_cast(_Float16, uint16_t(w >> (16 * (i & 1))))), 0x1p-24f, 0.f);
 }
 
 // Lane groups exchange words so that each step stays inside one scale's columns.
@@ -186,7 +191,7 @@ __device__ __forceinline__ void arrange(u32x4_t& w) {
 // x of up to kMaxRows rows in LDS:
 //   operands  [block][step][lane group][columns_of(m)] of 16 bytes (steps of 32: 8), column 4 row + byte
 //   starts    [block][group][row] of 4 integers: minus kMiddle times the sums of the row's bytes
-//   backs     [block][row]: the power of two that undoes the row's
+//   backs     [block][row]: the power of two that undoes the row's, but for what the scales have of it
 // An odd number of columns keeps the lanes that write a stretch of x off each other's banks.
 __host__ __device__ inline int columns_of(int m) { return m > 1 ? 4 * m + 1 : 4; }
 template <class F>
@@ -224,7 +229,8 @@ __device__ __forceinline__ u32x4_t by_byte(uint32_t a, uint32_t b, uint32_t c, u
 }
 
 // Convert eight columns (the u-th eight, as place_of says) of 128-wide block kb of row `row` of m into LDS.  The sixteen
-// lanes of a block call together: their power of two is a DPP maximum, 2^29 <= |x| 2^e < 2^30.  `share` multiplies the row.
+// lanes of a block call together: their power of two is a DPP maximum, 2^29 <= |x| 2^e < 2^30, at most kMostUp, by which
+// every f32 number is whole.  `share` multiplies the row.
 template <class F, class X>
 __device__ __forceinline__ void stage8(const typename X::elem* __restrict__ block, int u, int kb, int row, int m,
                                        int cols, float share, const Rows31& r) {
@@ -238,11 +244,11 @@ __device__ __forceinline__ void stage8(const typename X::elem* __restrict__ bloc
   top = max(top, move<0x4E>(top));
   top = max(top, move<0x141>(top));
   top = max(top, move<0x140>(top));
-  const int up = top > 0 ? min(29 + 127 - (top >> 23), 126) : 0;
-  const float s = __builtin_ldexpf(1.0f, up);
+  const int up = top > 0 ? min(29 + 127 - (top >> 23), kMostUp) : 0;
   uint32_t b[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) b[j] = (uint32_t(int(__builtin_rintf(v[j] * s))) + 0x00808080u) ^ 0x00808080u;   // signed bytes
+  for (int j = 0; j < 8; ++j)
+    b[j] = (uint32_t(int(__builtin_rintf(__builtin_ldexpf(v[j], up)))) + 0x00808080u) ^ 0x00808080u;   // signed bytes
   // The order of the codes' bytes: nibbles of a word, or 2-bit fields of bytes.
   const u32x4_t first = F::kBlocks == 2 ? by_byte(b[0], b[4], b[1], b[5]) : by_byte(b[0], b[2], b[4], b[6]);
   const u32x4_t second = F::kBlocks == 2 ? by_byte(b[2], b[6], b[3], b[7]) : by_byte(b[1], b[3], b[5], b[7]);
@@ -265,7 +271,7 @@ __device__ __forceinline__ void stage8(const typename X::elem* __restrict__ bloc
   constexpr int kLanes = F::kGroup / 8;
   if (u % kLanes == 0) r.starts[(kb * kGroups<F> + u / kLanes) * m + row] = sum;
   if (u == 0)
-    r.backs[kb * m + row] = top >= 0x7F800000 ? __builtin_nanf("") : __builtin_ldexpf(1.0f, -up) * share;
+    r.backs[kb * m + row] = top >= 0x7F800000 ? __builtin_nanf("") : __builtin_ldexpf(1.0f, kInScale - up) * share;
 }
 
 // Bytes from a step's operands to lane group g4's of a column.

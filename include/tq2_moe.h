@@ -116,7 +116,10 @@ size_t tq2_moe_experts_workspace_bytes(const tq2_moe_experts_args* args);
  * sums over a scale's columns exact, f32 beyond: each projection is within
  * 1e-5 * sum_k |x w| + 2^-30 * sum_k X_k |w|, with X_k the largest |x| of k's 128
  * columns (128 j .. 128 j + 127); the second term counts where a column far
- * above the others meets weights of almost zero.  The output is rounded once
+ * above the others meets weights of almost zero.  What f32 loses below its
+ * normal numbers comes on top, 2^-140 * (1 + sum |w|) at most.  A row between the
+ * projections and its product with its weight have to stay below 2^127: past
+ * that the output may be infinite or NaN.  The output is rounded once
  * to its type.  The order of all sums is fixed: a call repeats its results.
  * Only rows of x whose token chose an expert meet that expert's weights: a row
  * that is not finite reaches its own output alone.
