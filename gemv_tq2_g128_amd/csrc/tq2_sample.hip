@@ -260,7 +260,7 @@ __global__ __launch_bounds__(kThreads) void bins_kernel(Args a) {
   rule.set_top(top);
   // Each token's bin and its number there.  What min_p drops of a chunk by itself is no part of the row's either.
   constexpr uint32_t kDropped = ~0u;
-  int cut = rule.last_bin(min_p, rule.rate);
+  int cut = rule.last_bin(min_p);
   if (top_k > 0 && top_k <= kThreads / 2) {
     // Nor is what lies below top_k threads' own largest tokens: a first cut by these, one a thread.
     const int b = rule.bin(mine);
@@ -513,14 +513,11 @@ struct Choice {
     }
     __syncthreads();
   }
-  // f(key, weight) for the opened bin's tokens.
+  // f(key, weight) for the tokens at hand.
   template <class F>
-  __device__ void each(int bin, F f) {
+  __device__ void each(F f) {
     if (listed) {
-      for (uint32_t i = threadIdx.x; i < tokens; i += kRowThreads) {
-        const uint64_t k = s.list[i];
-        if (rule.bin(logit_of(uint32_t(k >> 32))) == bin) f(k, s.weights[i]);
-      }
+      for (uint32_t i = threadIdx.x; i < tokens; i += kRowThreads) f(s.list[i], s.weights[i]);
     } else {
       read([&](uint32_t, uint64_t k) { f(k, weight_of(k)); });       // the bin by itself
     }
@@ -542,8 +539,9 @@ struct Choice {
     open(bin);
     uint64_t part = 0;
     uint32_t n = 0;
-    each(bin, [&](uint64_t k, uint64_t w) {
-      if (uint32_t(k >> 32) >= border) part += w, ++n;
+    each([&](uint64_t k, uint64_t w) {
+      const uint32_t l = uint32_t(k >> 32);
+      if (l >= border && (low == high || rule.bin(logit_of(l)) == bin)) part += w, ++n;
     });
     total(part, n);
     if (t == bin) {
@@ -580,6 +578,7 @@ struct Choice {
       *through = got < end ? got : end;
       return s.key;
     }
+    // More than kFew: the bin by itself is at hand.
     if (g.count) g.count -= before_n;
     else g.sum -= before;
     uint64_t lo = 0, hi = ~uint64_t(0), passed = 0;
@@ -587,7 +586,7 @@ struct Choice {
     while (n > kFew) {
       // The keys' range, then bins over it.
       uint64_t least = ~uint64_t(0), most = 0;
-      each(bin, [&](uint64_t k, uint64_t) {
+      each([&](uint64_t k, uint64_t) {
         if (k < lo || k > hi) return;
         least = k < least ? k : least;
         most = k > most ? k : most;
@@ -610,7 +609,7 @@ struct Choice {
         most = s.part_b[w] > most ? s.part_b[w] : most;
       }
       const int width = 64 - __builtin_clzll((most - least) | 1), shift = width > 9 ? width - 9 : 0;
-      each(bin, [&](uint64_t k, uint64_t w) {
+      each([&](uint64_t k, uint64_t w) {
         if (k < lo || k > hi) return;
         const int b = int((most - k) >> shift);
         atomicAdd(reinterpret_cast<unsigned long long*>(&s.sums[b]), static_cast<unsigned long long>(w));
@@ -644,7 +643,7 @@ struct Choice {
     __syncthreads();
     if (t == 0) s.few = 0;
     __syncthreads();
-    each(bin, [&](uint64_t k, uint64_t w) {
+    each([&](uint64_t k, uint64_t w) {
       if (k < lo || k > hi) return;
       const uint32_t at = atomicAdd(&s.few, 1u);
       if (at < kFew) s.few_key[at] = k, s.few_sum[at] = w;

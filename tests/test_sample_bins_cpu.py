@@ -24,9 +24,8 @@ extern "C" float sieve(double temperature, float top, int cut) {
 }
 extern "C" int last_bin(double temperature, double min_p) {
   tq2::Bins b;
-  const double rate = 1.4426950408889634 / temperature;
-  b.set_rate(rate);
-  return b.last_bin(min_p, rate);
+  b.set_rate(1.4426950408889634 / temperature);
+  return b.last_bin(min_p);
 }
 """
 INF = float("inf")
