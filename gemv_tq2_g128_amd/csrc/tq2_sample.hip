@@ -632,8 +632,9 @@ struct Choice {
       }
       __syncthreads();
       hi = most - (uint64_t(s.bin) << shift);
-      lo = hi - ((uint64_t(1) << shift) - 1);
-      if (lo > hi) lo = 0;                               // below zero: the last bin may reach past the least key
+      // The last bin may reach past the least key: no lower than before, where other tokens follow.
+      const uint64_t below = (uint64_t(1) << shift) - 1;
+      if (hi - lo > below) lo = hi - below;
       n = s.count;
       passed += s.before;
       if (g.count) g.count -= s.count_before;
