@@ -44,15 +44,15 @@ class Exact:
         self.ids = np.stack([rng.permutation(experts)[:top_k] for _ in range(tokens)]).astype(np.int32)
         self.share = rng.choice([0.5, 1.0], (tokens, top_k)).astype(np.float32)
 
-    def packed(self, w):
-        """The framework's codes and scales of 1: (codes, scales), or 34-byte blocks."""
+    def packed(self, w, unit=1.0):
+        """The framework's codes and scales, all of them `unit`: (codes, scales), or 34-byte blocks."""
         if self.fmt == "q4":
             c = (w + 8).astype(np.uint8)
-            return c[..., 0::2] | c[..., 1::2] << 4, np.ones(w.shape[:2] + (w.shape[2] // self.group,), dtype=np.float16)
+            return c[..., 0::2] | c[..., 1::2] << 4, np.full(w.shape[:2] + (w.shape[2] // self.group,), unit, dtype=np.float16)
         f = (w + 1).astype(np.uint8).reshape(-1, 32, 4)
         blocks = np.empty((len(f), 34), dtype=np.uint8)
         blocks[:, :32] = f[..., 0] | f[..., 1] << 2 | f[..., 2] << 4 | f[..., 3] << 6
-        blocks[:, 32:] = np.ones((len(f), 1), dtype=np.float16).view(np.uint8)
+        blocks[:, 32:] = np.full((len(f), 1), unit, dtype=np.float16).view(np.uint8)
         return blocks.reshape(-1)
 
     def out(self, keep=lambda row: row):

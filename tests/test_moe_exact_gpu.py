@@ -16,11 +16,11 @@ pytestmark = pytest.mark.gpu
 SCALES = {"ones": (1.0, 1.0), "tiny": (2.0 ** -70, 2.0 ** -70), "tiny up": (1.0, 2.0 ** -133), "large": (2.0 ** 40, 2.0 ** 20)}
 
 
-def on_gpu(c):
+def on_gpu(c, unit=1.0):
     from gemv_tq2_g128_amd import tq2
     if c.fmt == "q4":
-        return [tuple(torch.from_numpy(a).cuda() for a in c.packed(w)) for w in (c.up, c.down)]
-    return [tq2.reformat_aos_to_soa(torch.from_numpy(c.packed(w)).cuda(), w.shape[0] * w.shape[1], w.shape[2])
+        return [tuple(torch.from_numpy(a).cuda() for a in c.packed(w, unit)) for w in (c.up, c.down)]
+    return [tq2.reformat_aos_to_soa(torch.from_numpy(c.packed(w, unit)).cuda(), w.shape[0] * w.shape[1], w.shape[2])
             for w in (c.up, c.down)]
 
 
@@ -35,6 +35,16 @@ def test_outputs_without_rounding(moe, fmt, group, tokens, top_k, experts, inter
     want = c.out()
     assert np.array_equal(want, want.astype(np.float32))
     assert np.array_equal(y.cpu().numpy().astype(np.float64), want)
+
+
+@pytest.mark.parametrize("fmt,group", FORMATS)
+@pytest.mark.parametrize("unit", [2.0 ** -24, 2.0 ** -20, 2.0 ** 15])
+@pytest.mark.parametrize("tokens", [1, 40])
+def test_scales_at_the_ends_of_binary16(moe, fmt, group, tokens, unit):  # noqa: F811
+    c = Exact(3, tokens, 2, 4, 256, fmt, group)
+    y = moe.experts(torch.from_numpy((c.x / unit).astype(np.float32)).cuda(), *on_gpu(c, unit), torch.from_numpy(c.ids).cuda(),
+                    torch.from_numpy(c.share).cuda(), experts=4)
+    assert np.array_equal(y.cpu().numpy().astype(np.float64), c.out() * unit)
 
 
 def check(c, y, least=0.0):
