@@ -23,9 +23,9 @@
 // Measured (us a call; share of the bytes that it cannot do without at a copy's 4.97 TB/s).  Hidden 2048, inter 768, 8 of
 // 128 experts, groups of 128, one token: 7.7 for gate and up, 6.1 for down and sum (0.30: two chains of id, weights, join).
 // 4096, 11008, 2 of 8, ternary, one token: 15.4 and 11.1 (0.57).  2048, 768, 8 of 128, groups of 64, 64 tokens: 5 for the
-// items, 55, 38, 5 for the sum (83 to 90 among other calls, whose ends overlap: 0.71 to 0.77).  4096, 1408, 6 of 64, ternary, 128
-// tokens: 5, 109, 64, 5 (0.38: the same loads without the products take 107 in all, as an expert's 12 tokens are two items
-// that each read its weights; the products hide behind them in part).
+// items, 55, 28 to 38, 5 for the sum (83 to 96 among other calls, whose ends overlap: 0.66 to 0.77).  4096, 1408, 6 of 64,
+// ternary, 128 tokens: 5, 96 to 109, 57 to 64, 5 (0.38: the same loads without the products take 107 in all, as an expert's
+// 12 tokens are two items that each read its weights; the products hide behind them in part).
 #include "tq2_device.h"
 #include "tq2_internal.h"
 #include "tq2_moe_internal.h"

@@ -16,7 +16,7 @@
 // chunks' bins at the row's largest logit and reads the tokens of the bins it needs.  Bound: logits are read from HBM
 // once, two bytes are written for each that is not dropped.
 //
-// Measured (us): one row of 32,000 f32 logits with top-k and top-p 5.6 and 12.9, one of 131,072 with top-p 8 and 14 to 26 (more for others),
+// Measured (us): one row of 32,000 f32 logits with top-k and top-p 5.8 and 12.1, one of 131,072 with top-p 8 and 14 to 26 (more for others),
 // by how many tokens share the run's last bin: chains of dependent steps, not bytes.  64 rows of 128,255 in bf16 of mixed
 // settings 20 and 34.  256 rows of 151,936 f32 logits with min-p 50 (3.1 TB/s) and 21.
 #include "tq2_device.h"

@@ -67,7 +67,8 @@ def route(x, weight, top_k, bias=None, scoring="softmax", renormalize=True, scal
 
 def experts(x, gate_up, down, ids, weights, experts=None, residual=None, out=None):
     """out[t] = residual[t] + sum_j weights[t, j] * (silu(x G^T) * (x U^T)) D^T with expert ids[t, j]'s G, U and D, for
-    the at most MAX_TOKENS rows of x [tokens, hidden].
+    the at most MAX_TOKENS rows of x [tokens, hidden]; more rows go in slices, a call each, which each read their
+    experts' weights.
 
     ids int32 [tokens, top_k] and weights f32 of the same shape, as ``route`` gives them; a place whose id is no expert
     (-1, say) takes no part.  x, residual and out have one dtype of float32, float16 and bfloat16; out may be x or
